@@ -20,9 +20,10 @@ from .api import (  # noqa: F401
     sgmv_expand_partials, sgmv_expand_partials_sigma, sgmv_fused_static, plan_opts_default,
     debug_checks,
 )
+from .layer import block_norm  # noqa: F401
 
 __all__ = ["Pool", "Plan", "sgmv_shrink", "sgmv_expand", "sgmv_fused", "sgmv_expand_sigma",
            "sgmv_fused_sigma", "sgmv_shrink_partials", "sgmv_expand_partials",
            "sgmv_expand_partials_sigma", "sgmv_fused_static",
            "pool_bytes_for", "extent_bytes", "pack_adapter", "Cache", "LoraError", "load",
-           "plan_opts_default", "debug_checks"]
+           "plan_opts_default", "debug_checks", "block_norm"]

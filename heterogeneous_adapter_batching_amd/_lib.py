@@ -44,6 +44,14 @@ class PlanOpts(ctypes.Structure):
                 ("shrink_groups", ctypes.c_int32), ("prefill_groups", ctypes.c_int32)]
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("stream_dtype", ctypes.c_int32),
+                ("num_tokens", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("post", ctypes.c_int32), ("pre", ctypes.c_int32), ("gate_act", ctypes.c_int32),
+                ("unit_offset", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("beta", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 _i32, _i64, _u64, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
 _vp, _i32p = ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)
 _pp = ctypes.POINTER(ctypes.c_void_p)
@@ -109,7 +117,14 @@ SIGNATURES = {
     "lora_cache_stats": (_i32, [_vp, _i32p, ctypes.POINTER(_u64), ctypes.POINTER(_u64),
                                 ctypes.POINTER(_u64), ctypes.POINTER(_u64),
                                 ctypes.POINTER(_u64)]),
+    "block_norm": (_i32, [ctypes.POINTER(NormDesc), _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
+                          _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
 }
+
+# lora_norm_kind, lora_gate_act
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
+LORA_NORM_MAX_WIDTH = 32768
 
 LORA_SIGMA_DIAG, LORA_SIGMA_FULL = 1, 2
 

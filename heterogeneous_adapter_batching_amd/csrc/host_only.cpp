@@ -3,6 +3,7 @@
 // exercises the pool, plan, validation and exchange bookkeeping under the
 // address and undefined-behaviour sanitizers on a machine without a GPU; no
 // call that launches a kernel can succeed in it.
+#include "layer_internal.h"
 #include "sgmv_internal.h"
 
 namespace lora {
@@ -23,6 +24,9 @@ hipError_t launch_expand_decode(int, int, const ExpandArgs &, int, hipStream_t) 
     return hipErrorInvalidValue;
 }
 hipError_t launch_expand_merge(int, int, int, const MergeArgs &, int, hipStream_t) {
+    return hipErrorInvalidValue;
+}
+hipError_t launch_block_norm(int, int, const NormArgs &, hipStream_t) {
     return hipErrorInvalidValue;
 }
 hipError_t static_scratch(void **, uint64_t *) { return hipErrorInvalidValue; }

@@ -351,6 +351,15 @@ lora_status set_error(lora_status st, const char *msg) {
     g_last_error = msg;
     return st;
 }
+lora_status set_errorf(lora_status st, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return st;
+}
 }  // namespace lora
 
 // ------------------------------------------------------------------ C ABI ----

@@ -361,6 +361,8 @@ constexpr uint32_t b_vec_off(BLayout b, int o, int v, int h_out) {
 
 // Sets the thread's last-error message (lora_last_error) and returns st.
 lora_status set_error(lora_status st, const char *msg);
+// The same with a printf format.
+lora_status set_errorf(lora_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 
 // Kernel launchers (kernels.hip).  dtype is a lora_dtype; tt is the number of
 // 16-token tiles of the largest block (1, 2 or 4); ks the K-steps of the

@@ -1,0 +1,113 @@
+"""The operators around the delta over the C ABI (argument marshalling only):
+the residual stream's norms."""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+from ._lib import GATE_ACTS, LORA_BF16, LORA_F32, NORMS, NormDesc, check, load
+from .api import _stream_handle, _torch
+
+
+def _dtype_code(t, name):
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return LORA_BF16
+    if t.dtype == torch.float32:
+        return LORA_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _matrix(t, name, shape=None, dtype=None, device=None):
+    """A 2-D CUDA tensor with contiguous rows, as (pointer, row stride)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be {list(shape) if shape else '2-D'}, got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(t, name, n, dtype, device):
+    """A contiguous vector of n elements, or None: its pointer (0 for None)."""
+    if t is None:
+        return 0
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
+
+
+def _code(table, key, what):
+    if key not in table:
+        raise ValueError(f"{what} {key!r} is not one of {', '.join(map(repr, table))}")
+    return table[key]
+
+
+def _on(device):
+    """Makes `device` current for a launch, if it is not already."""
+    torch = _torch()
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def block_norm(h, o=None, *, post="none", post_weight=None, post_bias=None, gate=None,
+               gate_act="none", alpha=1.0, beta=1.0, pre="rms", pre_weight=None, pre_bias=None,
+               eps=1e-5, unit_offset=False, h_out=None, u=None, stream=None):
+    """The residual stream past a block and the next block's input, in one pass:
+
+        h_out = beta h + alpha gate_act(gate) * N_post(o),   u = N_pre(h_out)
+
+    h [T][d] is the residual stream, o [T][d] the block's output (None: there
+    is none yet).  post and pre name the norms ("none", "rms", "layer"), each
+    with an optional weight and bias [d]; gate is a vector [d] or a row per
+    token [T][d], through gate_act ("none", "sigmoid", "tanh").  bfloat16 or
+    float32, with a float32 stream beside bfloat16 blocks if h is float32.
+    u is formed from the unrounded h_out.  Returns (h_out, u), in the tensors
+    given or new ones; h_out may be h itself.  Without a block output and
+    with beta 1 the stream is unchanged: h itself is returned unless h_out is
+    given.  u is None with pre="none".  Inference only."""
+    torch = _torch()
+    hp, ldh = _matrix(h, "h")
+    T, d = h.shape
+    dev = h.device
+    like = next((t for t in (o, u, pre_weight, pre_bias) if t is not None), h)
+    desc = NormDesc(_dtype_code(like, "o"), _dtype_code(h, "h"), T, d,
+                    _code(NORMS, post, "post norm"), _code(NORMS, pre, "pre norm"),
+                    _code(GATE_ACTS, gate_act, "gate_act"), int(bool(unit_offset)), alpha, beta,
+                    eps)
+    dt = like.dtype
+    op, ldo = _matrix(o, "o", (T, d), dt, dev) if o is not None else (0, d)
+    gp, ldg = 0, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gp = _vector(gate, "gate", d, dt, dev)
+        else:
+            gp, ldg = _matrix(gate, "gate", (T, d), dt, dev)
+    vec = [_vector(t, n, d, dt, dev) for t, n in (
+        (post_weight, "post_weight"), (post_bias, "post_bias"), (pre_weight, "pre_weight"),
+        (pre_bias, "pre_bias"))]
+    unchanged = o is None and beta == 1.0 and h_out is None
+    if h_out is None and not unchanged:
+        h_out = torch.empty((T, d), dtype=h.dtype, device=dev)
+    if pre != "none" and u is None:
+        u = torch.empty((T, d), dtype=dt, device=dev)
+    hop, ldho = _matrix(h_out, "h_out", (T, d), h.dtype, dev) if h_out is not None else (0, d)
+    up, ldu = _matrix(u, "u", (T, d), dt, dev) if u is not None else (0, d)
+    with _on(dev):
+        check(load().block_norm(ctypes.byref(desc), hp, ldh, op, ldo, vec[0], vec[1], gp, ldg,
+                                vec[2], vec[3], hop, ldho, up, ldu, _stream_handle(stream)))
+    return (h if unchanged else h_out), u

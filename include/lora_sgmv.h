@@ -568,6 +568,51 @@ lora_status sgmv_fused_sigma(const lora_pool *p, const lora_plan *pl, int32_t la
                              int32_t num_sigma, const void *base, int64_t ldb, void *y,
                              int64_t ldy, void *stream);
 
+/* ---------------------------------------------------- around the delta ---- */
+/* The operators next to the delta in a decoder layer: the residual stream's
+ * norms (block_norm), which make the x the delta reads and take the y it
+ * writes.  Inference only: no gradients.  They need no pool or plan; the
+ * conventions above hold, except that rows may have any width, any stride
+ * and only their elements' alignment. */
+
+/* Norms: none, v / sqrt(mean(v^2) + eps), or (v - mean v) / sqrt(mean((v -
+ * mean v)^2) + eps); each times its weight plus its bias. */
+typedef enum { LORA_NORM_NONE = 0, LORA_NORM_RMS = 1, LORA_NORM_LAYER = 2 } lora_norm_kind;
+/* What a gate's values go through: nothing, 1 / (1 + exp(-g)), tanh(g). */
+typedef enum { LORA_GATE_NONE = 0, LORA_GATE_SIGMOID = 1, LORA_GATE_TANH = 2 } lora_gate_act;
+
+#define LORA_NORM_MAX_WIDTH 32768
+
+typedef struct {
+    int32_t dtype;        /* lora_dtype of o, u, the gate and the norms' vectors */
+    int32_t stream_dtype; /* lora_dtype of h and h_out: dtype, or LORA_F32 */
+    int32_t num_tokens;   /* T >= 0 rows */
+    int32_t width;        /* 1 .. LORA_NORM_MAX_WIDTH elements a row */
+    int32_t post, pre;    /* lora_norm_kind of the block's output and of the next block's input */
+    int32_t gate_act;     /* lora_gate_act */
+    int32_t unit_offset;  /* 1: weights are stored less 1 (the factor is 1 + w) */
+    float alpha, beta;    /* scales of the block's output and of the stream */
+    float eps;            /* >= 0 */
+} lora_norm_desc;
+
+/* The residual stream past one block, and the input of the next, in one pass:
+ *     h_out = beta h + alpha gate_act(gate) * N_post(o),   u = N_pre(h_out),
+ * in float32 from the inputs' values, h_out and u each rounded once (u is
+ * formed from the unrounded h_out).  NULL pointers: o (no block output:
+ * h_out = beta h, and post and gate must be absent too), post_weight /
+ * pre_weight (ones), post_bias / pre_bias (zeros), gate (ones), h_out (not
+ * written), u (not written; pre must then be LORA_NORM_NONE).  gate is one
+ * row for every token (ldg = 0) or a row per token.  h_out may be h itself
+ * (same pointer and stride); no other output may overlap an input or the
+ * other output.  Rows at or past num_tokens are not touched.
+ * Errors: LORA_EINVAL (null or misaligned pointers, sizes, strides, kinds,
+ * overlap, scales that are not finite), LORA_EDTYPE, LORA_EHIP. */
+lora_status block_norm(const lora_norm_desc *d, const void *h, int64_t ldh, const void *o,
+                       int64_t ldo, const void *post_weight, const void *post_bias,
+                       const void *gate, int64_t ldg, const void *pre_weight,
+                       const void *pre_bias, void *h_out, int64_t ldho, void *u, int64_t ldu,
+                       void *stream);
+
 /* --------------------------------------------------------------- debug ---- */
 /* The library built with LORA_SGMV_DEBUG (libhab_lora_debug.so, for
  * debugging the kernels or a caller's plan memory) checks in every work unit
