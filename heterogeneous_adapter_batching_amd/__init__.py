@@ -20,10 +20,13 @@ from .api import (  # noqa: F401
     sgmv_expand_partials, sgmv_expand_partials_sigma, sgmv_fused_static, plan_opts_default,
     debug_checks,
 )
-from .layer import block_norm  # noqa: F401
+from .layer import (  # noqa: F401
+    block_norm, frozen_linear, linear_workspace_bytes, sgmv_linear, sgmv_linear_workspace_bytes,
+)
 
 __all__ = ["Pool", "Plan", "sgmv_shrink", "sgmv_expand", "sgmv_fused", "sgmv_expand_sigma",
            "sgmv_fused_sigma", "sgmv_shrink_partials", "sgmv_expand_partials",
            "sgmv_expand_partials_sigma", "sgmv_fused_static",
            "pool_bytes_for", "extent_bytes", "pack_adapter", "Cache", "LoraError", "load",
-           "plan_opts_default", "debug_checks", "block_norm"]
+           "plan_opts_default", "debug_checks", "block_norm", "frozen_linear",
+           "linear_workspace_bytes", "sgmv_linear", "sgmv_linear_workspace_bytes"]

@@ -52,6 +52,11 @@ class NormDesc(ctypes.Structure):
                 ("beta", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("act", ctypes.c_int32), ("glu", ctypes.c_int32)]
+
+
 _i32, _i64, _u64, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
 _vp, _i32p = ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)
 _pp = ctypes.POINTER(ctypes.c_void_p)
@@ -119,9 +124,16 @@ SIGNATURES = {
                                 ctypes.POINTER(_u64)]),
     "block_norm": (_i32, [ctypes.POINTER(NormDesc), _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
                           _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "frozen_linear_workspace_bytes": (_u64, [ctypes.POINTER(LinearDesc)]),
+    "frozen_linear": (_i32, [ctypes.POINTER(LinearDesc), _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp,
+                             _i64, _vp, _u64, _vp]),
+    "sgmv_linear_workspace_bytes": (_u64, [_vp, ctypes.POINTER(LinearDesc), _i32]),
+    "sgmv_linear": (_i32, [_vp, _vp, _i32, _i32, _i32p, _i32p, ctypes.POINTER(LinearDesc), _vp,
+                           _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _u64, _vp]),
 }
 
-# lora_norm_kind, lora_gate_act
+# lora_norm_kind, lora_gate_act, lora_act
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
 LORA_NORM_MAX_WIDTH = 32768

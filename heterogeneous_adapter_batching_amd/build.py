@@ -23,7 +23,7 @@ ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, "lora_sgmv.cpp"), os.path.join(CSRC, "exchange.cpp"),
            os.path.join(CSRC, "layer.cpp"), os.path.join(CSRC, "kernels.hip"),
-           os.path.join(CSRC, "norm.hip")]
+           os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "linear.hip")]
 
 # Packed float32 ALU ops are switched off for all device code; the compiler's
 # host pass warns that it does not know the feature, which is harmless.

@@ -29,7 +29,14 @@ hipError_t launch_expand_merge(int, int, int, const MergeArgs &, int, hipStream_
 hipError_t launch_block_norm(int, int, const NormArgs &, hipStream_t) {
     return hipErrorInvalidValue;
 }
+hipError_t launch_linear(int, const LinearPlan &, bool, LinearArgs, hipStream_t) {
+    return hipErrorInvalidValue;
+}
 hipError_t static_scratch(void **, uint64_t *) { return hipErrorInvalidValue; }
 bool debug_build() { return false; }
 hipError_t debug_errors(uint32_t *, bool) { return hipErrorInvalidValue; }
+hipError_t debug_word(uint32_t **word) {
+    *word = nullptr;
+    return hipSuccess;
+}
 }  // namespace lora

@@ -1784,6 +1784,12 @@ hipError_t debug_errors(uint32_t *bits, bool clear) {
     return hipSuccess;
 }
 
+hipError_t debug_word(uint32_t **word) {
+    *word = nullptr;
+    return kDebug ? hipGetSymbolAddress(reinterpret_cast<void **>(word), HIP_SYMBOL(g_debug_errors))
+                  : hipSuccess;
+}
+
 hipError_t launch_shrink(int dtype, int tt, bool mp, const ShrinkArgs &a, hipStream_t s) {
     if (a.units <= 0) return hipSuccess;
     return dtype == LORA_BF16 ? shrink_dispatch<uint16_t>(tt, mp, a, s)

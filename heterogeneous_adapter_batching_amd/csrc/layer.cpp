@@ -1,5 +1,7 @@
 // Host side of the operators around the delta: validation and launch geometry
-// of block_norm.  Nothing is enqueued unless every argument holds.
+// of block_norm and frozen_linear.  Nothing is enqueued unless every argument
+// holds.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -57,9 +59,150 @@ bool same(const Span &a, const Span &b) {
     return a.ptr == b.ptr && a.es == b.es && (a.ld == b.ld || (a.rows == 1 && b.rows == 1));
 }
 
+uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
+
+// Leading dimension of the partial products: whole 64-column groups, with
+// room for the vector that starts at the last column.
+int64_t partial_ld(int64_t wide) { return int64_t(round_up(uint64_t(wide) + 3, 64)); }
+
 }  // namespace
 
+namespace lora {
+
+LinearPlan linear_plan(int dtype, int T, int n, int k, bool glu) {
+    LinearPlan pl{};
+    const int es = esize(dtype);
+    const int nk = int((int64_t(k) * es + kKBytes - 1) / kKBytes);
+    const int64_t wide = glu ? 2 * int64_t(n) : n;
+    pl.splits = 1;
+    pl.k_tiles = nk;
+    if (T <= 32) {
+        pl.kind = kLinearRows;
+        pl.bt = T <= 16 ? 16 : 32;
+        pl.bn = 16;
+        return pl;
+    }
+    pl.kind = kLinearTile;
+    auto tiles = [&](int bt, int bn) { return int64_t((T + bt - 1) / bt) * ((wide + bn - 1) / bn); };
+    if (dtype == LORA_BF16 && T > 128 && tiles(256, 256) >= 200) {
+        pl.bt = pl.bn = 256;
+    } else {
+        pl.bt = T <= 64 ? 64 : 128;
+        pl.bn = 128;
+    }
+    // too few tiles for the chip: split K, at least 4 K tiles a split
+    const int64_t have = tiles(pl.bt, pl.bn);
+    if (have < 192) {
+        const int64_t want = std::min<int64_t>((256 + have - 1) / have, std::max(nk / 4, 1));
+        pl.k_tiles = int((nk + want - 1) / want);
+        pl.splits = (nk + pl.k_tiles - 1) / pl.k_tiles;
+    }
+    if (pl.splits > 1) pl.ws_bytes = round_up(4ull * pl.splits * T * partial_ld(wide), 256);
+    return pl;
+}
+
+lora_status check_linear_desc(const lora_linear_desc *d) {
+    if (!d) return set_errorf(LORA_EINVAL, "null product descriptor");
+    if (!is_dtype(d->dtype))
+        return set_errorf(LORA_EDTYPE, "dtype %d is neither LORA_F32 nor LORA_BF16", d->dtype);
+    if (d->num_tokens < 0) return set_errorf(LORA_EINVAL, "num_tokens %d < 0", d->num_tokens);
+    if (d->n < 1 || d->n > (1 << 28)) return set_errorf(LORA_EINVAL, "n %d not in 1..2^28", d->n);
+    if (d->k < 8 || d->k % 8 || d->k > LORA_LINEAR_MAX_K)
+        return set_errorf(LORA_EINVAL, "k %d is not a multiple of 8 in 8..%d", d->k,
+                          LORA_LINEAR_MAX_K);
+    if (d->act < LORA_ACT_NONE || d->act > LORA_ACT_GELU_TANH)
+        return set_errorf(LORA_EINVAL, "act %d is not a lora_act", d->act);
+    if (d->glu != 0 && d->glu != 1) return set_errorf(LORA_EINVAL, "glu %d is neither 0 nor 1", d->glu);
+    // tiles, and so workgroups, are counted in 32 bits
+    if (int64_t(d->num_tokens / 64 + 1) * (int64_t(d->n) * (1 + d->glu) / 64 + 1) > (1 << 30))
+        return set_errorf(LORA_EINVAL, "a product of %d x %d outputs is too large", d->num_tokens,
+                          d->n);
+    return LORA_OK;
+}
+
+lora_status check_linear(const LinearCall &c, uint64_t need) {
+    const lora_linear_desc &d = *c.d;
+    const int32_t es = esize(d.dtype);
+    const int64_t T = d.num_tokens, n = d.n, k = d.k, wide = n * (1 + d.glu);
+    const Span x{"x", c.x, c.ldx, k, T, es}, w{"w", c.w, c.ldw, k, wide, es},
+        b{"bias", c.bias, wide, wide, 1, es}, r{"residual", c.residual, c.ldr, n, T, es},
+        y{"y", c.y, c.ldy, n, T, es};
+    lora_status st;
+    for (const Span *s : {&x, &w}) {
+        if ((st = check_span(*s)) != LORA_OK) return st;
+        if (s->lo() % 16) return set_errorf(LORA_EINVAL, "%s must be 16-byte aligned", s->name);
+        if (s->ld < k || s->ld % 8 || s->ld > LORA_LINEAR_MAX_K)
+            return set_errorf(LORA_EINVAL, "ld of %s (%lld) is not a multiple of 8 in k..%d",
+                              s->name, (long long)s->ld, LORA_LINEAR_MAX_K);
+    }
+    if ((st = check_span(y)) != LORA_OK) return st;
+    if (b.ptr && (st = check_span(b)) != LORA_OK) return st;
+    if (r.ptr && (st = check_span(r)) != LORA_OK) return st;
+    for (const Span *in : {&x, &w, &b})
+        if (overlap(y, *in)) return set_errorf(LORA_EINVAL, "y overlaps %s", in->name);
+    if (overlap(y, r) && !same(y, r))
+        return set_errorf(LORA_EINVAL, "y overlaps residual without being it");
+    if (need) {
+        if (!c.ws || (reinterpret_cast<uintptr_t>(c.ws) & 255))
+            return set_errorf(LORA_EINVAL, "the workspace must be non-null and 256-byte aligned");
+        if (c.ws_bytes < need)
+            return set_errorf(LORA_ESTATE, "workspace of %llu bytes < %llu needed",
+                              (unsigned long long)c.ws_bytes, (unsigned long long)need);
+        const Span ws{"the workspace", c.ws, int64_t(need), int64_t(need), 1, 1};
+        for (const Span *s : {&x, &w, &b, &r, &y})
+            if (overlap(ws, *s))
+                return set_errorf(LORA_EINVAL, "the workspace overlaps %s", s->name);
+    }
+    return LORA_OK;
+}
+
+lora_status run_linear(const LinearCall &c, const LinearPlan &pl, void *partial,
+                       const DeltaArgs &delta, hipStream_t s) {
+    const lora_linear_desc &d = *c.d;
+    LinearArgs a{};
+    a.x = static_cast<const uint8_t *>(c.x);
+    a.w = static_cast<const uint8_t *>(c.w);
+    a.bias = static_cast<const uint8_t *>(c.bias);
+    a.residual = static_cast<const uint8_t *>(c.residual);
+    a.y = static_cast<uint8_t *>(c.y);
+    a.partial = static_cast<float *>(partial);
+    a.ldx = c.ldx;
+    a.ldw = c.ldw;
+    a.ldr = c.ldr;
+    a.ldy = c.ldy;
+    a.T = d.num_tokens;
+    a.k = d.k;
+    a.n = d.n;
+    a.wide = d.n * (1 + d.glu);
+    a.ldp = partial_ld(a.wide);
+    a.act = d.act;
+    a.delta = delta;
+    const hipError_t e = launch_linear(d.dtype, pl, d.glu != 0, a, s);
+    if (e != hipSuccess) return set_errorf(LORA_EHIP, "product launch: %s", hipGetErrorString(e));
+    return LORA_OK;
+}
+
+}  // namespace lora
+
 extern "C" {
+
+uint64_t frozen_linear_workspace_bytes(const lora_linear_desc *d) {
+    if (lora::check_linear_desc(d) != LORA_OK || d->num_tokens == 0) return 0;
+    return lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0).ws_bytes;
+}
+
+lora_status frozen_linear(const lora_linear_desc *d, const void *x, int64_t ldx, const void *w,
+                          int64_t ldw, const void *bias, const void *residual, int64_t ldr,
+                          void *y, int64_t ldy, void *ws, uint64_t ws_bytes, void *stream) {
+    lora_status st = lora::check_linear_desc(d);
+    if (st != LORA_OK) return st;
+    if (d->num_tokens == 0) return LORA_OK;   // empty batch: no tensor is looked at
+    const lora::LinearCall c{d, x, ldx, w, ldw, bias, residual, ldr, y, ldy, ws, ws_bytes};
+    const lora::LinearPlan pl = lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0);
+    st = lora::check_linear(c, pl.ws_bytes);
+    if (st != LORA_OK) return st;
+    return lora::run_linear(c, pl, ws, lora::DeltaArgs{}, static_cast<hipStream_t>(stream));
+}
 
 lora_status block_norm(const lora_norm_desc *d, const void *h, int64_t ldh, const void *o,
                        int64_t ldo, const void *post_weight, const void *post_bias,

@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include "lora_sgmv.h"
+#include "sgmv_internal.h"
 
 namespace lora {
 
@@ -31,5 +32,74 @@ constexpr int kNormChunk = 8;       // consecutive elements a lane holds
 constexpr int kNormMaxWidth = 16 * 64 * kNormChunk * 4;   // 16 waves of 4 chunks a lane
 static_assert(kNormMaxWidth == LORA_NORM_MAX_WIDTH, "the widest row the launch takes");
 hipError_t launch_block_norm(int dtype, int stream_dtype, const NormArgs &a, hipStream_t s);
+
+// ---------------------------------------------------------------- linear ----
+// The adapters of one product call: the delta scale * B v of every token,
+// added before the activation.  Columns are those before the activation
+// (with a gated pair: gate's, then up's).
+struct DeltaArgs {
+    const TokenRow *rows;        // [T], null: no adapters
+    const float *v;              // [T][ldv] float32, projection i at column i * r_max
+    const uint8_t *slab;
+    int64_t ldv;
+    int64_t coef_b[LORA_MAX_PROJ];  // B block offset = extent + r_pad * esize * coef_b[i]
+    int32_t h_out[LORA_MAX_PROJ];
+    int32_t y_off[LORA_MAX_PROJ];
+    int32_t nproj;
+    int32_t r_max;
+    uint32_t *dbg_word;          // debug build: where failed checks are noted
+    DebugBounds dbg;
+};
+
+struct LinearArgs {
+    const uint8_t *x, *w;        // [T][ldx], [wide][ldw]
+    const uint8_t *bias;         // [wide] or null
+    const uint8_t *residual;     // [T][ldr] or null
+    uint8_t *y;                  // [T][ldy]
+    float *partial;              // split products: [splits][T][ldp] float32
+    int64_t ldx, ldw, ldr, ldy, ldp;   // elements
+    int32_t T, k;
+    int32_t n;                   // width of y
+    int32_t wide;                // rows of w: n, or 2 n with a gated pair
+    int32_t act;                 // lora_act
+    int32_t tiles_t, tiles_n;    // tiles of the launch (tile kernel)
+    int32_t splits, k_tiles;     // K tiles (128 bytes of a row) of one split
+    int32_t units;               // workgroups with work (the grid is rounded up)
+    DeltaArgs delta;
+};
+
+// How a product runs: one launch, or `splits` > 1 partial products along K
+// and a launch that joins them.
+enum LinearKind : int32_t { kLinearRows, kLinearTile };
+struct LinearPlan {
+    LinearKind kind;
+    int32_t bt, bn;              // tokens and rows of w of a tile (rows: 16 TT, 16)
+    int32_t splits, k_tiles;
+    uint64_t ws_bytes;           // of the partial products
+};
+constexpr int kKBytes = 128;     // bytes of a row a K tile covers
+LinearPlan linear_plan(int dtype, int T, int n, int k, bool glu);
+
+// The arguments of a product call, as the entry points take them.
+struct LinearCall {
+    const lora_linear_desc *d;
+    const void *x;
+    int64_t ldx;
+    const void *w;
+    int64_t ldw;
+    const void *bias, *residual;
+    int64_t ldr;
+    void *y;
+    int64_t ldy;
+    void *ws;
+    uint64_t ws_bytes;
+};
+lora_status check_linear_desc(const lora_linear_desc *d);
+// `need`: the workspace bytes of the call
+lora_status check_linear(const LinearCall &c, uint64_t need);
+// Enqueues a checked call; partial sums at `partial` (of the plan's ws_bytes).
+lora_status run_linear(const LinearCall &c, const LinearPlan &pl, void *partial,
+                       const DeltaArgs &delta, hipStream_t s);
+hipError_t launch_linear(int dtype, const LinearPlan &pl, bool glu, LinearArgs a, hipStream_t s);
 
 }  // namespace lora

@@ -19,6 +19,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "layer_internal.h"
 #include "lora_sgmv.h"
 #include "sgmv_internal.h"
 
@@ -171,7 +172,7 @@ struct PlanCounts {
 // Byte offsets of the tables in a plan workspace, and its size.
 struct PlanLayout {
     uint64_t off_tok = 0, off_blocks = 0, off_tiles = 0, off_btok = 0, off_ttok = 0, off_tsig = 0,
-             off_tw = 0, off_mblocks = 0, off_part = 0;
+             off_tw = 0, off_mblocks = 0, off_trow = 0, off_part = 0;
     uint64_t off_lv = 0;   // long groups' v rows, from off_part (plain plans)
     uint64_t image_bytes = 0, part_bytes = 0, ws_bytes = 0;
 };
@@ -221,6 +222,7 @@ PlanLayout plan_layout(const lora_pool_desc &d, const PlanCounts &c, int32_t mp,
     L.off_tsig = o;    o = round_up(o + 4ull * T, 256);
     L.off_tw = o;      o = round_up(o + 4ull * T, 256);
     L.off_mblocks = o; o = round_up(o + sizeof(lora::MergeBlock) * uint64_t(c.mb), 256);
+    L.off_trow = o;    o = round_up(o + sizeof(lora::TokenRow) * T, 256);
     L.image_bytes = o;
     // the shrink's partial tiles: every rank tile at the plan's tiles per
     // block (a merge plan), or the short groups' tiles at one 16-token tile
@@ -251,6 +253,7 @@ struct lora_plan {
     std::vector<int32_t> token_order;    // plan order: grouped adapter tokens, then the rest
     std::vector<int32_t> token_sigma;    // core index per plan-order row (-1: none)
     std::vector<float> token_weight;     // weight per plan-order row (weighted plans)
+    std::vector<lora::TokenRow> token_rows;  // per token row (a merge plan's are not read)
     std::vector<int32_t> token_slot;     // merge slot per plan-order row (-1: none)
     bool weighted = false;
     int32_t merge_k = 0;                 // slots per segment of a merge plan (0: not one)
@@ -699,6 +702,7 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
     pl->max_rpad_long = pl->min_rpad_long = 0;
     pl->tt = 1;
     pl->token_group.assign(T, -1);
+    pl->token_rows.assign(T, lora::TokenRow{0u, 0u, 0, 0.f});
 
     // groups in first-appearance order (runs with rows only); a member is a
     // (row, run) pair
@@ -796,6 +800,10 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
             pl->token_sigma.push_back(rn ? rn->sigma : -1);
             pl->token_weight.push_back(rn ? rn->weight : 1.0f);
             pl->token_slot.push_back(rn ? rn->slot : -1);
+            if (sl)
+                pl->token_rows[m.first] =
+                    lora::TokenRow{uint32_t(sl->off & 0xffffffffu), uint32_t(sl->off >> 32),
+                                   sl->r_pad, sl->scale * (rn ? rn->weight : 1.0f)};
             if (rn) pl->max_sigma = std::max(pl->max_sigma, rn->sigma);
         }
     };
@@ -1089,6 +1097,8 @@ lora_status lora_plan_upload(lora_plan *pl, void *ws, uint64_t ws_bytes, int32_t
     if (R) std::memcpy(img + lay.off_tok, pl->token_order.data(), 4ull * R);
     if (R) std::memcpy(img + lay.off_tsig, pl->token_sigma.data(), 4ull * R);
     if (R && pl->weighted) std::memcpy(img + lay.off_tw, pl->token_weight.data(), 4ull * R);
+    if (pl->T)
+        std::memcpy(img + lay.off_trow, pl->token_rows.data(), sizeof(lora::TokenRow) * pl->T);
     if (!pl->mblocks.empty())
         std::memcpy(img + lay.off_mblocks, pl->mblocks.data(),
                     sizeof(lora::MergeBlock) * pl->mblocks.size());
@@ -1654,6 +1664,11 @@ lora_status fused_body(const lora_pool *p, const lora_plan *pl, int32_t layer, i
                       cores, &pt);
 }
 
+// The v rows of a product call with adapters, ahead of its partial products.
+uint64_t linear_v_bytes(const lora_pool *p, int32_t T, int32_t nproj) {
+    return round_up(4ull * uint64_t(T) * uint64_t(nproj) * uint64_t(p->d.r_max), 256);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1889,6 +1904,68 @@ lora_status sgmv_expand_partials_sigma(const lora_pool *p, const lora_plan *pl, 
     io.base = base;
     io.ldb = ldb;
     return run_prefill(p, pl, layer, nproj, projs, yoff, cc, io, hs, cores);
+}
+
+uint64_t sgmv_linear_workspace_bytes(const lora_pool *p, const lora_linear_desc *d,
+                                     int32_t nproj) {
+    if (!p || lora::check_linear_desc(d) != LORA_OK || d->num_tokens == 0 || nproj < 1 ||
+        nproj > LORA_MAX_PROJ)
+        return 0;
+    return linear_v_bytes(p, d->num_tokens, nproj) +
+           lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0).ws_bytes;
+}
+
+lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, int32_t nproj,
+                        const int32_t *projs, const int32_t *yoff, const lora_linear_desc *d,
+                        const void *x, int64_t ldx, const void *w, int64_t ldw, const void *bias,
+                        const void *residual, int64_t ldr, void *y, int64_t ldy, void *ws,
+                        uint64_t ws_bytes, void *stream) {
+    CallCheck cc;
+    lora_status st = check_call(p, pl, layer, nproj, projs, &cc);
+    if (st != LORA_OK) return st;
+    if (pl->merge_k) return fail(LORA_EINVAL, "a merge plan's delta is sgmv_fused's");
+    if (pl->max_sigma >= 0) return fail(LORA_EINVAL, "a plan with cores needs the sigma calls");
+    st = lora::check_linear_desc(d);
+    if (st != LORA_OK) return st;
+    if (d->dtype != p->d.dtype) return fail(LORA_EDTYPE, "dtype %d is not the pool's", d->dtype);
+    if (d->num_tokens != pl->T)
+        return fail(LORA_EINVAL, "num_tokens %d is not the plan's %d", d->num_tokens, pl->T);
+    if (d->k != cc.h_in)
+        return fail(LORA_EINVAL, "k %d is not the projections' h_in %d", d->k, cc.h_in);
+    if (!yoff) return fail(LORA_EINVAL, "null y_offsets");
+    for (int i = 0; i < nproj; ++i)
+        if (yoff[i] < 0 || int64_t(yoff[i]) + p->d.h_out[projs[i]] > int64_t(d->n) * (1 + d->glu))
+            return fail(LORA_EINVAL, "slice of projection %d exceeds the product's columns",
+                        projs[i]);
+    if (pl->T == 0) return LORA_OK;   // empty batch: nothing to read or write
+    const lora::LinearCall c{d, x, ldx, w, ldw, bias, residual, ldr, y, ldy, ws, ws_bytes};
+    const lora::LinearPlan lp = lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0);
+    const uint64_t v_bytes = linear_v_bytes(p, pl->T, nproj);
+    st = lora::check_linear(c, v_bytes + lp.ws_bytes);
+    if (st != LORA_OK) return st;
+    lora::DeltaArgs da{};
+    if (pl->nb_act > 0) {
+        da.v = static_cast<const float *>(ws);
+        da.ldv = int64_t(nproj) * p->d.r_max;
+        da.rows = reinterpret_cast<const lora::TokenRow *>(static_cast<const uint8_t *>(pl->ws) +
+                                                           pl->lay.off_trow);
+        da.slab = p->slab;
+        for (int i = 0; i < nproj; ++i) {
+            da.coef_b[i] = p->coef_b(layer, projs[i]);
+            da.h_out[i] = p->d.h_out[projs[i]];
+            da.y_off[i] = yoff[i];
+        }
+        da.nproj = nproj;
+        da.r_max = p->d.r_max;
+        da.dbg = debug_bounds(p, pl);
+        const hipError_t e = lora::debug_word(&da.dbg_word);
+        if (e != hipSuccess) return hip_fail(e, "debug word");
+        st = sgmv_shrink(p, pl, layer, nproj, projs, x, ldx, static_cast<float *>(ws), da.ldv,
+                         stream);
+        if (st != LORA_OK) return st;
+    }
+    return lora::run_linear(c, lp, static_cast<uint8_t *>(ws) + v_bytes, da,
+                            static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -94,6 +94,16 @@ struct TileDesc {
 };
 static_assert(sizeof(TileDesc) == 32, "TileDesc is 32 bytes");
 
+// One token row of a plan as the product with adapters reads it: its
+// adapter's extent, padded rank (0: none) and scale (with the segment's
+// weight).
+struct TokenRow {
+    uint32_t ext_lo, ext_hi;
+    int32_t r_pad;
+    float scale;
+};
+static_assert(sizeof(TokenRow) == 16, "TokenRow is one 16-byte load");
+
 // What the debug build checks every unit against (see LORA_SGMV_DEBUG in
 // kernels.hip): the slab's bytes (every adapter block a unit addresses lies
 // inside), the tokens of the batch (every token row read from the plan lies
@@ -402,5 +412,8 @@ hipError_t static_scratch(void **ptr, uint64_t *bytes);
 // device's debug error bits (after waiting for the device), cleared on request.
 bool debug_build();
 hipError_t debug_errors(uint32_t *bits, bool clear);
+// The address of the current device's debug error word (null in the release
+// build), for kernels of other files.
+hipError_t debug_word(uint32_t **word);
 
 }  // namespace lora

@@ -1,12 +1,13 @@
 """The operators around the delta over the C ABI (argument marshalling only):
-the residual stream's norms."""
+the residual stream's norms, the frozen layer's product, and the product with
+the delta inside its activation."""
 from __future__ import annotations
 
 import contextlib
 import ctypes
 
-from ._lib import GATE_ACTS, LORA_BF16, LORA_F32, NORMS, NormDesc, check, load
-from .api import _stream_handle, _torch
+from ._lib import (ACTS, GATE_ACTS, LORA_BF16, LORA_F32, NORMS, LinearDesc, NormDesc, check, load)
+from .api import _DTYPES, _offsets, _projs, _stream_handle, _torch
 
 
 def _dtype_code(t, name):
@@ -64,6 +65,16 @@ def _on(device):
     return torch.cuda.device(device)
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor for a launch on `stream` (None: the current one).  Freed memory
+    is given out again in the order of the stream it was made on, so another
+    one's use is noted."""
+    t = _torch().empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def block_norm(h, o=None, *, post="none", post_weight=None, post_bias=None, gate=None,
                gate_act="none", alpha=1.0, beta=1.0, pre="rms", pre_weight=None, pre_bias=None,
                eps=1e-5, unit_offset=False, h_out=None, u=None, stream=None):
@@ -102,12 +113,99 @@ def block_norm(h, o=None, *, post="none", post_weight=None, post_bias=None, gate
         (pre_bias, "pre_bias"))]
     unchanged = o is None and beta == 1.0 and h_out is None
     if h_out is None and not unchanged:
-        h_out = torch.empty((T, d), dtype=h.dtype, device=dev)
+        h_out = _new((T, d), h.dtype, dev, stream)
     if pre != "none" and u is None:
-        u = torch.empty((T, d), dtype=dt, device=dev)
+        u = _new((T, d), dt, dev, stream)
     hop, ldho = _matrix(h_out, "h_out", (T, d), h.dtype, dev) if h_out is not None else (0, d)
     up, ldu = _matrix(u, "u", (T, d), dt, dev) if u is not None else (0, d)
     with _on(dev):
         check(load().block_norm(ctypes.byref(desc), hp, ldh, op, ldo, vec[0], vec[1], gp, ldg,
                                 vec[2], vec[3], hop, ldho, up, ldu, _stream_handle(stream)))
     return (h if unchanged else h_out), u
+
+
+def _linear_desc(num_tokens, n, k, dtype, glu, act="none"):
+    return LinearDesc(dtype, num_tokens, n, k, _code(ACTS, act, "act"), int(bool(glu)))
+
+
+def linear_workspace_bytes(num_tokens: int, n: int, k: int, dtype: str = "bf16",
+                           glu: bool = False) -> int:
+    """Bytes of workspace a frozen_linear call of these sizes takes (0: none);
+    n is the width of y."""
+    d = _linear_desc(num_tokens, n, k, _DTYPES[dtype], glu)
+    return int(load().frozen_linear_workspace_bytes(ctypes.byref(d)))
+
+
+def sgmv_linear_workspace_bytes(pool, num_tokens: int, n: int, k: int, nproj: int,
+                                glu: bool = False) -> int:
+    """The same for sgmv_linear over nproj projections of the pool."""
+    d = _linear_desc(num_tokens, n, k, pool.desc.dtype, glu)
+    return int(load().sgmv_linear_workspace_bytes(pool.handle, ctypes.byref(d), nproj))
+
+
+def _linear_call(x, w, bias, act, glu, residual, y, ws, stream, need, call):
+    """Checks the tensors of a product call, makes y and the workspace where
+    they are not given, and hands the C arguments to `call`."""
+    torch = _torch()
+    xp, ldx = _matrix(x, "x")
+    dev, dt = x.device, x.dtype
+    wp, ldw = _matrix(w, "w", None, dt, dev)
+    (T, k), (wide, kw) = x.shape, w.shape
+    if kw != k:
+        raise ValueError(f"w has rows of {kw}, x of {k}")
+    if glu and wide % 2:
+        raise ValueError(f"w must hold a gate and an up of the same rows, got {wide}")
+    n = wide // 2 if glu else wide
+    bp = _vector(bias, "bias", wide, dt, dev)
+    rp, ldr = _matrix(residual, "residual", (T, n), dt, dev) if residual is not None else (0, n)
+    if y is None:
+        y = _new((T, n), dt, dev, stream)
+    yp, ldy = _matrix(y, "y", (T, n), dt, dev)
+    desc = _linear_desc(T, n, k, _dtype_code(x, "x"), glu, act)
+    if ws is None:
+        size = need(desc)
+        ws = _new((size,), torch.uint8, dev, stream) if size else None
+    elif not ws.is_cuda or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
+    wsp, wsn = (ws.data_ptr(), ws.numel() * ws.element_size()) if ws is not None else (0, 0)
+    with _on(dev):
+        check(call(desc, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, wsp, wsn, _stream_handle(stream)))
+    return y
+
+
+def frozen_linear(x, w, *, bias=None, act="none", glu=False, residual=None, y=None, ws=None,
+                  stream=None):
+    """The frozen layer's product with its epilogue, rounded once:
+
+        y = act(x w^T + bias) + residual
+        y = act(x wg^T + bias_g) * (x wu^T + bias_u) + residual     (glu)
+
+    x [T][k], w [n][k] (with glu [2 n][k]: the gate's rows, then the up's),
+    bias [rows of w], residual and y [T][n], all of one type, bfloat16 or
+    float32; k and the row strides of x and w are multiples of 8.  act is
+    "none", "relu", "silu", "gelu" or "gelu_tanh".  residual may be y.  ws: a
+    workspace of linear_workspace_bytes (made per call if not given).
+    Inference only.  Returns y."""
+    lib = load()
+    return _linear_call(
+        x, w, bias, act, glu, residual, y, ws, stream,
+        lambda d: lib.frozen_linear_workspace_bytes(ctypes.byref(d)),
+        lambda d, *a: lib.frozen_linear(ctypes.byref(d), *a))
+
+
+def sgmv_linear(pool, plan, layer, projs, y_offsets, x, w, *, bias=None, act="none", glu=False,
+                residual=None, y=None, ws=None, stream=None):
+    """frozen_linear with every token's LoRA delta inside the activation:
+    before it, columns y_offsets[i] .. + h_out of x w^T + bias get
+    s B (A x) of projection projs[i] (with glu the columns are the gate's n,
+    then the up's n).  plan: a plain or weighted plan of x's tokens."""
+    lib = pool.lib
+    count, parr = _projs(projs)
+    offs = _offsets(y_offsets)
+    if len(tuple(y_offsets)) != count:
+        raise ValueError("y_offsets must have one entry per projection")
+    return _linear_call(
+        x, w, bias, act, glu, residual, y, ws, stream,
+        lambda d: lib.sgmv_linear_workspace_bytes(pool.handle, ctypes.byref(d), count),
+        lambda d, *a: lib.sgmv_linear(pool.handle, plan.handle, layer, count, parr, offs,
+                                      ctypes.byref(d), *a))

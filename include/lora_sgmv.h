@@ -571,9 +571,11 @@ lora_status sgmv_fused_sigma(const lora_pool *p, const lora_plan *pl, int32_t la
 /* ---------------------------------------------------- around the delta ---- */
 /* The operators next to the delta in a decoder layer: the residual stream's
  * norms (block_norm), which make the x the delta reads and take the y it
- * writes.  Inference only: no gradients.  They need no pool or plan; the
- * conventions above hold, except that rows may have any width, any stride
- * and only their elements' alignment. */
+ * writes, and the frozen layer's product that the delta is added to
+ * (frozen_linear), also with the delta inside its activation (sgmv_linear).
+ * Inference only: no gradients.  The conventions above hold, except that
+ * rows may have any width and stride and only their elements' alignment
+ * where that is said. */
 
 /* Norms: none, v / sqrt(mean(v^2) + eps), or (v - mean v) / sqrt(mean((v -
  * mean v)^2) + eps); each times its weight plus its bias. */
@@ -612,6 +614,67 @@ lora_status block_norm(const lora_norm_desc *d, const void *h, int64_t ldh, cons
                        const void *gate, int64_t ldg, const void *pre_weight,
                        const void *pre_bias, void *h_out, int64_t ldho, void *u, int64_t ldu,
                        void *stream);
+
+/* Activations: v, max(v, 0), v / (1 + exp(-v)), v (1 + erf(v / sqrt 2)) / 2,
+ * v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2. */
+typedef enum {
+    LORA_ACT_NONE = 0,
+    LORA_ACT_RELU = 1,
+    LORA_ACT_SILU = 2,
+    LORA_ACT_GELU = 3,
+    LORA_ACT_GELU_TANH = 4
+} lora_act;
+
+#define LORA_LINEAR_MAX_K 1048576   /* also the largest leading dimension of x and w */
+
+typedef struct {
+    int32_t dtype;      /* lora_dtype of x, w, bias, residual and y */
+    int32_t num_tokens; /* T >= 0 */
+    int32_t n;          /* width of y, >= 1 */
+    int32_t k;          /* width of x: a multiple of 8, at most LORA_LINEAR_MAX_K */
+    int32_t act;        /* lora_act */
+    int32_t glu;        /* 1: w holds 2 n rows, the gate's n, then the up's n */
+} lora_linear_desc;
+
+/* The frozen layer's product with its epilogue, one rounding at the end:
+ *     y = act(x w^T + bias) + residual                                   (glu 0)
+ *     y = act(x wg^T + bias_g) * (x wu^T + bias_u) + residual            (glu 1)
+ * x: [T][ldx], w: [n or 2 n][ldw], y and residual: [T][ldy / ldr]; bias: n or
+ * 2 n values or NULL; residual may be NULL, and may be y itself (same
+ * pointer and stride).  x and w are 16-byte aligned with leading dimensions
+ * that are multiples of 8 (and at most LORA_LINEAR_MAX_K); bias, residual
+ * and y take any stride and their elements' alignment, and n any value.
+ * Products are exact and sums float32, in an order fixed by the sizes.  No
+ * tensor has a limit of 2 GiB here.
+ * A product with too few output tiles for the chip is split along k, through
+ * float32 partial sums in `ws`: at least frozen_linear_workspace_bytes(d)
+ * bytes, 256-byte aligned (0 bytes: ws may be NULL), overwritten by the
+ * call; calls that share it must not overlap.
+ * Errors: LORA_EINVAL (null or misaligned pointers, sizes, strides, an output
+ * that overlaps an input), LORA_EDTYPE, LORA_ESTATE (ws too small), LORA_EHIP. */
+uint64_t frozen_linear_workspace_bytes(const lora_linear_desc *d);
+lora_status frozen_linear(const lora_linear_desc *d, const void *x, int64_t ldx, const void *w,
+                          int64_t ldw, const void *bias, const void *residual, int64_t ldr,
+                          void *y, int64_t ldy, void *ws, uint64_t ws_bytes, void *stream);
+
+/* frozen_linear with every token's delta inside the activation:
+ *     z[:, y_offsets[i] : y_offsets[i] + h_out] = x w^T + bias + s B (A x),
+ * y = act(z) + residual (glu: act of z's first n columns times the other n).
+ * An adapter of a projection before an activation cannot be added after it,
+ * and one of a plain projection spares y a rounding and a pass.  `plan` is a
+ * plain or weighted plan over num_tokens tokens, uploaded for at least nproj
+ * projections; a merge plan and one with cores are refused.  Tokens without
+ * an adapter get the plain product.  The pool's dtype is d's, h_in of the
+ * listed projections is d->k, and their slices lie in the n (2 n with glu)
+ * columns of z.  v = A x goes through `ws` (sgmv_linear_workspace_bytes); the
+ * shrink uses the plan's workspace as sgmv_shrink does.  Other arguments and
+ * errors as frozen_linear and sgmv_shrink (x spans at most 2 GiB). */
+uint64_t sgmv_linear_workspace_bytes(const lora_pool *p, const lora_linear_desc *d, int32_t nproj);
+lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, int32_t nproj,
+                        const int32_t *projs, const int32_t *y_offsets, const lora_linear_desc *d,
+                        const void *x, int64_t ldx, const void *w, int64_t ldw, const void *bias,
+                        const void *residual, int64_t ldr, void *y, int64_t ldy, void *ws,
+                        uint64_t ws_bytes, void *stream);
 
 /* --------------------------------------------------------------- debug ---- */
 /* The library built with LORA_SGMV_DEBUG (libhab_lora_debug.so, for
