@@ -29,6 +29,7 @@ hipError_t launch_expand_merge(int, int, int, const MergeArgs &, int, hipStream_
 hipError_t launch_block_norm(int, int, const NormArgs &, hipStream_t) {
     return hipErrorInvalidValue;
 }
+hipError_t launch_operand(int, const OperandArgs &, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_linear(int, const LinearPlan &, bool, LinearArgs, hipStream_t) {
     return hipErrorInvalidValue;
 }

@@ -273,36 +273,6 @@ __global__ __launch_bounds__(256) void k_shrink(const ShrinkArgs a) {
     }
 }
 
-// Float offset of v entries (token slot `slot`, ranks j .. j + 3) of chunk 0
-// in the shrink's partials, and the stride between chunks.  Unit u = (rank
-// tile, chunk c, projection p) wrote tile u * ptt * 256: u = tile * nproj * c0
-// + c * nproj + p, token slot s and rank i at s * 16 + i.
-__device__ __forceinline__ uint32_t partial_off(int rt, int j, int slot, int p, int nproj, int c0,
-                                                int ptt) {
-    return uint32_t((rt + j / kTile) * nproj * c0 + p) * uint32_t(ptt * kTile * kTile) +
-           uint32_t(slot * kTile + j % kTile);
-}
-
-// The whole chunk sum in the one order: the ways, then ((s0 + s1) + s2) + s3.
-__device__ __forceinline__ f32x4 chunk_sum(rsrc_t pr, uint32_t off, uint32_t stride, int c0) {
-    f32x4 w[kSumWays];
-#pragma unroll
-    for (int k = 0; k < kSumWays; ++k) w[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int c = 0; c < c0; c += 8) {
-        u32x4 part[8];
-#pragma unroll
-        for (int g = 0; g < 8; ++g)
-            part[g] = bload16(pr, off_or_oob(c + g < c0, (off + uint32_t(c + g) * stride) * 4));
-#pragma unroll
-        for (int g = 0; g < 8; ++g)
-            if (c + g < c0) w[g % kSumWays] += __builtin_bit_cast(f32x4, part[g]);
-    }
-    f32x4 s = w[0];
-#pragma unroll
-    for (int k = 1; k < kSumWays; ++k) s += w[k];
-    return s;
-}
-
 // --------------------------------------------------------------- reduce -----
 // One workgroup per (expand block, projection): v = sum of the chunk partials.
 template <int TT>

@@ -38,18 +38,38 @@ hipError_t launch_block_norm(int dtype, int stream_dtype, const NormArgs &a, hip
 // added before the activation.  Columns are those before the activation
 // (with a gated pair: gate's, then up's).
 struct DeltaArgs {
-    const TokenRow *rows;        // [T], null: no adapters
-    const float *v;              // [T][ldv] float32, projection i at column i * r_max
+    const int32_t *order;        // [T] token row of each plan position; null: no adapters
+    const GroupRow *groups;      // adapter groups, in plan order
+    const int32_t *pos_group;    // [T] group of each plan position
+    const uint8_t *v;            // the operand: [T positions][nproj][pieces][r_max]
     const uint8_t *slab;
-    int64_t ldv;
     int64_t coef_b[LORA_MAX_PROJ];  // B block offset = extent + r_pad * esize * coef_b[i]
     int32_t h_out[LORA_MAX_PROJ];
     int32_t y_off[LORA_MAX_PROJ];
+    int32_t n_active;            // positions with an adapter (they come first)
+    int32_t max_rpad;            // largest padded rank of the plan
     int32_t nproj;
     int32_t r_max;
     uint32_t *dbg_word;          // debug build: where failed checks are noted
     DebugBounds dbg;
 };
+
+// The product's operand of the delta, scale * v, for every plan position of
+// the adapter blocks [0, nb): of short groups' blocks summed from the
+// shrink's partials, of long groups' ([0, nb_long)) read from v.
+struct OperandArgs {
+    const BlockDesc *blocks;
+    const float *partial;
+    const float *v;              // [T positions][nproj * r_max]
+    const float *tok_w;          // weights by plan position (null: none)
+    uint8_t *out;
+    uint32_t partial_bytes;
+    int32_t nb, nb_long, nproj, c0, r_max;
+    DebugBounds dbg;
+};
+// bytes of one operand entry: three bf16 pieces, or the float32 value
+constexpr int operand_bytes(int dtype) { return dtype == LORA_BF16 ? 6 : 4; }
+hipError_t launch_operand(int dtype, const OperandArgs &a, hipStream_t s);
 
 struct LinearArgs {
     const uint8_t *x, *w;        // [T][ldx], [wide][ldw]

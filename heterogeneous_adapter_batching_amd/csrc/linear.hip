@@ -124,7 +124,7 @@ template <typename T, bool GLU>
 __device__ __forceinline__ void finish(const LinearArgs &a, int t, int f, float (&v)[4],
                                        float (&up)[4]) {
     const int n = a.n - f;
-    if (t >= a.T || n <= 0) return;
+    if (t < 0 || n <= 0) return;
     if (a.bias) {
         float b[4];
         Run4<T>::load(a.bias, f, n, b);
@@ -150,91 +150,135 @@ __device__ __forceinline__ void finish(const LinearArgs &a, int t, int f, float 
     Run4<T>::store(a.y, int64_t(t) * a.ldy + f, n, v);
 }
 
+// -------------------------------------------------------------- operand -----
+// The delta's right operand for one (block, projection): scale * v of each
+// position, as three bf16 pieces whose sum is that float32 value exactly, or
+// (float32) the value.  The scale goes into v here, one float32 rounding per
+// entry, so that the products below need none.
+template <typename T> __global__ __launch_bounds__(256) void k_operand(const OperandArgs a) {
+    constexpr int P = VOperand<T>::kPieces, E = Elem<T>::E;
+    const int b = blockIdx.x / a.nproj, p = blockIdx.x % a.nproj;
+    BlockDesc blk = load_invariant(a.blocks + b);
+    if constexpr (kDebug) {
+        const bool ok = blk.tok_off >= 0 && blk.n_tok >= 0 &&
+                        blk.tok_off + blk.n_tok <= a.dbg.num_rows;
+        blk.n_tok = ok ? min(blk.n_tok, kMaxBlockTokens) : 0;
+    }
+    const rsrc_t pr = make_rsrc(a.partial, a.partial_bytes);
+    const int vecs = a.r_max / E;
+    for (int i = threadIdx.x; i < blk.n_tok * vecs; i += 256) {
+        const int ti = i / vecs, j = (i % vecs) * E, pos = blk.tok_off + ti;
+        const float s = a.tok_w ? blk.scale * a.tok_w[pos] : blk.scale;
+        float f[E];
+#pragma unroll
+        for (int h = 0; h < E / 4; ++h) {
+            f32x4 s4{0.f, 0.f, 0.f, 0.f};
+            if (j + 4 * h < blk.r_pad) {
+                if (b < a.nb_long)
+                    s4 = *reinterpret_cast<const f32x4 *>(
+                        a.v + (int64_t(pos) * a.nproj + p) * a.r_max + j + 4 * h);
+                else
+                    s4 = chunk_sum(pr, partial_off(blk.rt_before, j + 4 * h, blk.slot0 + ti, p,
+                                                   a.nproj, a.c0, 1),
+                                   uint32_t(a.nproj * kTile * kTile), a.c0);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[4 * h + k] = s * s4[k];
+        }
+        VOperand<T> vo;
+        vo.set(f);
+        uint8_t *o = a.out + ((int64_t(pos) * a.nproj + p) * P * a.r_max + j) * int64_t(sizeof(T));
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+            *reinterpret_cast<u32x4 *>(o + int64_t(k) * a.r_max * int64_t(sizeof(T))) = vo.piece[k];
+    }
+}
+
 // ---------------------------------------------------------------- delta -----
-// Adds scale * B v to one 16-token tile's accumulators: rows of the left
+// Adds the delta to the accumulators of 16 plan positions: rows of the left
 // operand are outputs f(j, r) = f0 + (r / 4) 4 G + 4 j + r % 4, so a lane
-// holds outputs f0 + 4 G q .. + 4 G of its token.  The tile's distinct
-// adapters are taken one after another (their B rows against every token's
-// v, kept only in the columns of the adapter's own tokens); of `nw` waves
-// that share the tile, wave w takes every nw-th of them.  v is split into
-// three bf16 pieces whose sum is v, so B v is the float32 product.
-template <typename T, int G>
-__device__ __forceinline__ void add_delta(const DeltaArgs &d, int T_, int t0, int f0, int w,
-                                          int nw, f32x4 (&acc)[G]) {
-    constexpr int E = Elem<T>::E, SPAN = 4 * E, KS = LORA_MAX_RANK / SPAN;
+// holds outputs f0 + 4 G q .. + 4 G of its position.  Positions are in plan
+// order, so their adapters are consecutive groups: each group's B rows
+// multiply every position's operand and are kept in the columns of the
+// group's own (so one adapter's infinities stay with its tokens).  Of `nw`
+// waves that share the tile, wave w takes every nw-th group.  A dependent
+// round trip to memory per group would be the cost here, so the B rows of NB
+// groups are in flight together: with one at a time the join of a decode
+// batch's q/k/v took 16.3 us.  KS: K-steps of the plan's largest rank.
+template <typename T, int G, int KS>
+__device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, int w, int nw,
+                                          f32x4 (&acc)[G]) {
+    constexpr int E = Elem<T>::E, SPAN = 4 * E, P = VOperand<T>::kPieces;
+    constexpr int NB = G * KS >= 16 ? 1 : G * KS >= 8 ? 2 : 4;
+    if (p0 >= d.n_active) return;                // uniform
     const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-    const int t = t0 + n;
-    TokenRow tr{0u, 0u, 0, 0.f};
-    if (t < T_) tr = d.rows[t];
-    const uint32_t have = uint32_t(__builtin_amdgcn_ballot_w64(tr.r_pad > 0)) & 0xffffu;
-    if (!have) return;
+    const int pos = p0 + n;
+    const int g0 = load_invariant(d.pos_group + p0);
+    const int g1 = load_invariant(d.pos_group + min(p0 + 15, d.n_active - 1));
+    const int vrow = P * d.r_max * int(sizeof(T));
     for (int p = 0; p < d.nproj; ++p) {
         const int lo = d.y_off[p], ho = d.h_out[p];
         if (f0 + 16 * G <= lo || f0 >= lo + ho) continue;
-        VOperand<T> vo[KS];
+        u32x4 vo[KS][P];
+        const uint8_t *vp = d.v + (int64_t(pos) * d.nproj + p) * vrow;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const int j0 = ks * SPAN + q * E;
-            float f[E];
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int i = 0; i < E; ++i) f[i] = 0.f;
-            if (j0 < tr.r_pad) {
-                const f32x4 *src = reinterpret_cast<const f32x4 *>(
-                    d.v + int64_t(t) * d.ldv + int64_t(p) * d.r_max + j0);
-#pragma unroll
-                for (int i = 0; i < E / 4; ++i) {
-                    const f32x4 s4 = src[i];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) f[4 * i + k] = s4[k];
-                }
+            for (int i = 0; i < P; ++i) {
+                vo[ks][i] = u32x4{0u, 0u, 0u, 0u};
+                const int j = ks * SPAN + q * E;
+                if (pos < d.n_active && j < d.r_max)
+                    vo[ks][i] = *reinterpret_cast<const u32x4 *>(
+                        vp + (i * d.r_max + j) * int(sizeof(T)));
             }
-            vo[ks].set(f);
-        }
-        uint32_t todo = have;
-        for (int idx = 0; todo; ++idx) {
-            const int l = __builtin_ctz(todo);
-            const uint32_t elo = __builtin_amdgcn_readlane(tr.ext_lo, l);
-            const uint32_t ehi = __builtin_amdgcn_readlane(tr.ext_hi, l);
-            const int r_pad = __builtin_amdgcn_readlane(tr.r_pad, l);
-            const bool mine = tr.ext_lo == elo && tr.ext_hi == ehi && tr.r_pad > 0;
-            todo &= ~uint32_t(__builtin_amdgcn_ballot_w64(mine));
-            if (idx % nw != w) continue;
-            const uint64_t off = extent(elo, ehi) + uint64_t(r_pad) * sizeof(T) *
-                                                        uint64_t(d.coef_b[p]);
-            const uint64_t bytes = uint64_t(ho) * uint64_t(r_pad) * sizeof(T);
-            uint32_t range = uint32_t(bytes);
-            if constexpr (kDebug) {
-                if (off + bytes > d.dbg.slab_bytes) {
-                    atomicOr(d.dbg_word, uint32_t(kDbgSlab));
-                    range = 0u;
-                }
-            }
-            const rsrc_t br = make_rsrc(d.slab + off, range);
-            const BLayout bl = b_layout(r_pad, int(sizeof(T)));
-            u32x4 bf[G][KS];
+        for (int g = g0 + w; g <= g1; g += NB * nw) {
+            u32x4 bf[NB][G][KS];
+            int first[NB], end[NB], rp[NB];
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const int o = f0 + (n >> 2) * 4 * G + 4 * j + (n & 3) - lo;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const int v = ks * 4 + q;
-                    bf[j][ks] = bload16(br, off_or_oob(o >= 0 && o < ho && v < bl.nv,
-                                                       b_vec_off(bl, o, v, ho)));
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-                f32x4 s4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    if (ks * SPAN < r_pad) {             // uniform
-#pragma unroll
-                        for (int i = VOperand<T>::kPieces - 1; i >= 0; --i)
-                            s4 = mma<T>(bf[j][ks], vo[ks].piece[i], s4);
+            for (int b = 0; b < NB; ++b) {
+                const int gi = min(g + b * nw, g1);
+                const GroupRow gr = load_invariant(d.groups + gi);
+                first[b] = gr.first;
+                end[b] = g + b * nw <= g1 ? load_invariant(&d.groups[gi + 1].first) : 0;
+                rp[b] = gr.r_pad;
+                const uint64_t off = extent(gr.ext_lo, gr.ext_hi) +
+                                     uint64_t(gr.r_pad) * sizeof(T) * uint64_t(d.coef_b[p]);
+                uint64_t bytes = uint64_t(ho) * uint64_t(gr.r_pad) * sizeof(T);
+                if constexpr (kDebug) {
+                    if (off + bytes > d.dbg.slab_bytes) {
+                        atomicOr(d.dbg_word, uint32_t(kDbgSlab));
+                        bytes = 0;
                     }
+                }
+                const rsrc_t br = make_rsrc(d.slab + off, uint32_t(bytes));
+                const BLayout bl = b_layout(gr.r_pad, int(sizeof(T)));
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[j][i] = mine ? acc[j][i] + tr.scale * s4[i] : acc[j][i];
+                for (int j = 0; j < G; ++j) {
+                    const int o = f0 + (n >> 2) * 4 * G + 4 * j + (n & 3) - lo;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        const int v = ks * 4 + q;
+                        bf[b][j][ks] = bload16(br, off_or_oob(o >= 0 && o < ho && v < bl.nv,
+                                                              b_vec_off(bl, o, v, ho)));
+                    }
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const bool mine = pos >= first[b] && pos < end[b];
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    f32x4 s4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+                        if (ks * SPAN < rp[b]) {         // uniform
+#pragma unroll
+                            for (int i = P - 1; i >= 0; --i)
+                                s4 = mma<T>(bf[b][j][ks], vo[ks][i], s4);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j][i] = mine ? acc[j][i] + s4[i] : acc[j][i];
+                }
             }
         }
     }
@@ -252,7 +296,7 @@ __device__ __forceinline__ int xcd_range(int units) {
 // the same 16 of up); wave w takes its share of K for all of them and all of
 // the up to 16 TT tokens, in batches of F vectors a lane whose loads are in
 // flight while the batch before multiplies.  The waves' sums meet in LDS.
-template <typename T, int TT, bool GLU, bool ADAPT, int NW>
+template <typename T, int TT, bool GLU, int KS, int NW>
 __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs a) {
     constexpr int E = Elem<T>::E, SPAN = 4 * E, NR = GLU ? 2 : 1;
     constexpr int F = TT == 1 ? 4 : 2;
@@ -279,10 +323,14 @@ __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs
     const int s_lo = w * per, s_hi = min(s_lo + per, steps);
 
     f32x4 acc[NR][TT];
+    int tok[TT];                                 // token rows (with adapters: in plan order)
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
+    for (int tt = 0; tt < TT; ++tt) {
+        const int pos = tt * 16 + n;
+        tok[tt] = pos < a.T ? (KS ? a.delta.order[pos] : pos) : -1;
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt) acc[r][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < NR; ++r) acc[r][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 
     struct Batch {
         u32x4 w[NR][F], x[TT][F];
@@ -297,8 +345,8 @@ __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs
                 b.w[r][f] = bload16_nt(wr[r], off_or_oob(ok && n < rows, uint32_t(n) * wrow + kq));
 #pragma unroll
             for (int tt = 0; tt < TT; ++tt)
-                b.x[tt][f] = bload16(xr, off_or_oob(ok && tt * 16 + n < a.T,
-                                                    uint32_t(tt * 16 + n) * xrow + kq));
+                b.x[tt][f] = bload16(xr, off_or_oob(ok && tok[tt] >= 0,
+                                                    uint32_t(tok[tt]) * xrow + kq));
         }
     };
     auto multiply = [&](const Batch &b) {
@@ -311,13 +359,13 @@ __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs
     };
     Batch b0, b1;
     load(b0, s_lo);
-    if constexpr (ADAPT) {
+    if constexpr (KS > 0) {
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
             for (int tt = 0; tt < TT; ++tt) {
                 f32x4 d[1] = {acc[r][tt]};
-                add_delta<T, 1>(a.delta, a.T, tt * 16, r * a.n + f0, w, NW, d);
+                add_delta<T, 1, KS>(a.delta, tt * 16, r * a.n + f0, w, NW, d);
                 acc[r][tt] = d[0];
             }
     }
@@ -342,7 +390,10 @@ __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[r][i] = s4[i];
         }
-        finish<T, GLU>(a, w * 16 + n, f0 + 4 * q, v[0], v[NR - 1]);
+        int t = tok[0];
+#pragma unroll
+        for (int tt = 1; tt < TT; ++tt) t = w == tt ? tok[tt] : t;
+        finish<T, GLU>(a, t, f0 + 4 * q, v[0], v[NR - 1]);
     }
 }
 
@@ -369,6 +420,113 @@ __device__ __forceinline__ u32x4 raw_rsrc(const void *base, uint32_t bytes) {
                  uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(p >> 32) & 0xffffu)),
                  uint32_t(__builtin_amdgcn_readfirstlane(bytes)), uint32_t(kRsrcWord3)};
 }
+
+// One K tile of the delta as a lane copies it.
+struct DeltaTile {
+    BLayout bl;
+    uint64_t off;                // B block in the slab
+    uint32_t bytes;
+    uint32_t voff;               // the lane's vector in a position's operand row
+    int vrow;                    // bytes of such a row
+    int first, end;              // positions of the group
+    int col0, h_out;             // row of B of the tile's first output
+    int vec;                     // the lane's vector of a B row
+    int half;                    // 1: gate (or all), 2: up
+    bool ok;                     // the lane has a vector
+};
+
+// What a stage of the delta holds: the half of W's rows (1: gate, or all; 2:
+// up; 0: nothing) and the group's positions.
+struct DeltaHeld {
+    int half, first, end;
+};
+
+// The walk over a tile's delta K tiles: groups, projections, halves, then the
+// 8-vector steps of pieces x vectors.  All of it is uniform.
+template <typename T, int HALVES> struct DeltaTiles {
+    static constexpr int P = VOperand<T>::kPieces;
+    int g, g1, p, h, s, first, end, f0, feat, n;
+    GroupRow gr;
+
+    __device__ __forceinline__ int steps() const {
+        return (P * (gr.r_pad * int(sizeof(T)) / 16) + 7) / 8;
+    }
+    __device__ __forceinline__ bool meets(const DeltaArgs &d) const {
+        const int c0 = h * n + f0, lo = d.y_off[p];
+        return c0 < lo + d.h_out[p] && c0 + feat > lo;
+    }
+    __device__ __forceinline__ void load(const DeltaArgs &d) {
+        gr = load_invariant(d.groups + g);
+        first = gr.first;
+        end = load_invariant(&d.groups[g + 1].first);
+    }
+    // on to the first (projection, half) from the current one that the tile meets
+    __device__ __forceinline__ void settle(const DeltaArgs &d) {
+        while (g <= g1 && !meets(d)) {
+            if (++h < HALVES) continue;
+            h = 0;
+            if (++p < d.nproj) continue;
+            p = 0;
+            if (++g <= g1) load(d);
+        }
+    }
+    __device__ __forceinline__ void start(const DeltaArgs &d, int t0, int rows, int f0_, int feat_,
+                                          int n_) {
+        f0 = f0_;
+        feat = feat_;
+        n = n_;
+        p = h = s = 0;
+        const int last = min(t0 + rows, d.n_active) - 1;
+        g = 1;
+        g1 = 0;
+        bool any = false;                        // a tile that meets no projection has no walk
+        for (int i = 0; i < d.nproj; ++i)
+            for (int k = 0; k < HALVES; ++k)
+                any |= k * n + f0 < d.y_off[i] + d.h_out[i] && k * n + f0 + feat > d.y_off[i];
+        if (last < t0 || !any) return;
+        g = load_invariant(d.pos_group + t0);
+        g1 = load_invariant(d.pos_group + last);
+        load(d);
+        settle(d);
+    }
+    // what the current tile is; past the end one without vectors
+    __device__ __forceinline__ DeltaTile tile(const DeltaArgs &d, uint32_t vec) const {
+        DeltaTile e{};
+        e.vrow = d.nproj * P * d.r_max * int(sizeof(T));
+        if (g > g1) return e;
+        e.bl = b_layout(gr.r_pad, int(sizeof(T)));
+        e.off = extent(gr.ext_lo, gr.ext_hi) + uint64_t(gr.r_pad) * sizeof(T) * uint64_t(d.coef_b[p]);
+        e.h_out = d.h_out[p];
+        e.bytes = uint32_t(e.h_out) * uint32_t(gr.r_pad) * uint32_t(sizeof(T));
+        if constexpr (kDebug) {
+            if (e.off + e.bytes > d.dbg.slab_bytes) {
+                atomicOr(d.dbg_word, uint32_t(kDbgSlab));
+                e.bytes = 0;
+            }
+        }
+        const int at = s * 8 + int(vec), piece = at / e.bl.nv;
+        e.vec = at - piece * e.bl.nv;
+        e.ok = piece < P;
+        e.voff = uint32_t(((p * P + piece) * d.r_max) * int(sizeof(T)) + e.vec * 16);
+        e.first = first;
+        e.end = end;
+        e.col0 = h * n + f0 - d.y_off[p];
+        e.half = h + 1;
+        return e;
+    }
+    __device__ __forceinline__ void next(const DeltaArgs &d) {
+        if (g > g1 || ++s < steps()) return;
+        s = 0;
+        if (++h == HALVES) {
+            h = 0;
+            if (++p == d.nproj) {
+                p = 0;
+                if (++g <= g1) load(d);
+            }
+        }
+        settle(d);
+    }
+};
 
 // One workgroup per BT tokens x BN rows of W (with a gated pair BN / 2 of
 // gate and the same BN / 2 of up), WT x WN waves, over the K tiles of its
@@ -402,47 +560,83 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
     const uint32_t kb = uint32_t(a.k) * sizeof(T);
 
     const int xrows = min(BT, a.T - t0), wrows = min(FEAT, wide - f0);
-    const u32x4 xr = raw_rsrc(a.x + int64_t(t0) * xrow, uint32_t(xrows - 1) * xrow + kb);
+    // with adapters x's rows are gathered in plan order (x spans at most 2 GiB)
+    const u32x4 xr = ADAPT ? raw_rsrc(a.x, uint32_t(a.T - 1) * xrow + kb)
+                           : raw_rsrc(a.x + int64_t(t0) * xrow, uint32_t(xrows - 1) * xrow + kb);
     const u32x4 wr = raw_rsrc(a.w + int64_t(f0) * wrow, uint32_t(wrows - 1) * wrow + kb);
     const u32x4 wr2 = GLU ? raw_rsrc(a.w + (int64_t(a.n) + f0) * wrow,
                                      uint32_t(wrows - 1) * wrow + kb) : wr;
 
-    // this lane's copies: the row and the vector of the row each brings in
-    uint32_t xo[XL], wo[WL], xc[XL], wc[WL];
+    // this lane's copies: the rows, and the vector of them (the same for all:
+    // its copies are a multiple of 16 rows apart)
+    static_assert(NTH / 8 % 16 == 0, "one vector index a lane");
+    const uint32_t vec = uint32_t((tid & 7) ^ ((tid >> 4) & 7));
+    uint32_t xo[XL], wo[WL];
+    int wf[WL];                                              // output of the row, from f0
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
         const int row = (i * NTH + tid) >> 3;
-        xc[i] = uint32_t((tid & 7) ^ ((row >> 1) & 7)) * 16u;
-        xo[i] = row < xrows ? uint32_t(row) * xrow + xc[i] : kOOB;
+        const int t = ADAPT && row < xrows ? a.delta.order[t0 + row] : row;
+        xo[i] = row < xrows ? uint32_t(t) * xrow + vec * 16u : kOOB;
     }
 #pragma unroll
     for (int i = 0; i < WL; ++i) {
         const int row = (i * NTH + tid) >> 3;
-        wc[i] = uint32_t((tid & 7) ^ ((row >> 1) & 7)) * 16u;
         const int share = row / (16 * TJ), j = row / 16 % TJ, r = row % 16;
-        const int f = share * 16 * G + (r >> 2) * 4 * G + (j % G) * 4 + (r & 3);
-        wo[i] = f < wrows ? uint32_t(f) * wrow + wc[i] : kOOB;
+        wf[i] = share * 16 * G + (r >> 2) * 4 * G + (j % G) * 4 + (r & 3);
+        wo[i] = wf[i] < wrows ? uint32_t(wf[i]) * wrow + vec * 16u : kOOB;
     }
     const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) uint8_t *)lds));
     const int nk = (int(kb) + kKBytes - 1) / kKBytes;
     const int k_lo = SPLIT ? z * a.k_tiles : 0, k_hi = SPLIT ? min(k_lo + a.k_tiles, nk) : nk;
 
-    // copies of K tile kt into stage st; past the split's end, and past the
-    // row's end in its last tile, lanes are out of range
-    auto fetch = [&](int kt, int st) {
-        const uint32_t soff = uint32_t(kt) * kKBytes;
-        const uint32_t left = kt < k_hi ? kb - soff : 0u;     // bytes of the row from here
+    auto up_rows = [&](int i) {                              // uniform
+        return GLU && ((i * NTH + wave * 64) / 8 / 16) % TJ >= G;
+    };
+    // copy `at` of K tile kt into stage st; in a row's last tile, lanes past
+    // its end, and past the last tile all lanes, are out of range
+    auto fetch_one = [&](int kt, int st, auto index) {
+        constexpr int at = decltype(index)::value;
         const uint32_t base = lds0 + uint32_t(st * STAGE) + uint32_t(wave) * 1024u;
+        const uint32_t soff = uint32_t(kt) * kKBytes;
+        const bool in = kt < k_hi && vec * 16u < kb - soff;
+        if constexpr (at < XL)
+            copy_to_lds(xr, in ? xo[at] : kOOB, soff, base + uint32_t(at * NTH * 16));
+        else
+            copy_to_lds(up_rows(at - XL) ? wr2 : wr, in ? wo[at - XL] : kOOB, soff,
+                        base + uint32_t(BT * kKBytes + (at - XL) * NTH * 16));
+    };
+    auto fetch = [&](int kt, int st) {
+        each<XL + WL>([&](auto at) { fetch_one(kt, st, at); });
+    };
+    // The delta as further K tiles: for each adapter group among the tile's
+    // positions and each projection among its columns, the columns are the
+    // group's operand, piece after piece (zero for other groups' positions),
+    // against B's rows, repeated for each piece.  With a gated pair a tile
+    // belongs to one half.
+    auto fetch_delta = [&](auto &dt, int st) -> DeltaHeld {
+        const uint32_t base = lds0 + uint32_t(st * STAGE) + uint32_t(wave) * 1024u;
+        const DeltaArgs &d = a.delta;
+        const DeltaTile e = dt.tile(d, vec);
+        const u32x4 vr = raw_rsrc(d.v + int64_t(t0) * e.vrow, uint32_t(xrows) * uint32_t(e.vrow));
+        const u32x4 br = raw_rsrc(d.slab + e.off, e.bytes);
 #pragma unroll
-        for (int i = 0; i < XL; ++i)
-            copy_to_lds(xr, xc[i] < left ? xo[i] : kOOB, soff, base + uint32_t(i * NTH * 16));
+        for (int i = 0; i < XL; ++i) {
+            const int row = (i * NTH + tid) >> 3;
+            const bool in = e.ok && t0 + row >= e.first && t0 + row < e.end;
+            copy_to_lds(vr, in ? uint32_t(row) * uint32_t(e.vrow) + e.voff : kOOB, 0u,
+                        base + uint32_t(i * NTH * 16));
+        }
 #pragma unroll
         for (int i = 0; i < WL; ++i) {
-            const bool up = GLU && ((i * NTH + wave * 64) / 8 / 16) % TJ >= G;   // uniform
-            copy_to_lds(up ? wr2 : wr, wc[i] < left ? wo[i] : kOOB, soff,
+            const int o = e.col0 + wf[i];
+            const bool in = e.ok && (!GLU || up_rows(i) == (e.half == 2)) && o >= 0 && o < e.h_out;
+            copy_to_lds(br, in ? b_vec_off(e.bl, o, e.vec, e.h_out) : kOOB, 0u,
                         base + uint32_t(BT * kKBytes + i * NTH * 16));
         }
+        dt.next(d);
+        return DeltaHeld{e.half, e.first, e.end};
     };
 
     f32x4 acc[TI][TJ];
@@ -456,62 +650,142 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
     for (int kk = 0; kk < 2; ++kk)
         fo[kk] = uint32_t(n) * kKBytes + uint32_t((kk * 4 + q) ^ ((n >> 1) & 7)) * 16u;
 
+    auto x_frag = [&](int st, int i, int kk) {
+        return *reinterpret_cast<const u32x4 *>(lds + st * STAGE + (wt * TI + i) * 16 * kKBytes +
+                                                fo[kk]);
+    };
+    auto w_frag = [&](int st, int j, int kk) {
+        return *reinterpret_cast<const u32x4 *>(lds + st * STAGE + BT * kKBytes +
+                                                (wn * TJ + j) * 16 * kKBytes + fo[kk]);
+    };
+    struct Frags {
+        u32x4 f[TJ + TI];                        // W's row tiles, then x's token tiles
+    };
+    auto read = [&](Frags &f, int st, int kk, auto index) {
+        constexpr int r = decltype(index)::value;
+        if constexpr (r < TJ) f.f[r] = w_frag(st, r, kk);
+        else f.f[r] = x_frag(st, r - TJ, kk);
+    };
+    // One half of a K tile: the products of `use` in groups of 4, and between
+    // the groups the reads of the next half's fragments into `next` (early,
+    // so that they have arrived at the half's end) and `copies` of the ND
+    // copies of a stage to come.  Spelled out and pinned, because a wave may
+    // be alone on its SIMD: what it issues in one go, its matrix core waits for.
+    constexpr int NM = TI * TJ, MG = NM >= 4 ? 4 : NM, NS = NM / MG, NR = TI + TJ, ND = XL + WL;
+    constexpr int RPS = (NR + (NS + 1) / 2 - 1) / ((NS + 1) / 2), DPS = (ND + NS - 1) / NS;
+    auto half = [&](const Frags &use, Frags &next, int st, int kk, auto with_copies, int kt,
+                    int st_in) {
+        each<NS>([&](auto step) {
+            constexpr int s = decltype(step)::value;
+            each<RPS>([&](auto r) {
+                constexpr int at = s * RPS + decltype(r)::value;
+                if constexpr (at < NR) read(next, st, kk, std::integral_constant<int, at>{});
+            });
+            if constexpr (decltype(with_copies)::value)
+                each<DPS>([&](auto r) {
+                    constexpr int at = s * DPS + decltype(r)::value;
+                    if constexpr (at < ND) fetch_one(kt, st_in, std::integral_constant<int, at>{});
+                });
+            each<MG>([&](auto m) {
+                constexpr int at = s * MG + decltype(m)::value, i = at / TJ, j = at % TJ;
+                acc[i][j] = mma<T>(use.f[j], use.f[TJ + i], acc[i][j]);
+            });
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    // acc += a stage of one group's delta, in the columns of its positions
+    // only: other positions' tiles are passed over, and in a tile that holds
+    // both, a sum apart is kept or dropped by column (zeros in the operand
+    // would not do: an infinite or NaN adapter times zero is NaN)
+    auto multiply_delta = [&](int st, const DeltaHeld &e) {
+        each<TI>([&](auto index) {
+            constexpr int i = decltype(index)::value;
+            const int p0 = t0 + (wt * TI + i) * 16;
+            if (p0 >= e.end || p0 + 16 <= e.first) return;   // uniform
+            const bool mine = p0 + n >= e.first && p0 + n < e.end;
+            const u32x4 x0 = x_frag(st, i, 0), x1 = x_frag(st, i, 1);
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s) fetch(k_lo + s, s);
-    int st = 0, st_in = S - 1;
+            for (int j = 0; j < G; ++j) {
+                f32x4 s4 = mma<T>(w_frag(st, (e.half - 1) * G + j, 0), x0, f32x4{0.f, 0.f, 0.f, 0.f});
+                s4 = mma<T>(w_frag(st, (e.half - 1) * G + j, 1), x1, s4);
+                // (both halves by selects: a branch would turn the
+                // accumulators into memory)
+                const bool lower = mine && e.half == 1, upper = mine && e.half == 2;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    acc[i][j][k] = lower ? acc[i][j][k] + s4[k] : acc[i][j][k];
+                    if constexpr (GLU)
+                        acc[i][TJ - G + j][k] = upper ? acc[i][TJ - G + j][k] + s4[k]
+                                                      : acc[i][TJ - G + j][k];
+                }
+            }
+        });
+    };
+    int st = 0;
+    // Every LDS read runs under a half's products: the second half's
+    // fragments are read while the first multiplies, the next stage's first
+    // half while the second does; the one barrier of a K tile stands between,
+    // when this wave has its second half in registers, and frees the stage
+    // for the copies of K tile kt + S.
+    Frags fa, fb;
+#pragma unroll
+    for (int s = 0; s < S; ++s) fetch(k_lo + s, s);
+    wait_copies<(S - 1) * (XL + WL)>();
+    __builtin_amdgcn_s_barrier();
+    each<NR>([&](auto r) { read(fa, 0, 0, r); });
     for (int kt = k_lo; kt < k_hi; ++kt) {
-        wait_copies<(S - 2) * (XL + WL)>();      // this stage's copies, in order
-        __builtin_amdgcn_s_barrier();            // everyone's; stage st_in is free
-        fetch(kt + S - 1, st_in);
-        const uint8_t *xs = lds + st * STAGE + wt * (TI * 16 * kKBytes);
-        const uint8_t *ws = lds + st * STAGE + BT * kKBytes + wn * (TJ * 16 * kKBytes);
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            u32x4 xf[TI], wf[TJ];
-#pragma unroll
-            for (int j = 0; j < TJ; ++j)
-                wf[j] = *reinterpret_cast<const u32x4 *>(ws + j * 16 * kKBytes + fo[kk]);
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-                xf[i] = *reinterpret_cast<const u32x4 *>(xs + i * 16 * kKBytes + fo[kk]);
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-#pragma unroll
-                for (int j = 0; j < TJ; ++j) acc[i][j] = mma<T>(wf[j], xf[i], acc[i][j]);
-        }
-        wait_lds();                              // this wave has read the stage
+        half(fa, fb, st, 1, std::false_type{}, 0, 0);
+        wait_copies<(S - 2) * (XL + WL)>();      // the next stage's copies, in order
+        wait_lds();
+        __builtin_amdgcn_s_barrier();
+        const int free = st;
         st = st + 1 == S ? 0 : st + 1;
-        st_in = st_in + 1 == S ? 0 : st_in + 1;
+        half(fb, fa, st, 0, std::true_type{}, kt + S, free);
+    }
+    if constexpr (ADAPT) {
+        DeltaTiles<T, GLU ? 2 : 1> dt;
+        dt.start(a.delta, t0, min(BT, xrows), f0, FEAT, a.n);
+        wait_copies<0>();
+        wait_lds();
+        __builtin_amdgcn_s_barrier();            // every stage is free
+        DeltaHeld held[S];                       // the stages to come, in order
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s) held[s] = fetch_delta(dt, s);
+        int st_in = S - 1;
+        st = 0;
+        while (held[0].half) {                   // uniform
+            wait_copies<(S - 2) * (XL + WL)>();
+            __builtin_amdgcn_s_barrier();
+            held[S - 1] = fetch_delta(dt, st_in);
+            multiply_delta(st, held[0]);
+            wait_lds();
+#pragma unroll
+            for (int s = 0; s < S - 1; ++s) held[s] = held[s + 1];
+            st = st + 1 == S ? 0 : st + 1;
+            st_in = st_in + 1 == S ? 0 : st_in + 1;
+        }
     }
     wait_copies<0>();                            // none may land after the workgroup's end
 
     const int fw = f0 + wn * 16 * G;             // the wave's first output
     each<TI>([&](auto index) {                   // accumulators need constant indexes
         constexpr int i = decltype(index)::value;
-        const int ti = t0 + (wt * TI + i) * 16, t = ti + n;
+        const int ti = t0 + (wt * TI + i) * 16, pos = ti + n;
         if (ti >= a.T) return;                   // uniform
         if constexpr (SPLIT) {
-            if (t < a.T) {
-                float *p = a.partial + (int64_t(z) * a.T + t) * a.ldp + fw + q * 4 * G;
+            if (pos < a.T) {
+                float *p = a.partial + (int64_t(z) * a.T + pos) * a.ldp + fw + q * 4 * G;
 #pragma unroll
                 for (int j = 0; j < TJ; ++j)
                     if (fw + q * 4 * G + 4 * j < a.ldp) *reinterpret_cast<f32x4 *>(p + 4 * j) = acc[i][j];
             }
         } else {
-            f32x4 g[G], u[G];
+            const int t = pos < a.T ? (ADAPT ? a.delta.order[pos] : pos) : -1;
 #pragma unroll
             for (int j = 0; j < G; ++j) {
-                g[j] = acc[i][j];
-                u[j] = acc[i][TJ - G + j];
-            }
-            if constexpr (ADAPT) {
-                add_delta<T, G>(a.delta, a.T, ti, fw, 0, 1, g);
-                if constexpr (GLU) add_delta<T, G>(a.delta, a.T, ti, a.n + fw, 0, 1, u);
-            }
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-                float v[4] = {g[j][0], g[j][1], g[j][2], g[j][3]};
-                float v2[4] = {u[j][0], u[j][1], u[j][2], u[j][3]};
+                const f32x4 g = acc[i][j], u = acc[i][TJ - G + j];
+                float v[4] = {g[0], g[1], g[2], g[3]};
+                float v2[4] = {u[0], u[1], u[2], u[3]};
                 finish<T, GLU>(a, t, fw + q * 4 * G + 4 * j, v, v2);
             }
         }
@@ -523,7 +797,7 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
 // partial products w, w + 4, ... and the deltas of every fourth adapter, the
 // waves' sums meet in LDS, and each wave finishes 4 tokens (a row of 64
 // outputs is one contiguous store).
-template <typename T, bool GLU, bool ADAPT>
+template <typename T, bool GLU, int KS>
 __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
     constexpr int NR = GLU ? 2 : 1, G = 4;
     __shared__ f32x4 red[4][NR * G][kWaveSize];
@@ -532,7 +806,8 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
     const int w = wave_id();
     const int tiles_t = (a.T + 15) / 16;
     const int t0 = unit % tiles_t * 16, f0 = unit / tiles_t * 64;
-    const int t = t0 + n;
+    auto token = [&](int pos) { return pos < a.T ? (KS ? a.delta.order[pos] : pos) : -1; };
+    const int t = token(t0 + n);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         const int c0 = r * a.n + f0;             // column before the activation
@@ -543,13 +818,13 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
             const float *p = a.partial + (int64_t(z) * a.T + t) * a.ldp + c0 + q * 16;
 #pragma unroll
             for (int j = 0; j < G; ++j)
-                if (t < a.T && c0 + q * 16 + 4 * j < a.wide) {
+                if (t >= 0 && c0 + q * 16 + 4 * j < a.wide) {
                     // (any alignment: the second half of a pair starts at column n)
                     const u32x4 v = *reinterpret_cast<const u32x4_any *>(p + 4 * j);
                     s[j] += __builtin_bit_cast(f32x4, v);
                 }
         }
-        if constexpr (ADAPT) add_delta<T, G>(a.delta, a.T, t0, c0, w, 4, s);
+        if constexpr (KS > 0) add_delta<T, G, KS>(a.delta, t0, c0, w, 4, s);
 #pragma unroll
         for (int j = 0; j < G; ++j) red[w][r * G + j][lane] = s[j];
     }
@@ -566,19 +841,36 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[r][i] = s4[i];
     }
-    finish<T, GLU>(a, t0 + tok, f0 + 4 * m, v[0], v[NR - 1]);
+    finish<T, GLU>(a, token(t0 + tok), f0 + 4 * m, v[0], v[NR - 1]);
 }
 
 // ------------------------------------------------------------- launches -----
 dim3 grid_of(int units) { return dim3((units + kXcds - 1) / kXcds * kXcds); }
 
+// K-steps of the delta's largest rank, as the kernels are built for it
+template <typename T> int delta_steps(const LinearArgs &a) {
+    if (!a.delta.order) return 0;
+    return a.delta.max_rpad <= 4 * Elem<T>::E ? 1 : LORA_MAX_RANK / (4 * Elem<T>::E);
+}
+
 template <typename T, int TT, bool GLU, int NW>
 hipError_t rows_launch(const LinearArgs &a, hipStream_t s) {
-    if (a.delta.rows)
-        hipLaunchKernelGGL((k_linear_rows<T, TT, GLU, true, NW>), grid_of(a.units), dim3(NW * 64), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_linear_rows<T, TT, GLU, false, NW>), grid_of(a.units), dim3(NW * 64), 0, s, a);
+    constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E);
+    const dim3 grid = grid_of(a.units), block(NW * 64);
+    const int ks = delta_steps<T>(a);
+    if (ks == 0) hipLaunchKernelGGL((k_linear_rows<T, TT, GLU, 0, NW>), grid, block, 0, s, a);
+    else if (ks == 1) hipLaunchKernelGGL((k_linear_rows<T, TT, GLU, 1, NW>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_linear_rows<T, TT, GLU, KM, NW>), grid, block, 0, s, a);
     return hipGetLastError();
+}
+
+template <typename T, bool GLU> void join_launch(const LinearArgs &a, hipStream_t s) {
+    constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E);
+    const dim3 grid(((a.T + 15) / 16) * ((a.n + 63) / 64)), block(256);
+    const int ks = delta_steps<T>(a);
+    if (ks == 0) hipLaunchKernelGGL((k_linear_join<T, GLU, 0>), grid, block, 0, s, a);
+    else if (ks == 1) hipLaunchKernelGGL((k_linear_join<T, GLU, 1>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_linear_join<T, GLU, KM>), grid, block, 0, s, a);
 }
 
 template <typename T, bool GLU>
@@ -590,19 +882,13 @@ hipError_t rows_dispatch(const LinearPlan &pl, const LinearArgs &a, hipStream_t 
 template <typename T, int BT, int BN, int WT, int WN, int S>
 hipError_t tile_launch(const LinearPlan &pl, bool glu, const LinearArgs &a, hipStream_t s) {
     const dim3 grid = grid_of(a.units), block(WT * WN * 64);
-    const bool adapt = a.delta.rows != nullptr;
+    const bool adapt = a.delta.order != nullptr;
     if (pl.splits > 1) {
         hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, true, false>), grid, block, 0, s, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        const dim3 jgrid(((a.T + 15) / 16) * ((a.n + 63) / 64)), jblock(256);
-        if (glu) {
-            if (adapt) hipLaunchKernelGGL((k_linear_join<T, true, true>), jgrid, jblock, 0, s, a);
-            else hipLaunchKernelGGL((k_linear_join<T, true, false>), jgrid, jblock, 0, s, a);
-        } else {
-            if (adapt) hipLaunchKernelGGL((k_linear_join<T, false, true>), jgrid, jblock, 0, s, a);
-            else hipLaunchKernelGGL((k_linear_join<T, false, false>), jgrid, jblock, 0, s, a);
-        }
+        if (glu) join_launch<T, true>(a, s);
+        else join_launch<T, false>(a, s);
     } else if (glu) {
         if (adapt) hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, true, false, true>), grid, block, 0, s, a);
         else hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, true, false, false>), grid, block, 0, s, a);
@@ -625,6 +911,14 @@ hipError_t linear_dispatch(const LinearPlan &pl, bool glu, const LinearArgs &a, 
 }
 
 }  // namespace
+
+hipError_t launch_operand(int dtype, const OperandArgs &a, hipStream_t s) {
+    if (a.nb <= 0) return hipSuccess;
+    const dim3 grid(a.nb * a.nproj), block(256);
+    if (dtype == LORA_BF16) hipLaunchKernelGGL(k_operand<uint16_t>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(k_operand<float>, grid, block, 0, s, a);
+    return hipGetLastError();
+}
 
 hipError_t launch_linear(int dtype, const LinearPlan &pl, bool glu, LinearArgs a, hipStream_t s) {
     if (a.T <= 0) return hipSuccess;

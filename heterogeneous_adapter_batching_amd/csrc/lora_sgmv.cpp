@@ -165,6 +165,7 @@ struct PlanCounts {
     int64_t T = 0, nb = 0, rt = 0, mb = 0;   // rows (tokens, or (token, slot) rows), blocks,
     int32_t tt = 1;                          // rank tiles, merge blocks; tiles per block
     bool merge = false;                      // a merge plan (its shrink covers every tile)
+    int64_t ng = 0;                          // adapter groups
     int64_t rt_long = 0;                     // a plain plan: rank tiles of long groups
     int64_t long_rows = 0;                   // ... and rows of the long groups' v region
 };
@@ -172,7 +173,8 @@ struct PlanCounts {
 // Byte offsets of the tables in a plan workspace, and its size.
 struct PlanLayout {
     uint64_t off_tok = 0, off_blocks = 0, off_tiles = 0, off_btok = 0, off_ttok = 0, off_tsig = 0,
-             off_tw = 0, off_mblocks = 0, off_trow = 0, off_part = 0;
+             off_tw = 0, off_mblocks = 0, off_groups = 0, off_pgroup = 0,
+             off_part = 0;
     uint64_t off_lv = 0;   // long groups' v rows, from off_part (plain plans)
     uint64_t image_bytes = 0, part_bytes = 0, ws_bytes = 0;
 };
@@ -222,7 +224,8 @@ PlanLayout plan_layout(const lora_pool_desc &d, const PlanCounts &c, int32_t mp,
     L.off_tsig = o;    o = round_up(o + 4ull * T, 256);
     L.off_tw = o;      o = round_up(o + 4ull * T, 256);
     L.off_mblocks = o; o = round_up(o + sizeof(lora::MergeBlock) * uint64_t(c.mb), 256);
-    L.off_trow = o;    o = round_up(o + sizeof(lora::TokenRow) * T, 256);
+    L.off_groups = o;  o = round_up(o + sizeof(lora::GroupRow) * uint64_t(c.ng + 1), 256);
+    L.off_pgroup = o;  o = round_up(o + 4ull * T, 256);
     L.image_bytes = o;
     // the shrink's partial tiles: every rank tile at the plan's tiles per
     // block (a merge plan), or the short groups' tiles at one 16-token tile
@@ -253,7 +256,10 @@ struct lora_plan {
     std::vector<int32_t> token_order;    // plan order: grouped adapter tokens, then the rest
     std::vector<int32_t> token_sigma;    // core index per plan-order row (-1: none)
     std::vector<float> token_weight;     // weight per plan-order row (weighted plans)
-    std::vector<lora::TokenRow> token_rows;  // per token row (a merge plan's are not read)
+    // the adapter groups and each plan position's (-1: none), for the product
+    // with adapters
+    std::vector<lora::GroupRow> group_rows{lora::GroupRow{0u, 0u, 0, 0}};
+    std::vector<int32_t> position_group;
     std::vector<int32_t> token_slot;     // merge slot per plan-order row (-1: none)
     bool weighted = false;
     int32_t merge_k = 0;                 // slots per segment of a merge plan (0: not one)
@@ -306,6 +312,7 @@ struct lora_plan {
         c.T = rows();
         c.mb = int64_t(mblocks.size());
         c.nb = nb_all();
+        c.ng = int64_t(group_rows.size()) - 1;
         c.rt = rt_total();
         c.tt = tt;
         c.merge = merge_k > 0;
@@ -702,7 +709,8 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
     pl->max_rpad_long = pl->min_rpad_long = 0;
     pl->tt = 1;
     pl->token_group.assign(T, -1);
-    pl->token_rows.assign(T, lora::TokenRow{0u, 0u, 0, 0.f});
+    pl->group_rows.clear();
+    pl->position_group.clear();
 
     // groups in first-appearance order (runs with rows only); a member is a
     // (row, run) pair
@@ -755,6 +763,9 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
     auto add_group = [&](const std::vector<std::pair<int32_t, int32_t>> &rows, int32_t g,
                          const Slot *sl) {
         const int32_t base = int32_t(pl->token_order.size());
+        pl->group_rows.push_back(lora::GroupRow{sl ? uint32_t(sl->off & 0xffffffffu) : 0u,
+                                                sl ? uint32_t(sl->off >> 32) : 0u,
+                                                sl ? sl->r_pad : 0, base});
         const int32_t rt = sl ? (sl->r_pad + lora::kTile - 1) / lora::kTile : 0;
         const bool lg = sl && use_long && rows.size() >= long_group;
         const int32_t smax = lg ? lora::kMaxBlockTokens : lora::kTile;
@@ -800,10 +811,7 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
             pl->token_sigma.push_back(rn ? rn->sigma : -1);
             pl->token_weight.push_back(rn ? rn->weight : 1.0f);
             pl->token_slot.push_back(rn ? rn->slot : -1);
-            if (sl)
-                pl->token_rows[m.first] =
-                    lora::TokenRow{uint32_t(sl->off & 0xffffffffu), uint32_t(sl->off >> 32),
-                                   sl->r_pad, sl->scale * (rn ? rn->weight : 1.0f)};
+            pl->position_group.push_back(sl ? g : -1);
             if (rn) pl->max_sigma = std::max(pl->max_sigma, rn->sigma);
         }
     };
@@ -1053,6 +1061,7 @@ uint64_t lora_workspace_bytes(const lora_pool *p, int32_t num_tokens, int32_t nu
     PlanCounts c;
     c.T = T;
     c.nb = T;
+    c.ng = std::min<int64_t>(num_segs, T);
     const int64_t sblocks = std::min<int64_t>(T, T / lora::kTile + 1 + std::min<int64_t>(num_segs, T));
     c.rt = sblocks * ((p->d.r_max + lora::kTile - 1) / lora::kTile);
     c.tt = long_ok ? lora::kMaxBlockTokens / lora::kTile : 1;
@@ -1097,8 +1106,9 @@ lora_status lora_plan_upload(lora_plan *pl, void *ws, uint64_t ws_bytes, int32_t
     if (R) std::memcpy(img + lay.off_tok, pl->token_order.data(), 4ull * R);
     if (R) std::memcpy(img + lay.off_tsig, pl->token_sigma.data(), 4ull * R);
     if (R && pl->weighted) std::memcpy(img + lay.off_tw, pl->token_weight.data(), 4ull * R);
-    if (pl->T)
-        std::memcpy(img + lay.off_trow, pl->token_rows.data(), sizeof(lora::TokenRow) * pl->T);
+    std::memcpy(img + lay.off_groups, pl->group_rows.data(),
+                sizeof(lora::GroupRow) * pl->group_rows.size());
+    if (R) std::memcpy(img + lay.off_pgroup, pl->position_group.data(), 4ull * R);
     if (!pl->mblocks.empty())
         std::memcpy(img + lay.off_mblocks, pl->mblocks.data(),
                     sizeof(lora::MergeBlock) * pl->mblocks.size());
@@ -1664,9 +1674,46 @@ lora_status fused_body(const lora_pool *p, const lora_plan *pl, int32_t layer, i
                       cores, &pt);
 }
 
-// The v rows of a product call with adapters, ahead of its partial products.
-uint64_t linear_v_bytes(const lora_pool *p, int32_t T, int32_t nproj) {
-    return round_up(4ull * uint64_t(T) * uint64_t(nproj) * uint64_t(p->d.r_max), 256);
+// A region of T rows of nproj * r_max entries in a product call's workspace.
+uint64_t linear_v_bytes(const lora_pool *p, int32_t T, int32_t nproj, int32_t entry) {
+    return round_up(uint64_t(entry) * uint64_t(T) * uint64_t(nproj) * uint64_t(p->d.r_max), 256);
+}
+
+// The product's right operand of the delta: scale * (A x) of every plan
+// position with an adapter (short groups from the shrink's partials, long
+// ones from the prompt kernel's v).
+lora_status run_operand(const lora_pool *p, const lora_plan *pl, int32_t layer, int32_t nproj,
+                        const int32_t *projs, const void *x, int64_t ldx, const CallCheck &cc,
+                        float *v, uint8_t *operand, hipStream_t hs) {
+    lora::OperandArgs a{};
+    const Partials pt = workspace_partials(pl);
+    lora_status st = run_shrink(p, pl, layer, nproj, projs, x, ldx, cc, hs, &a.c0, pt);
+    if (st != LORA_OK) return st;
+    pl->part_long = false;
+    PrefillIO io;
+    io.mode = lora::kPrefillShrink;
+    io.x = x;
+    io.ldx = ldx;
+    io.v = v;
+    io.ldv = int64_t(nproj) * p->d.r_max;
+    io.v_by_pos = true;
+    st = run_prefill(p, pl, layer, nproj, projs, nullptr, cc, io, hs);
+    if (st != LORA_OK) return st;
+    const uint8_t *ws = static_cast<const uint8_t *>(pl->ws);
+    a.blocks = reinterpret_cast<const BlockDesc *>(ws + pl->lay.off_blocks);
+    a.partial = pt.ptr;
+    a.partial_bytes = uint32_t(std::min<uint64_t>(pt.bytes, lora::kMaxTensorBytes));
+    a.v = v;
+    a.tok_w = pl->weighted ? reinterpret_cast<const float *>(ws + pl->lay.off_tw) : nullptr;
+    a.out = operand;
+    a.nb = pl->nb_act;
+    a.nb_long = pl->nb_long;
+    a.nproj = nproj;
+    a.r_max = p->d.r_max;
+    a.dbg = debug_bounds(p, pl);
+    const hipError_t e = lora::launch_operand(p->d.dtype, a, hs);
+    if (e != hipSuccess) return hip_fail(e, "product operand launch");
+    return LORA_OK;
 }
 
 }  // namespace
@@ -1911,7 +1958,8 @@ uint64_t sgmv_linear_workspace_bytes(const lora_pool *p, const lora_linear_desc 
     if (!p || lora::check_linear_desc(d) != LORA_OK || d->num_tokens == 0 || nproj < 1 ||
         nproj > LORA_MAX_PROJ)
         return 0;
-    return linear_v_bytes(p, d->num_tokens, nproj) +
+    return linear_v_bytes(p, d->num_tokens, nproj, 4) +
+           linear_v_bytes(p, d->num_tokens, nproj, lora::operand_bytes(d->dtype)) +
            lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0).ws_bytes;
 }
 
@@ -1938,31 +1986,42 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
             return fail(LORA_EINVAL, "slice of projection %d exceeds the product's columns",
                         projs[i]);
     if (pl->T == 0) return LORA_OK;   // empty batch: nothing to read or write
+    // the shrink and the gathered rows address x within 2 GiB, the partials too
+    if (ldx > 0 && tensor_bytes(pl->T, ldx, cc.h_in, cc.es) > lora::kMaxTensorBytes)
+        return fail(LORA_EINVAL, "x spans more than 2 GiB");
     const lora::LinearCall c{d, x, ldx, w, ldw, bias, residual, ldr, y, ldy, ws, ws_bytes};
     const lora::LinearPlan lp = lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0);
-    const uint64_t v_bytes = linear_v_bytes(p, pl->T, nproj);
+    const uint64_t v_bytes = linear_v_bytes(p, pl->T, nproj, 4) +
+                             linear_v_bytes(p, pl->T, nproj, lora::operand_bytes(d->dtype));
     st = lora::check_linear(c, v_bytes + lp.ws_bytes);
     if (st != LORA_OK) return st;
     lora::DeltaArgs da{};
     if (pl->nb_act > 0) {
-        da.v = static_cast<const float *>(ws);
-        da.ldv = int64_t(nproj) * p->d.r_max;
-        da.rows = reinterpret_cast<const lora::TokenRow *>(static_cast<const uint8_t *>(pl->ws) +
-                                                           pl->lay.off_trow);
+        // v (float32, by plan position) of the long groups, then every
+        // position's scaled v as the product's operand
+        float *v = static_cast<float *>(ws);
+        uint8_t *operand = static_cast<uint8_t *>(ws) + linear_v_bytes(p, pl->T, nproj, 4);
+        st = run_operand(p, pl, layer, nproj, projs, x, ldx, cc, v, operand,
+                         static_cast<hipStream_t>(stream));
+        if (st != LORA_OK) return st;
+        const uint8_t *pw = static_cast<const uint8_t *>(pl->ws);
+        da.order = reinterpret_cast<const int32_t *>(pw + pl->lay.off_tok);
+        da.groups = reinterpret_cast<const lora::GroupRow *>(pw + pl->lay.off_groups);
+        da.pos_group = reinterpret_cast<const int32_t *>(pw + pl->lay.off_pgroup);
+        da.v = operand;
         da.slab = p->slab;
         for (int i = 0; i < nproj; ++i) {
             da.coef_b[i] = p->coef_b(layer, projs[i]);
             da.h_out[i] = p->d.h_out[projs[i]];
             da.y_off[i] = yoff[i];
         }
+        da.n_active = pl->n_active;
+        da.max_rpad = pl->max_rpad;
         da.nproj = nproj;
         da.r_max = p->d.r_max;
         da.dbg = debug_bounds(p, pl);
         const hipError_t e = lora::debug_word(&da.dbg_word);
         if (e != hipSuccess) return hip_fail(e, "debug word");
-        st = sgmv_shrink(p, pl, layer, nproj, projs, x, ldx, static_cast<float *>(ws), da.ldv,
-                         stream);
-        if (st != LORA_OK) return st;
     }
     return lora::run_linear(c, lp, static_cast<uint8_t *>(ws) + v_bytes, da,
                             static_cast<hipStream_t>(stream));

@@ -94,15 +94,16 @@ struct TileDesc {
 };
 static_assert(sizeof(TileDesc) == 32, "TileDesc is 32 bytes");
 
-// One token row of a plan as the product with adapters reads it: its
-// adapter's extent, padded rank (0: none) and scale (with the segment's
-// weight).
-struct TokenRow {
+// One adapter group of a plain plan as the product with adapters reads it:
+// the adapter's extent, padded rank, and the group's first position in the
+// plan's token order (groups are consecutive there; one entry past the last
+// group holds the end of all of them).
+struct GroupRow {
     uint32_t ext_lo, ext_hi;
     int32_t r_pad;
-    float scale;
+    int32_t first;
 };
-static_assert(sizeof(TokenRow) == 16, "TokenRow is one 16-byte load");
+static_assert(sizeof(GroupRow) == 16, "GroupRow is one 16-byte load");
 
 // What the debug build checks every unit against (see LORA_SGMV_DEBUG in
 // kernels.hip): the slab's bytes (every adapter block a unit addresses lies

@@ -93,7 +93,7 @@ def test_linear_workspace_bytes():
     assert hab.linear_workspace_bytes(128, 4096, 14337) == 0
     pool = hab.Pool(1, [4096], [4096], r_max=64, slab_ptr=1 << 20, slab_bytes=1 << 24)
     assert hab.sgmv_linear_workspace_bytes(pool, 128, 4096, 4096, 1) == \
-        hab.linear_workspace_bytes(128, 4096, 4096) + 4 * 128 * 64
+        hab.linear_workspace_bytes(128, 4096, 4096) + (4 + 6) * 128 * 64
     assert hab.sgmv_linear_workspace_bytes(pool, 128, 4096, 4096, 0) == 0
 
 
