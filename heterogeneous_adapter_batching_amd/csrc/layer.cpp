@@ -69,36 +69,108 @@ int64_t partial_ld(int64_t wide) { return int64_t(round_up(uint64_t(wide) + 3, 6
 
 namespace lora {
 
-LinearPlan linear_plan(int dtype, int T, int n, int k, bool glu) {
+// What the plan of a product chooses from, and what it goes by: the time of
+// one K tile (128 bytes of every row) of one workgroup with a CU to itself,
+// measured on MI355X with W from HBM (bf16 over 1024..28672 rows of W, K 4096
+// and 14336, 17..4096 tokens; float32 is bound by its matrix rate).  Small
+// tiles cost little each and keep every CU busy; large ones read less per
+// product.  At 128 x 4096 x 14336 (bf16) the plan's 64 x 128 tiles in 4
+// splits take 36 us, 256 x 128 in 2 splits 85, 128 x 128 unsplit 140; at
+// 4096 x 4096 x 4096 256 x 256 takes 102 and 128 x 128 160.
+struct TileCost {
+    int bt, bn;
+    float us[2];                 // float32, bf16 (0: not built)
+};
+constexpr TileCost kTiles[] = {{32, 64, {0.35f, 0.30f}},   {64, 128, {0.85f, 0.55f}},
+                               {128, 64, {0.f, 0.55f}},    {128, 128, {1.70f, 0.80f}},
+                               {256, 128, {0.f, 0.95f}},   {256, 256, {0.f, 1.50f}}};
+constexpr int kCus = 256;
+// A launch more (the join), and partial sums written and read at about this
+// rate (TB/s = bytes / us / 1e6).
+constexpr float kJoinUs = 2.5f, kPartialBytesPerUs = 3.5e6f;
+// One K tile of a delta (a dependent step of a small batch of work).
+constexpr float kDeltaTileUs = 0.6f;
+
+namespace {
+
+int k_tiles_of(int dtype, int k) {
+    return int((int64_t(k) * esize(dtype) + kKBytes - 1) / kKBytes);
+}
+float rounds(int64_t units) { return float((units + kCus - 1) / kCus); }
+
+struct Choice {
     LinearPlan pl{};
-    const int es = esize(dtype);
-    const int nk = int((int64_t(k) * es + kKBytes - 1) / kKBytes);
+    float us = 0.f;
+    void offer(float t, int bt, int bn, int splits, bool joined, int k_tiles) {
+        if (us != 0.f && t >= us) return;
+        us = t;
+        pl = LinearPlan{kLinearTile, bt, bn, splits, k_tiles, joined, 0};
+    }
+};
+
+// The best single launch.  With adapters it also runs, for each token tile,
+// the delta's K tiles: its groups, 3 pieces (bf16) of the largest rank's
+// vectors in eights, once per half of a pair.
+Choice direct(int dtype, int T, int n, int k, bool glu, int groups, int max_rpad) {
+    Choice c;
+    const int nk = k_tiles_of(dtype, k);
+    const int per = ((dtype == LORA_BF16 ? 3 : 1) * max_rpad * esize(dtype) / 16 + 7) / 8;
+    for (const TileCost &t : kTiles) {
+        const float us = t.us[dtype == LORA_BF16 ? 1 : 0];
+        if (us == 0.f) continue;
+        const int64_t tt = (T + t.bt - 1) / t.bt;
+        const int feat = glu ? t.bn / 2 : t.bn;              // gate and up rows in pairs
+        float one = float(nk) * us;
+        if (groups) one += (float(groups) / float(tt) + 1.f) * float(per * (glu ? 2 : 1)) * kDeltaTileUs;
+        c.offer(rounds(tt * ((int64_t(n) + feat - 1) / feat)) * one, t.bt, t.bn, 1, false, nk);
+    }
+    return c;
+}
+
+// The best product in parts along K (from `least` parts on) joined by a launch.
+Choice joined(int dtype, int T, int64_t wide, int k, int least) {
+    Choice c;
+    const int nk = k_tiles_of(dtype, k);
+    for (const TileCost &t : kTiles) {
+        const float us = t.us[dtype == LORA_BF16 ? 1 : 0];
+        if (us == 0.f) continue;
+        const int64_t tiles = int64_t((T + t.bt - 1) / t.bt) * ((wide + t.bn - 1) / t.bn);
+        for (int want = least; want <= 16; want = want < 4 ? want + 1 : want * 2) {
+            const int kt = (nk + want - 1) / want;
+            if (want > 1 && kt < 4) break;                   // too short to fill the pipeline
+            const int splits = (nk + kt - 1) / kt;
+            c.offer(rounds(tiles * splits) * float(kt) * us + kJoinUs +
+                        8.f * float(splits) * float(T) * float(wide) / kPartialBytesPerUs,
+                    t.bt, t.bn, splits, true, kt);
+        }
+    }
+    return c;
+}
+
+uint64_t partial_bytes(int splits, int T, int64_t wide) {
+    return round_up(4ull * uint64_t(splits) * uint64_t(T) * uint64_t(partial_ld(wide)), 256);
+}
+
+}  // namespace
+
+LinearPlan linear_plan(int dtype, int T, int n, int k, bool glu, int groups, int max_rpad) {
+    // A few tokens: W straight to registers, one launch.  Around 8 to 16
+    // tokens it and the tile kernel meet (4096 x 4096: 11.4 us against 13.4
+    // for one token, 14.1 against 14.0 for 16).
+    if (T <= kRowsTokens) return LinearPlan{kLinearRows, 16, 16, 1, k_tiles_of(dtype, k), false, 0};
     const int64_t wide = glu ? 2 * int64_t(n) : n;
-    pl.splits = 1;
-    pl.k_tiles = nk;
-    if (T <= 32) {
-        pl.kind = kLinearRows;
-        pl.bt = T <= 16 ? 16 : 32;
-        pl.bn = 16;
-        return pl;
-    }
-    pl.kind = kLinearTile;
-    auto tiles = [&](int bt, int bn) { return int64_t((T + bt - 1) / bt) * ((wide + bn - 1) / bn); };
-    if (dtype == LORA_BF16 && T > 128 && tiles(256, 256) >= 200) {
-        pl.bt = pl.bn = 256;
-    } else {
-        pl.bt = T <= 64 ? 64 : 128;
-        pl.bn = 128;
-    }
-    // too few tiles for the chip: split K, at least 4 K tiles a split
-    const int64_t have = tiles(pl.bt, pl.bn);
-    if (have < 192) {
-        const int64_t want = std::min<int64_t>((256 + have - 1) / have, std::max(nk / 4, 1));
-        pl.k_tiles = int((nk + want - 1) / want);
-        pl.splits = (nk + pl.k_tiles - 1) / pl.k_tiles;
-    }
-    if (pl.splits > 1) pl.ws_bytes = round_up(4ull * pl.splits * T * partial_ld(wide), 256);
+    const Choice d = direct(dtype, T, n, k, glu, groups, max_rpad);
+    const Choice j = joined(dtype, T, wide, k, groups ? 1 : 2);
+    LinearPlan pl = j.us != 0.f && j.us < d.us ? j.pl : d.pl;
+    if (pl.joined) pl.ws_bytes = partial_bytes(pl.splits, T, wide);
     return pl;
+}
+
+uint64_t linear_ws_bound(int dtype, int T, int n, int k, bool glu) {
+    if (T <= kRowsTokens) return 0;
+    const int64_t wide = glu ? 2 * int64_t(n) : n;
+    return partial_bytes(std::max(joined(dtype, T, wide, k, 1).pl.splits,
+                                  joined(dtype, T, wide, k, 2).pl.splits), T, wide);
 }
 
 lora_status check_linear_desc(const lora_linear_desc *d) {
@@ -188,7 +260,7 @@ extern "C" {
 
 uint64_t frozen_linear_workspace_bytes(const lora_linear_desc *d) {
     if (lora::check_linear_desc(d) != LORA_OK || d->num_tokens == 0) return 0;
-    return lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0).ws_bytes;
+    return lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0, 0, 0).ws_bytes;
 }
 
 lora_status frozen_linear(const lora_linear_desc *d, const void *x, int64_t ldx, const void *w,
@@ -198,7 +270,7 @@ lora_status frozen_linear(const lora_linear_desc *d, const void *x, int64_t ldx,
     if (st != LORA_OK) return st;
     if (d->num_tokens == 0) return LORA_OK;   // empty batch: no tensor is looked at
     const lora::LinearCall c{d, x, ldx, w, ldw, bias, residual, ldr, y, ldy, ws, ws_bytes};
-    const lora::LinearPlan pl = lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0);
+    const lora::LinearPlan pl = lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0, 0, 0);
     st = lora::check_linear(c, pl.ws_bytes);
     if (st != LORA_OK) return st;
     return lora::run_linear(c, pl, ws, lora::DeltaArgs{}, static_cast<hipStream_t>(stream));

@@ -88,18 +88,23 @@ struct LinearArgs {
     DeltaArgs delta;
 };
 
-// How a product runs: one launch, or `splits` > 1 partial products along K
-// and a launch that joins them.
+// How a product runs: one launch, or (joined) partial products along K and a
+// launch that joins them.
 enum LinearKind : int32_t { kLinearRows, kLinearTile };
 struct LinearPlan {
     LinearKind kind;
-    int32_t bt, bn;              // tokens and rows of w of a tile (rows: 16 TT, 16)
-    int32_t splits, k_tiles;
+    int32_t bt, bn;              // tokens and rows of w of a tile
+    int32_t splits, k_tiles;     // parts along K, and K tiles of one
+    bool joined;
     uint64_t ws_bytes;           // of the partial products
 };
 constexpr int kKBytes = 128;     // bytes of a row a K tile covers
-LinearPlan linear_plan(int dtype, int T, int n, int k, bool glu);
-
+constexpr int kRowsTokens = 12;  // most tokens of the rows kernel
+// groups, max_rpad: adapter groups of the batch and their largest padded rank
+// (0: no adapters)
+LinearPlan linear_plan(int dtype, int T, int n, int k, bool glu, int groups, int max_rpad);
+// the most workspace a plan of these sizes takes, whatever its adapters
+uint64_t linear_ws_bound(int dtype, int T, int n, int k, bool glu);
 // The arguments of a product call, as the entry points take them.
 struct LinearCall {
     const lora_linear_desc *d;

@@ -7,7 +7,7 @@
 // A few tokens read W once and are bound by its bytes; a prompt is bound by
 // the matrix cores.  So there are two kernels over W's rows (the left operand
 // of every MFMA, so that a lane ends with consecutive outputs of one token):
-//   k_linear_rows  up to 16 TT tokens: a workgroup per 16 rows of W, its waves
+//   k_linear_rows  up to 12 tokens: a workgroup per 16 rows of W, its waves
 //                  splitting K; W goes from HBM to registers.
 //   k_linear_tile  token tiles x row tiles through LDS; where the tiles are
 //                  too few for the chip, K is split over workgroups into
@@ -107,47 +107,108 @@ template <typename T> __device__ __forceinline__ float logistic(float v) {
     return 1.0f / (1.0f + expf(-v));
 }
 
-template <typename T> __device__ __forceinline__ float activate(float v, int act) {
+template <typename T, int N> __device__ __forceinline__ void activate(float (&v)[N], int act) {
     switch (act) {                                   // uniform
-    case LORA_ACT_RELU: return v < 0.f ? 0.f : v;    // NaN stays NaN
-    case LORA_ACT_SILU: return v * logistic<T>(v);
-    case LORA_ACT_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
+    case LORA_ACT_RELU:
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // NaN stays NaN
+        break;
+    case LORA_ACT_SILU:
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= logistic<T>(v[i]);
+        break;
+    case LORA_ACT_GELU:
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= 0.5f * erfcf(-0.70710678118654752f * v[i]);
+        break;
     case LORA_ACT_GELU_TANH:                         // (1 + tanh z) / 2 = logistic(2 z)
-        return v * logistic<T>(1.5957691216057308f * (v + 0.044715f * v * v * v));
-    default: return v;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] *= logistic<T>(1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+        break;
+    default: break;
     }
 }
 
-// The end of one token's outputs f .. f + 3: bias, activation, gating,
-// residual, rounding, store.
-template <typename T, bool GLU>
-__device__ __forceinline__ void finish(const LinearArgs &a, int t, int f, float (&v)[4],
-                                       float (&up)[4]) {
-    const int n = a.n - f;
-    if (t < 0 || n <= 0) return;
-    if (a.bias) {
-        float b[4];
-        Run4<T>::load(a.bias, f, n, b);
+// N consecutive outputs of one token (N 4, or 8 for one 16-byte store of
+// bf16), from column f on.
+template <typename T, int N> struct RunN {
+    static __device__ __forceinline__ void load(const T *p, int n, float (&o)[N]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += b[i];
-        if constexpr (GLU) {
-            Run4<T>::load(a.bias, int64_t(a.n) + f, n, b);
+        for (int h = 0; h < N / 4; ++h) {
+            float v[4];
+            Run4<T>::load(reinterpret_cast<const uint8_t *>(p), 4 * h, n - 4 * h, v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) up[i] += b[i];
+            for (int i = 0; i < 4; ++i) o[4 * h + i] = v[i];
         }
     }
+    static __device__ __forceinline__ void store(T *p, int n, const float (&o)[N]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = activate<T>(v[i], a.act);
-        if constexpr (GLU) v[i] *= up[i];
+        for (int h = 0; h < N / 4; ++h) {
+            const float v[4] = {o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]};
+            Run4<T>::store(reinterpret_cast<uint8_t *>(p), 4 * h, n - 4 * h, v);
+        }
+    }
+};
+template <> struct RunN<uint16_t, 8> {
+    static __device__ __forceinline__ void load(const uint16_t *p, int n, float (&o)[8]) {
+        if (n >= 8) {
+            const u32x4 w = *reinterpret_cast<const u32x4_any *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[2 * i] = bf16_lo(w[i]);
+                o[2 * i + 1] = bf16_hi(w[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = i < n ? bf16_lo(p[i]) : 0.f;
+        }
+    }
+    static __device__ __forceinline__ void store(uint16_t *p, int n, const float (&o)[8]) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = bf16x2_rne(o[2 * i], o[2 * i + 1]);
+        if (n >= 8) {
+            *reinterpret_cast<u32x4_any *>(p) = w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < n) p[i] = uint16_t(w[i / 2] >> (16 * (i % 2)));
+        }
+    }
+};
+
+// The end of one token's outputs f .. f + N - 1: bias, activation, gating,
+// residual, rounding, store.  `n`: outputs from f on that exist (N or more:
+// all of them, one vector each way).
+template <typename T, bool GLU, int N>
+__device__ __forceinline__ void finish(const LinearArgs &a, int t, int f, int n, float (&v)[N],
+                                       float (&up)[N]) {
+    if (t < 0 || n <= 0) return;
+    if (a.bias) {
+        const T *bias = reinterpret_cast<const T *>(a.bias) + f;
+        float b[N];
+        RunN<T, N>::load(bias, n, b);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += b[i];
+        if constexpr (GLU) {
+            RunN<T, N>::load(bias + a.n, n, b);
+#pragma unroll
+            for (int i = 0; i < N; ++i) up[i] += b[i];
+        }
+    }
+    activate<T>(v, a.act);
+    if constexpr (GLU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= up[i];
     }
     if (a.residual) {
-        float r[4];
-        Run4<T>::load(a.residual, int64_t(t) * a.ldr + f, n, r);
+        float r[N];
+        RunN<T, N>::load(reinterpret_cast<const T *>(a.residual) + int64_t(t) * a.ldr + f, n, r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += r[i];
+        for (int i = 0; i < N; ++i) v[i] += r[i];
     }
-    Run4<T>::store(a.y, int64_t(t) * a.ldy + f, n, v);
+    RunN<T, N>::store(reinterpret_cast<T *>(a.y) + int64_t(t) * a.ldy + f, n, v);
 }
 
 // -------------------------------------------------------------- operand -----
@@ -294,13 +355,14 @@ __device__ __forceinline__ int xcd_range(int units) {
 // ----------------------------------------------------------------- rows -----
 // One workgroup per 16 outputs (rows of W; with a gated pair 16 of gate and
 // the same 16 of up); wave w takes its share of K for all of them and all of
-// the up to 16 TT tokens, in batches of F vectors a lane whose loads are in
+// the up to 16 tokens, in batches of F vectors a lane whose loads are in
 // flight while the batch before multiplies.  The waves' sums meet in LDS.
-template <typename T, int TT, bool GLU, int KS, int NW>
+// Bound by W's bytes: 235 MB of gate and up rows at K 4096 in 46 us (5.1
+// TB/s, as a plain copy's).  KS: K-steps of the delta, 0 without adapters.
+template <typename T, bool GLU, int KS, int NW>
 __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs a) {
-    constexpr int E = Elem<T>::E, SPAN = 4 * E, NR = GLU ? 2 : 1;
-    constexpr int F = TT == 1 ? 4 : 2;
-    __shared__ f32x4 red[NW][NR * TT][kWaveSize];
+    constexpr int E = Elem<T>::E, SPAN = 4 * E, NR = GLU ? 2 : 1, F = 4;
+    __shared__ f32x4 red[NW][NR][kWaveSize];
     const int unit = xcd_range(a.units);
     if (unit >= a.units) return;                 // whole workgroup
     const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
@@ -322,18 +384,14 @@ __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs
     per += per & 1;                              // whole 128-byte lines a wave
     const int s_lo = w * per, s_hi = min(s_lo + per, steps);
 
-    f32x4 acc[NR][TT];
-    int tok[TT];                                 // token rows (with adapters: in plan order)
+    // this lane's token row (with adapters: in plan order)
+    const int tok = n < a.T ? (KS ? a.delta.order[n] : n) : -1;
+    f32x4 acc[NR];
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-        const int pos = tt * 16 + n;
-        tok[tt] = pos < a.T ? (KS ? a.delta.order[pos] : pos) : -1;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) acc[r][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int r = 0; r < NR; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     struct Batch {
-        u32x4 w[NR][F], x[TT][F];
+        u32x4 w[NR][F], x[F];
     };
     auto load = [&](Batch &b, int s0) {
 #pragma unroll
@@ -343,31 +401,24 @@ __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs
 #pragma unroll
             for (int r = 0; r < NR; ++r)
                 b.w[r][f] = bload16_nt(wr[r], off_or_oob(ok && n < rows, uint32_t(n) * wrow + kq));
-#pragma unroll
-            for (int tt = 0; tt < TT; ++tt)
-                b.x[tt][f] = bload16(xr, off_or_oob(ok && tok[tt] >= 0,
-                                                    uint32_t(tok[tt]) * xrow + kq));
+            b.x[f] = bload16(xr, off_or_oob(ok && tok >= 0, uint32_t(tok) * xrow + kq));
         }
     };
     auto multiply = [&](const Batch &b) {
 #pragma unroll
         for (int f = 0; f < F; ++f)
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-#pragma unroll
-                for (int tt = 0; tt < TT; ++tt) acc[r][tt] = mma<T>(b.w[r][f], b.x[tt][f], acc[r][tt]);
+            for (int r = 0; r < NR; ++r) acc[r] = mma<T>(b.w[r][f], b.x[f], acc[r]);
     };
     Batch b0, b1;
     load(b0, s_lo);
     if constexpr (KS > 0) {
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-            for (int tt = 0; tt < TT; ++tt) {
-                f32x4 d[1] = {acc[r][tt]};
-                add_delta<T, 1, KS>(a.delta, tt * 16, r * a.n + f0, w, NW, d);
-                acc[r][tt] = d[0];
-            }
+        for (int r = 0; r < NR; ++r) {
+            f32x4 d[1] = {acc[r]};
+            add_delta<T, 1, KS>(a.delta, 0, r * a.n + f0, w, NW, d);
+            acc[r] = d[0];
+        }
     }
     for (int s = s_lo; s < s_hi; s += 2 * F) {   // uniform
         load(b1, s + F);
@@ -376,24 +427,19 @@ __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs
         multiply(b1);
     }
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt) red[w][r * TT + tt][lane] = acc[r][tt];
+    for (int r = 0; r < NR; ++r) red[w][r][lane] = acc[r];
     __syncthreads();
-    if (w < TT) {
+    if (w == 0) {
         float v[NR][4];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            f32x4 s4 = red[0][r * TT + w][lane];
+            f32x4 s4 = red[0][r][lane];
 #pragma unroll
-            for (int i = 1; i < NW; ++i) s4 += red[i][r * TT + w][lane];
+            for (int i = 1; i < NW; ++i) s4 += red[i][r][lane];
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[r][i] = s4[i];
         }
-        int t = tok[0];
-#pragma unroll
-        for (int tt = 1; tt < TT; ++tt) t = w == tt ? tok[tt] : t;
-        finish<T, GLU>(a, t, f0 + 4 * q, v[0], v[NR - 1]);
+        finish<T, GLU>(a, tok, f0 + 4 * q, a.n - f0 - 4 * q, v[0], v[NR - 1]);
     }
 }
 
@@ -552,8 +598,12 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
     const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, q = lane >> 4;
     const int wave = wave_id();
     const int wt = wave / WN, wn = wave % WN;
-    const int tt = unit % a.tiles_t, rest = unit / a.tiles_t;
-    const int nt = rest % a.tiles_n, z = rest / a.tiles_n;
+    // tiles in order: 8 token tiles beside one another, then along W, so that
+    // the 32 workgroups of an XCD share 8 tiles of x and 4 of W in its L2
+    const int z = unit / (a.tiles_t * a.tiles_n), in_z = unit % (a.tiles_t * a.tiles_n);
+    const int group = in_z / (8 * a.tiles_n), in_g = in_z % (8 * a.tiles_n);
+    const int gt = min(8, a.tiles_t - group * 8);
+    const int tt = group * 8 + in_g % gt, nt = in_g / gt;
     const int t0 = tt * BT, f0 = nt * FEAT;
     const int wide = GLU ? a.n : a.wide;                     // rows of one half of W
     const uint32_t wrow = uint32_t(a.ldw) * sizeof(T), xrow = uint32_t(a.ldx) * sizeof(T);
@@ -781,13 +831,19 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
             }
         } else {
             const int t = pos < a.T ? (ADAPT ? a.delta.order[pos] : pos) : -1;
+            constexpr int N = G % 2 == 0 ? 8 : 4;
+            each<G * 4 / N>([&](auto run) {
+                constexpr int j0 = decltype(run)::value * (N / 4);
+                float v[N], u[N];
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const f32x4 g = acc[i][j], u = acc[i][TJ - G + j];
-                float v[4] = {g[0], g[1], g[2], g[3]};
-                float v2[4] = {u[0], u[1], u[2], u[3]};
-                finish<T, GLU>(a, t, fw + q * 4 * G + 4 * j, v, v2);
-            }
+                for (int k = 0; k < N; ++k) {
+                    v[k] = acc[i][j0 + k / 4][k % 4];
+                    u[k] = acc[i][TJ - G + j0 + k / 4][k % 4];
+                }
+                // (a tile inside W: no counts by lane)
+                const int f = fw + q * 4 * G + 4 * j0;
+                finish<T, GLU>(a, t, f, f0 + FEAT <= a.n ? N : a.n - f, v, u);
+            });
         }
     });
 }
@@ -841,7 +897,7 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[r][i] = s4[i];
     }
-    finish<T, GLU>(a, token(t0 + tok), f0 + 4 * m, v[0], v[NR - 1]);
+    finish<T, GLU>(a, token(t0 + tok), f0 + 4 * m, a.n - f0 - 4 * m, v[0], v[NR - 1]);
 }
 
 // ------------------------------------------------------------- launches -----
@@ -853,14 +909,14 @@ template <typename T> int delta_steps(const LinearArgs &a) {
     return a.delta.max_rpad <= 4 * Elem<T>::E ? 1 : LORA_MAX_RANK / (4 * Elem<T>::E);
 }
 
-template <typename T, int TT, bool GLU, int NW>
+template <typename T, bool GLU, int NW>
 hipError_t rows_launch(const LinearArgs &a, hipStream_t s) {
     constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E);
     const dim3 grid = grid_of(a.units), block(NW * 64);
     const int ks = delta_steps<T>(a);
-    if (ks == 0) hipLaunchKernelGGL((k_linear_rows<T, TT, GLU, 0, NW>), grid, block, 0, s, a);
-    else if (ks == 1) hipLaunchKernelGGL((k_linear_rows<T, TT, GLU, 1, NW>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_linear_rows<T, TT, GLU, KM, NW>), grid, block, 0, s, a);
+    if (ks == 0) hipLaunchKernelGGL((k_linear_rows<T, GLU, 0, NW>), grid, block, 0, s, a);
+    else if (ks == 1) hipLaunchKernelGGL((k_linear_rows<T, GLU, 1, NW>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_linear_rows<T, GLU, KM, NW>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -874,16 +930,19 @@ template <typename T, bool GLU> void join_launch(const LinearArgs &a, hipStream_
 }
 
 template <typename T, bool GLU>
-hipError_t rows_dispatch(const LinearPlan &pl, const LinearArgs &a, hipStream_t s) {
-    if (pl.bt == 16) return rows_launch<T, 1, GLU, 16>(a, s);
-    return rows_launch<T, 2, GLU, 8>(a, s);
+hipError_t rows_dispatch(const LinearArgs &a, hipStream_t s) {
+    // waves a workgroup: with few workgroups (narrow products) more of them
+    // keep the chip's loads busy: 8 against 4 take 10.6 us and 11.3 at
+    // 1024 x 4096, 53.6 and 50.2 at 28672 x 4096, 30.3 and 27.2 at 4096 x 14336
+    if (a.units <= 128) return rows_launch<T, GLU, 8>(a, s);
+    return rows_launch<T, GLU, 4>(a, s);
 }
 
 template <typename T, int BT, int BN, int WT, int WN, int S>
 hipError_t tile_launch(const LinearPlan &pl, bool glu, const LinearArgs &a, hipStream_t s) {
     const dim3 grid = grid_of(a.units), block(WT * WN * 64);
     const bool adapt = a.delta.order != nullptr;
-    if (pl.splits > 1) {
+    if (pl.joined) {
         hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, true, false>), grid, block, 0, s, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -902,11 +961,15 @@ hipError_t tile_launch(const LinearPlan &pl, bool glu, const LinearArgs &a, hipS
 template <typename T>
 hipError_t linear_dispatch(const LinearPlan &pl, bool glu, const LinearArgs &a, hipStream_t s) {
     if (pl.kind == kLinearRows)
-        return glu ? rows_dispatch<T, true>(pl, a, s) : rows_dispatch<T, false>(pl, a, s);
-    if (pl.bt == 64) return tile_launch<T, 64, 128, 1, 4, 4>(pl, glu, a, s);
-    if (pl.bt == 128) return tile_launch<T, 128, 128, 2, 2, 2>(pl, glu, a, s);
-    if constexpr (sizeof(T) == 2)
-        if (pl.bt == 256) return tile_launch<T, 256, 256, 2, 4, 2>(pl, glu, a, s);
+        return glu ? rows_dispatch<T, true>(a, s) : rows_dispatch<T, false>(a, s);
+    if (pl.bt == 32 && pl.bn == 64) return tile_launch<T, 32, 64, 1, 2, 4>(pl, glu, a, s);
+    if (pl.bt == 64 && pl.bn == 128) return tile_launch<T, 64, 128, 1, 4, 4>(pl, glu, a, s);
+    if (pl.bt == 128 && pl.bn == 128) return tile_launch<T, 128, 128, 2, 2, 4>(pl, glu, a, s);
+    if constexpr (sizeof(T) == 2) {
+        if (pl.bt == 128 && pl.bn == 64) return tile_launch<T, 128, 64, 2, 2, 4>(pl, glu, a, s);
+        if (pl.bt == 256 && pl.bn == 128) return tile_launch<T, 256, 128, 4, 2, 3>(pl, glu, a, s);
+        if (pl.bt == 256 && pl.bn == 256) return tile_launch<T, 256, 256, 2, 4, 2>(pl, glu, a, s);
+    }
     return hipErrorInvalidValue;
 }
 
@@ -927,11 +990,12 @@ hipError_t launch_linear(int dtype, const LinearPlan &pl, bool glu, LinearArgs a
     if (pl.kind == kLinearRows) {
         a.units = (a.n + 15) / 16;
     } else {
-        // a split product takes W's rows as they are, a direct one takes gate
+        // a joined product takes W's rows as they are, a direct one takes gate
         // and up rows in pairs
-        const int feat = glu && pl.splits == 1 ? pl.bn / 2 : pl.bn;
+        const bool pairs = glu && !pl.joined;
+        const int feat = pairs ? pl.bn / 2 : pl.bn;
         a.tiles_t = (a.T + pl.bt - 1) / pl.bt;
-        a.tiles_n = ((glu && pl.splits == 1 ? a.n : a.wide) + feat - 1) / feat;
+        a.tiles_n = ((pairs ? a.n : a.wide) + feat - 1) / feat;
         a.units = a.tiles_t * a.tiles_n * pl.splits;
     }
     return dtype == LORA_BF16 ? linear_dispatch<uint16_t>(pl, glu, a, s)

@@ -1960,7 +1960,7 @@ uint64_t sgmv_linear_workspace_bytes(const lora_pool *p, const lora_linear_desc 
         return 0;
     return linear_v_bytes(p, d->num_tokens, nproj, 4) +
            linear_v_bytes(p, d->num_tokens, nproj, lora::operand_bytes(d->dtype)) +
-           lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0).ws_bytes;
+           lora::linear_ws_bound(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0);
 }
 
 lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, int32_t nproj,
@@ -1990,7 +1990,9 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
     if (ldx > 0 && tensor_bytes(pl->T, ldx, cc.h_in, cc.es) > lora::kMaxTensorBytes)
         return fail(LORA_EINVAL, "x spans more than 2 GiB");
     const lora::LinearCall c{d, x, ldx, w, ldw, bias, residual, ldr, y, ldy, ws, ws_bytes};
-    const lora::LinearPlan lp = lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0);
+    const int32_t groups = int32_t(pl->group_adapter.size());
+    const lora::LinearPlan lp = lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0,
+                                                  groups, pl->max_rpad);
     const uint64_t v_bytes = linear_v_bytes(p, pl->T, nproj, 4) +
                              linear_v_bytes(p, pl->T, nproj, lora::operand_bytes(d->dtype));
     st = lora::check_linear(c, v_bytes + lp.ws_bytes);
