@@ -20,9 +20,19 @@ from .api import (  # noqa: F401
     sgmv_expand_partials, sgmv_expand_partials_sigma, sgmv_fused_static, plan_opts_default,
     debug_checks,
 )
-from .layer import (  # noqa: F401
-    block_norm, frozen_linear, linear_workspace_bytes, sgmv_linear, sgmv_linear_workspace_bytes,
-)
+# The operators around the delta take torch tensors only, so their module is
+# imported on first use: the package itself loads without torch.
+_LAYER = ("block_norm", "frozen_linear", "linear_workspace_bytes", "sgmv_linear",
+          "sgmv_linear_workspace_bytes")
+
+
+def __getattr__(name):
+    if name in _LAYER:
+        from . import layer
+        globals()[name] = getattr(layer, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 __all__ = ["Pool", "Plan", "sgmv_shrink", "sgmv_expand", "sgmv_fused", "sgmv_expand_sigma",
            "sgmv_fused_sigma", "sgmv_shrink_partials", "sgmv_expand_partials",

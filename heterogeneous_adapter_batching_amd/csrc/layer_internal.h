@@ -40,7 +40,7 @@ hipError_t launch_block_norm(int dtype, int stream_dtype, const NormArgs &a, hip
 struct DeltaArgs {
     const int32_t *order;        // [T] token row of each plan position; null: no adapters
     const GroupRow *groups;      // adapter groups, in plan order
-    const int32_t *pos_group;    // [T] group of each plan position
+    const PosRow *pos;           // [T] the plan positions
     const uint8_t *v;            // the operand: [T positions][nproj][pieces][r_max]
     const uint8_t *slab;
     int64_t coef_b[LORA_MAX_PROJ];  // B block offset = extent + r_pad * esize * coef_b[i]

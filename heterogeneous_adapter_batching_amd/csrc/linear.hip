@@ -259,23 +259,23 @@ template <typename T> __global__ __launch_bounds__(256) void k_operand(const Ope
 // Adds the delta to the accumulators of 16 plan positions: rows of the left
 // operand are outputs f(j, r) = f0 + (r / 4) 4 G + 4 j + r % 4, so a lane
 // holds outputs f0 + 4 G q .. + 4 G of its position.  Positions are in plan
-// order, so their adapters are consecutive groups: each group's B rows
-// multiply every position's operand and are kept in the columns of the
-// group's own (so one adapter's infinities stay with its tokens).  Of `nw`
-// waves that share the tile, wave w takes every nw-th group.  A dependent
-// round trip to memory per group would be the cost here, so the B rows of NB
-// groups are in flight together: with one at a time the join of a decode
-// batch's q/k/v took 16.3 us.  KS: K-steps of the plan's largest rank.
+// order, so a group's are neighbours: each group's B rows multiply every
+// position's operand and are kept in the columns of the group's own (so one
+// adapter's infinities stay with its tokens).  Of `nw` waves that share the
+// tile, wave w takes every nw-th group.  What this costs is the chain of
+// dependent loads position -> B rows, so the positions bring their group's
+// extent with them and the B rows of NB groups are in flight together.
+// KS: K-steps of the plan's largest rank.
 template <typename T, int G, int KS>
 __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, int w, int nw,
                                           f32x4 (&acc)[G]) {
     constexpr int E = Elem<T>::E, SPAN = 4 * E, P = VOperand<T>::kPieces;
-    constexpr int NB = G * KS >= 16 ? 1 : G * KS >= 8 ? 2 : 4;
+    constexpr int NB = G * KS >= 8 ? 1 : 8 / (G * KS);
     if (p0 >= d.n_active) return;                // uniform
     const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
     const int pos = p0 + n;
-    const int g0 = load_invariant(d.pos_group + p0);
-    const int g1 = load_invariant(d.pos_group + min(p0 + 15, d.n_active - 1));
+    PosRow pr{0u, 0u, 0, -1};
+    if (pos < d.n_active) pr = d.pos[pos];
     const int vrow = P * d.r_max * int(sizeof(T));
     for (int p = 0; p < d.nproj; ++p) {
         const int lo = d.y_off[p], ho = d.h_out[p];
@@ -292,19 +292,25 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
                     vo[ks][i] = *reinterpret_cast<const u32x4 *>(
                         vp + (i * d.r_max + j) * int(sizeof(T)));
             }
-        for (int g = g0 + w; g <= g1; g += NB * nw) {
+        // the first position of each group in the tile, one bit a lane
+        const int before = __shfl_up(pr.group, 1, 16);
+        uint32_t todo = uint32_t(__builtin_amdgcn_ballot_w64(
+                            pr.group >= 0 && (n == 0 || pr.group != before))) & 0xffffu;
+        for (int i = 0; i < w && todo; ++i) todo &= todo - 1;
+        while (todo) {                           // uniform
             u32x4 bf[NB][G][KS];
-            int first[NB], end[NB], rp[NB];
+            int grp[NB], rp[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const int gi = min(g + b * nw, g1);
-                const GroupRow gr = load_invariant(d.groups + gi);
-                first[b] = gr.first;
-                end[b] = g + b * nw <= g1 ? load_invariant(&d.groups[gi + 1].first) : 0;
-                rp[b] = gr.r_pad;
-                const uint64_t off = extent(gr.ext_lo, gr.ext_hi) +
-                                     uint64_t(gr.r_pad) * sizeof(T) * uint64_t(d.coef_b[p]);
-                uint64_t bytes = uint64_t(ho) * uint64_t(gr.r_pad) * sizeof(T);
+                const bool any = todo != 0;
+                const int l = any ? __builtin_ctz(todo) : 0;
+                for (int i = 0; i < nw; ++i) todo &= todo - 1;
+                grp[b] = any ? __builtin_amdgcn_readlane(pr.group, l) : -2;
+                rp[b] = any ? __builtin_amdgcn_readlane(pr.r_pad, l) : 0;
+                const uint64_t off = extent(__builtin_amdgcn_readlane(pr.ext_lo, l),
+                                            __builtin_amdgcn_readlane(pr.ext_hi, l)) +
+                                     uint64_t(rp[b]) * sizeof(T) * uint64_t(d.coef_b[p]);
+                uint64_t bytes = uint64_t(ho) * uint64_t(rp[b]) * sizeof(T);
                 if constexpr (kDebug) {
                     if (off + bytes > d.dbg.slab_bytes) {
                         atomicOr(d.dbg_word, uint32_t(kDbgSlab));
@@ -312,7 +318,7 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
                     }
                 }
                 const rsrc_t br = make_rsrc(d.slab + off, uint32_t(bytes));
-                const BLayout bl = b_layout(gr.r_pad, int(sizeof(T)));
+                const BLayout bl = b_layout(rp[b], int(sizeof(T)));
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
                     const int o = f0 + (n >> 2) * 4 * G + 4 * j + (n & 3) - lo;
@@ -326,7 +332,7 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const bool mine = pos >= first[b] && pos < end[b];
+                const bool mine = pr.group == grp[b];
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
                     f32x4 s4{0.f, 0.f, 0.f, 0.f};
@@ -530,8 +536,8 @@ template <typename T, int HALVES> struct DeltaTiles {
             for (int k = 0; k < HALVES; ++k)
                 any |= k * n + f0 < d.y_off[i] + d.h_out[i] && k * n + f0 + feat > d.y_off[i];
         if (last < t0 || !any) return;
-        g = load_invariant(d.pos_group + t0);
-        g1 = load_invariant(d.pos_group + last);
+        g = load_invariant(&d.pos[t0].group);
+        g1 = load_invariant(&d.pos[last].group);
         load(d);
         settle(d);
     }
@@ -778,41 +784,53 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
     // when this wave has its second half in registers, and frees the stage
     // for the copies of K tile kt + S.
     Frags fa, fb;
+    DeltaTiles<T, GLU ? 2 : 1> dt;
+    DeltaHeld held[S];                           // the delta's stages to come, in order
+    auto next_delta = [&](int st) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) fetch(k_lo + s, s);
+        for (int s = 0; s < S - 1; ++s) held[s] = held[s + 1];
+        held[S - 1] = fetch_delta(dt, st);
+    };
+    if constexpr (ADAPT) dt.start(a.delta, t0, min(BT, xrows), f0, FEAT, a.n);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        if (!ADAPT || k_lo + s < k_hi) fetch(k_lo + s, s);
+        else next_delta(s);
+    }
     wait_copies<(S - 1) * (XL + WL)>();
     __builtin_amdgcn_s_barrier();
     each<NR>([&](auto r) { read(fa, 0, 0, r); });
-    for (int kt = k_lo; kt < k_hi; ++kt) {
+    auto first_half = [&] {
         half(fa, fb, st, 1, std::false_type{}, 0, 0);
         wait_copies<(S - 2) * (XL + WL)>();      // the next stage's copies, in order
         wait_lds();
         __builtin_amdgcn_s_barrier();
         const int free = st;
         st = st + 1 == S ? 0 : st + 1;
+        return free;
+    };
+    int kt = k_lo;
+    for (; kt < (ADAPT ? k_hi - S : k_hi); ++kt) {
+        const int free = first_half();
         half(fb, fa, st, 0, std::true_type{}, kt + S, free);
     }
     if constexpr (ADAPT) {
-        DeltaTiles<T, GLU ? 2 : 1> dt;
-        dt.start(a.delta, t0, min(BT, xrows), f0, FEAT, a.n);
-        wait_copies<0>();
-        wait_lds();
-        __builtin_amdgcn_s_barrier();            // every stage is free
-        DeltaHeld held[S];                       // the stages to come, in order
-#pragma unroll
-        for (int s = 0; s < S - 1; ++s) held[s] = fetch_delta(dt, s);
-        int st_in = S - 1;
-        st = 0;
+        // the delta's first stages come in under the last K tiles
+        for (; kt < k_hi; ++kt) {
+            const int free = first_half();
+            next_delta(free);
+            half(fb, fa, st, 0, std::false_type{}, 0, 0);
+        }
+    }
+    if constexpr (ADAPT) {
         while (held[0].half) {                   // uniform
-            wait_copies<(S - 2) * (XL + WL)>();
+            wait_copies<(S - 1) * (XL + WL)>();
             __builtin_amdgcn_s_barrier();
-            held[S - 1] = fetch_delta(dt, st_in);
             multiply_delta(st, held[0]);
             wait_lds();
-#pragma unroll
-            for (int s = 0; s < S - 1; ++s) held[s] = held[s + 1];
+            __builtin_amdgcn_s_barrier();        // the stage is free
+            next_delta(st);
             st = st + 1 == S ? 0 : st + 1;
-            st_in = st_in + 1 == S ? 0 : st_in + 1;
         }
     }
     wait_copies<0>();                            // none may land after the workgroup's end
@@ -849,55 +867,54 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
 }
 
 // ----------------------------------------------------------------- join -----
-// One workgroup per 16 tokens x 64 outputs of a split product: wave w adds
-// partial products w, w + 4, ... and the deltas of every fourth adapter, the
-// waves' sums meet in LDS, and each wave finishes 4 tokens (a row of 64
-// outputs is one contiguous store).
-template <typename T, bool GLU, int KS>
+// One wave per 16 tokens (with adapters: plan positions) x 16 G outputs of a
+// product in parts: the parts' sum, the delta, and the end of the outputs,
+// with nothing shared between waves.  A wave's chain of dependent loads is
+// what it waits for, so small waves, many of them resident, beat fewer that
+// share a tile through LDS (G 4 and the parts and groups dealt to 4 or 8
+// waves: 12.4 and 17.7 us for a decode batch's q/k/v, 66 and 69 for its
+// gated pair of mixed ranks).
+template <typename T, bool GLU, int KS, int G>
 __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
-    constexpr int NR = GLU ? 2 : 1, G = 4;
-    __shared__ f32x4 red[4][NR * G][kWaveSize];
-    const int unit = blockIdx.x;
+    constexpr int NR = GLU ? 2 : 1, N = 4 * G, Z = 4;
     const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-    const int w = wave_id();
     const int tiles_t = (a.T + 15) / 16;
-    const int t0 = unit % tiles_t * 16, f0 = unit / tiles_t * 64;
-    auto token = [&](int pos) { return pos < a.T ? (KS ? a.delta.order[pos] : pos) : -1; };
-    const int t = token(t0 + n);
+    const int p0 = blockIdx.x % tiles_t * 16;
+    const int f0 = (blockIdx.x / tiles_t * 4 + wave_id()) * 16 * G;
+    if (f0 >= a.n) return;
+    const int pos = p0 + n;
+    const int t = pos < a.T ? (KS ? a.delta.order[pos] : pos) : -1;
+    float v[NR][N];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         const int c0 = r * a.n + f0;             // column before the activation
         f32x4 s[G];
 #pragma unroll
         for (int j = 0; j < G; ++j) s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int z = w; z < a.splits; z += 4) {
-            const float *p = a.partial + (int64_t(z) * a.T + t) * a.ldp + c0 + q * 16;
+        if constexpr (KS > 0) add_delta<T, G, KS>(a.delta, p0, c0, 0, 1, s);
+        // the parts in order, Z of them in flight
+        const float *p = a.partial + int64_t(t) * a.ldp + c0 + q * N;
+        const int64_t step = int64_t(a.T) * a.ldp;
+        for (int z = 0; z < a.splits; z += Z) {
+            u32x4 w[Z][G];
 #pragma unroll
-            for (int j = 0; j < G; ++j)
-                if (t >= 0 && c0 + q * 16 + 4 * j < a.wide) {
+            for (int k = 0; k < Z; ++k)
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    w[k][j] = u32x4{0u, 0u, 0u, 0u};
                     // (any alignment: the second half of a pair starts at column n)
-                    const u32x4 v = *reinterpret_cast<const u32x4_any *>(p + 4 * j);
-                    s[j] += __builtin_bit_cast(f32x4, v);
+                    if (t >= 0 && z + k < a.splits && c0 + q * N + 4 * j < a.wide)
+                        w[k][j] = *reinterpret_cast<const u32x4_any *>(p + (z + k) * step + 4 * j);
                 }
+#pragma unroll
+            for (int k = 0; k < Z; ++k)
+#pragma unroll
+                for (int j = 0; j < G; ++j) s[j] += __builtin_bit_cast(f32x4, w[k][j]);
         }
-        if constexpr (KS > 0) add_delta<T, G, KS>(a.delta, t0, c0, w, 4, s);
 #pragma unroll
-        for (int j = 0; j < G; ++j) red[w][r * G + j][lane] = s[j];
+        for (int k = 0; k < N; ++k) v[r][k] = s[k / 4][k % 4];
     }
-    __syncthreads();
-    // outputs 4 m .. 4 m + 3 of token 4 w + lane / 16
-    const int m = lane & 15, tok = 4 * w + (lane >> 4);
-    float v[NR][4];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        const int e = (m >> 2) * 16 + tok;
-        f32x4 s4 = red[0][r * G + (m & 3)][e];
-#pragma unroll
-        for (int i = 1; i < 4; ++i) s4 += red[i][r * G + (m & 3)][e];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[r][i] = s4[i];
-    }
-    finish<T, GLU>(a, token(t0 + tok), f0 + 4 * m, a.n - f0 - 4 * m, v[0], v[NR - 1]);
+    finish<T, GLU>(a, t, f0 + q * N, a.n - f0 - q * N, v[0], v[NR - 1]);
 }
 
 // ------------------------------------------------------------- launches -----
@@ -920,13 +937,17 @@ hipError_t rows_launch(const LinearArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Outputs of a join wave: 16, and 32 for bf16 adapters beyond one K-step,
+// whose operand (6 vectors a lane) then serves twice the rows of B (a gated
+// decode batch of ranks 8 to 64: 43 us against 55; rank 16 q/k/v 13.4
+// against 12.7).
 template <typename T, bool GLU> void join_launch(const LinearArgs &a, hipStream_t s) {
-    constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E);
-    const dim3 grid(((a.T + 15) / 16) * ((a.n + 63) / 64)), block(256);
-    const int ks = delta_steps<T>(a);
-    if (ks == 0) hipLaunchKernelGGL((k_linear_join<T, GLU, 0>), grid, block, 0, s, a);
-    else if (ks == 1) hipLaunchKernelGGL((k_linear_join<T, GLU, 1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_linear_join<T, GLU, KM>), grid, block, 0, s, a);
+    constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E), GM = sizeof(T) == 2 ? 2 : 1;
+    const int ks = delta_steps<T>(a), g = ks > 1 ? GM : 1;
+    const dim3 grid(((a.T + 15) / 16) * ((a.n + 64 * g - 1) / (64 * g))), block(256);
+    if (ks == 0) hipLaunchKernelGGL((k_linear_join<T, GLU, 0, 1>), grid, block, 0, s, a);
+    else if (ks == 1) hipLaunchKernelGGL((k_linear_join<T, GLU, 1, 1>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_linear_join<T, GLU, KM, GM>), grid, block, 0, s, a);
 }
 
 template <typename T, bool GLU>

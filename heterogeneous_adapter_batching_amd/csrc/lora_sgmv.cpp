@@ -173,7 +173,7 @@ struct PlanCounts {
 // Byte offsets of the tables in a plan workspace, and its size.
 struct PlanLayout {
     uint64_t off_tok = 0, off_blocks = 0, off_tiles = 0, off_btok = 0, off_ttok = 0, off_tsig = 0,
-             off_tw = 0, off_mblocks = 0, off_groups = 0, off_pgroup = 0,
+             off_tw = 0, off_mblocks = 0, off_groups = 0, off_pos = 0,
              off_part = 0;
     uint64_t off_lv = 0;   // long groups' v rows, from off_part (plain plans)
     uint64_t image_bytes = 0, part_bytes = 0, ws_bytes = 0;
@@ -225,7 +225,7 @@ PlanLayout plan_layout(const lora_pool_desc &d, const PlanCounts &c, int32_t mp,
     L.off_tw = o;      o = round_up(o + 4ull * T, 256);
     L.off_mblocks = o; o = round_up(o + sizeof(lora::MergeBlock) * uint64_t(c.mb), 256);
     L.off_groups = o;  o = round_up(o + sizeof(lora::GroupRow) * uint64_t(c.ng + 1), 256);
-    L.off_pgroup = o;  o = round_up(o + 4ull * T, 256);
+    L.off_pos = o;     o = round_up(o + sizeof(lora::PosRow) * T, 256);
     L.image_bytes = o;
     // the shrink's partial tiles: every rank tile at the plan's tiles per
     // block (a merge plan), or the short groups' tiles at one 16-token tile
@@ -259,7 +259,7 @@ struct lora_plan {
     // the adapter groups and each plan position's (-1: none), for the product
     // with adapters
     std::vector<lora::GroupRow> group_rows{lora::GroupRow{0u, 0u, 0, 0}};
-    std::vector<int32_t> position_group;
+    std::vector<lora::PosRow> positions;
     std::vector<int32_t> token_slot;     // merge slot per plan-order row (-1: none)
     bool weighted = false;
     int32_t merge_k = 0;                 // slots per segment of a merge plan (0: not one)
@@ -710,7 +710,7 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
     pl->tt = 1;
     pl->token_group.assign(T, -1);
     pl->group_rows.clear();
-    pl->position_group.clear();
+    pl->positions.clear();
 
     // groups in first-appearance order (runs with rows only); a member is a
     // (row, run) pair
@@ -811,7 +811,10 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
             pl->token_sigma.push_back(rn ? rn->sigma : -1);
             pl->token_weight.push_back(rn ? rn->weight : 1.0f);
             pl->token_slot.push_back(rn ? rn->slot : -1);
-            pl->position_group.push_back(sl ? g : -1);
+            pl->positions.push_back(
+                sl ? lora::PosRow{uint32_t(sl->off & 0xffffffffu), uint32_t(sl->off >> 32),
+                                  sl->r_pad, g}
+                   : lora::PosRow{0u, 0u, 0, -1});
             if (rn) pl->max_sigma = std::max(pl->max_sigma, rn->sigma);
         }
     };
@@ -1108,7 +1111,7 @@ lora_status lora_plan_upload(lora_plan *pl, void *ws, uint64_t ws_bytes, int32_t
     if (R && pl->weighted) std::memcpy(img + lay.off_tw, pl->token_weight.data(), 4ull * R);
     std::memcpy(img + lay.off_groups, pl->group_rows.data(),
                 sizeof(lora::GroupRow) * pl->group_rows.size());
-    if (R) std::memcpy(img + lay.off_pgroup, pl->position_group.data(), 4ull * R);
+    if (R) std::memcpy(img + lay.off_pos, pl->positions.data(), sizeof(lora::PosRow) * R);
     if (!pl->mblocks.empty())
         std::memcpy(img + lay.off_mblocks, pl->mblocks.data(),
                     sizeof(lora::MergeBlock) * pl->mblocks.size());
@@ -2009,7 +2012,7 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
         const uint8_t *pw = static_cast<const uint8_t *>(pl->ws);
         da.order = reinterpret_cast<const int32_t *>(pw + pl->lay.off_tok);
         da.groups = reinterpret_cast<const lora::GroupRow *>(pw + pl->lay.off_groups);
-        da.pos_group = reinterpret_cast<const int32_t *>(pw + pl->lay.off_pgroup);
+        da.pos = reinterpret_cast<const lora::PosRow *>(pw + pl->lay.off_pos);
         da.v = operand;
         da.slab = p->slab;
         for (int i = 0; i < nproj; ++i) {

@@ -105,6 +105,15 @@ struct GroupRow {
 };
 static_assert(sizeof(GroupRow) == 16, "GroupRow is one 16-byte load");
 
+// One plan position: its group (-1: no adapter) with the group's extent and
+// padded rank, so that a lane has them in one load.
+struct PosRow {
+    uint32_t ext_lo, ext_hi;
+    int32_t r_pad;
+    int32_t group;
+};
+static_assert(sizeof(PosRow) == 16, "PosRow is one 16-byte load");
+
 // What the debug build checks every unit against (see LORA_SGMV_DEBUG in
 // kernels.hip): the slab's bytes (every adapter block a unit addresses lies
 // inside), the tokens of the batch (every token row read from the plan lies

@@ -1,48 +1,56 @@
 """The operators around the delta over the C ABI (argument marshalling only):
 the residual stream's norms, the frozen layer's product, and the product with
-the delta inside its activation."""
+the delta inside its activation.
+
+A decode step makes hundreds of such calls, each a few microseconds on the
+GPU, so what is the same from call to call (descriptors, device checks) is
+made once and each tensor is asked for each of its properties once."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
+
+import torch
 
 from ._lib import (ACTS, GATE_ACTS, LORA_BF16, LORA_F32, NORMS, LinearDesc, NormDesc, check, load)
-from .api import _DTYPES, _offsets, _projs, _stream_handle, _torch
+from .api import _DTYPES, _offsets, _projs
+
+_CODES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
 
 
-def _dtype_code(t, name):
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return LORA_BF16
-    if t.dtype == torch.float32:
-        return LORA_F32
-    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+def _dtype_code(dtype, name):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+    return code
 
 
-def _matrix(t, name, shape=None, dtype=None, device=None):
-    """A 2-D CUDA tensor with contiguous rows, as (pointer, row stride)."""
-    torch = _torch()
+def _matrix(t, name, shape, dtype, device):
+    """A 2-D CUDA tensor with contiguous rows, as (pointer, row stride); None
+    for shape, dtype or device: any."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must be {list(shape) if shape else '2-D'}, got {list(t.shape)}")
+    s = t.shape
+    if s != shape and (shape is not None or len(s) != 2):
+        raise ValueError(f"{name} must be {list(shape) if shape else '2-D'}, got {list(s)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = s
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} rows must be contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), (ld if rows > 1 else cols)
 
 
 def _vector(t, name, n, dtype, device):
     """A contiguous vector of n elements, or None: its pointer (0 for None)."""
     if t is None:
         return 0
-    torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {n}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -57,22 +65,34 @@ def _code(table, key, what):
     return table[key]
 
 
-def _on(device):
-    """Makes `device` current for a launch, if it is not already."""
-    torch = _torch()
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _enqueue(fn, args, device, stream):
+    """Calls the library with `stream` (None: the device's current one) as the
+    last argument, with `device` current for the launches."""
+    index = device.index
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        check(fn(*args, handle))
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, handle))
 
 
 def _new(shape, dtype, device, stream):
     """A tensor for a launch on `stream` (None: the current one).  Freed memory
     is given out again in the order of the stream it was made on, so another
     one's use is noted."""
-    t = _torch().empty(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=device)
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+# (descriptors are only read by the library: one per distinct set of values)
+@functools.lru_cache(maxsize=1024)
+def _norm_desc(dtype, stream_dtype, T, d, post, pre, gate_act, unit_offset, alpha, beta, eps):
+    return ctypes.byref(NormDesc(
+        dtype, stream_dtype, T, d, _code(NORMS, post, "post norm"), _code(NORMS, pre, "pre norm"),
+        _code(GATE_ACTS, gate_act, "gate_act"), int(unit_offset), alpha, beta, eps))
 
 
 def block_norm(h, o=None, *, post="none", post_weight=None, post_bias=None, gate=None,
@@ -91,63 +111,62 @@ def block_norm(h, o=None, *, post="none", post_weight=None, post_bias=None, gate
     given or new ones; h_out may be h itself.  Without a block output and
     with beta 1 the stream is unchanged: h itself is returned unless h_out is
     given.  u is None with pre="none".  Inference only."""
-    torch = _torch()
-    hp, ldh = _matrix(h, "h")
-    T, d = h.shape
-    dev = h.device
-    like = next((t for t in (o, u, pre_weight, pre_bias) if t is not None), h)
-    desc = NormDesc(_dtype_code(like, "o"), _dtype_code(h, "h"), T, d,
-                    _code(NORMS, post, "post norm"), _code(NORMS, pre, "pre norm"),
-                    _code(GATE_ACTS, gate_act, "gate_act"), int(bool(unit_offset)), alpha, beta,
-                    eps)
-    dt = like.dtype
-    op, ldo = _matrix(o, "o", (T, d), dt, dev) if o is not None else (0, d)
+    hp, ldh = _matrix(h, "h", None, None, None)
+    shape, dev, hdt = h.shape, h.device, h.dtype
+    T, d = shape
+    dt = hdt
+    for t in (o, u, pre_weight, pre_bias):
+        if t is not None:
+            dt = t.dtype
+            break
+    desc = _norm_desc(_dtype_code(dt, "o"), _dtype_code(hdt, "h"), T, d, post, pre, gate_act,
+                      bool(unit_offset), alpha, beta, eps)
+    op, ldo = _matrix(o, "o", shape, dt, dev) if o is not None else (0, d)
     gp, ldg = 0, 0
     if gate is not None:
         if gate.dim() == 1:
             gp = _vector(gate, "gate", d, dt, dev)
         else:
-            gp, ldg = _matrix(gate, "gate", (T, d), dt, dev)
-    vec = [_vector(t, n, d, dt, dev) for t, n in (
-        (post_weight, "post_weight"), (post_bias, "post_bias"), (pre_weight, "pre_weight"),
-        (pre_bias, "pre_bias"))]
+            gp, ldg = _matrix(gate, "gate", shape, dt, dev)
     unchanged = o is None and beta == 1.0 and h_out is None
     if h_out is None and not unchanged:
-        h_out = _new((T, d), h.dtype, dev, stream)
-    if pre != "none" and u is None:
-        u = _new((T, d), dt, dev, stream)
-    hop, ldho = _matrix(h_out, "h_out", (T, d), h.dtype, dev) if h_out is not None else (0, d)
-    up, ldu = _matrix(u, "u", (T, d), dt, dev) if u is not None else (0, d)
-    with _on(dev):
-        check(load().block_norm(ctypes.byref(desc), hp, ldh, op, ldo, vec[0], vec[1], gp, ldg,
-                                vec[2], vec[3], hop, ldho, up, ldu, _stream_handle(stream)))
+        h_out = _new(shape, hdt, dev, stream)
+    if u is None and pre != "none":
+        u = _new(shape, dt, dev, stream)
+    hop, ldho = _matrix(h_out, "h_out", shape, hdt, dev) if h_out is not None else (0, d)
+    up, ldu = _matrix(u, "u", shape, dt, dev) if u is not None else (0, d)
+    _enqueue(load().block_norm,
+             (desc, hp, ldh, op, ldo, _vector(post_weight, "post_weight", d, dt, dev),
+              _vector(post_bias, "post_bias", d, dt, dev), gp, ldg,
+              _vector(pre_weight, "pre_weight", d, dt, dev),
+              _vector(pre_bias, "pre_bias", d, dt, dev), hop, ldho, up, ldu), dev, stream)
     return (h if unchanged else h_out), u
 
 
+@functools.lru_cache(maxsize=1024)
 def _linear_desc(num_tokens, n, k, dtype, glu, act="none"):
-    return LinearDesc(dtype, num_tokens, n, k, _code(ACTS, act, "act"), int(bool(glu)))
+    return ctypes.byref(LinearDesc(dtype, num_tokens, n, k, _code(ACTS, act, "act"), int(glu)))
 
 
 def linear_workspace_bytes(num_tokens: int, n: int, k: int, dtype: str = "bf16",
                            glu: bool = False) -> int:
     """Bytes of workspace a frozen_linear call of these sizes takes (0: none);
     n is the width of y."""
-    d = _linear_desc(num_tokens, n, k, _DTYPES[dtype], glu)
-    return int(load().frozen_linear_workspace_bytes(ctypes.byref(d)))
+    return int(load().frozen_linear_workspace_bytes(
+        _linear_desc(num_tokens, n, k, _DTYPES[dtype], bool(glu))))
 
 
 def sgmv_linear_workspace_bytes(pool, num_tokens: int, n: int, k: int, nproj: int,
                                 glu: bool = False) -> int:
     """The same for sgmv_linear over nproj projections of the pool."""
-    d = _linear_desc(num_tokens, n, k, pool.desc.dtype, glu)
-    return int(load().sgmv_linear_workspace_bytes(pool.handle, ctypes.byref(d), nproj))
+    return int(load().sgmv_linear_workspace_bytes(
+        pool.handle, _linear_desc(num_tokens, n, k, pool.desc.dtype, bool(glu)), nproj))
 
 
-def _linear_call(x, w, bias, act, glu, residual, y, ws, stream, need, call):
+def _linear_call(x, w, bias, act, glu, residual, y, ws, stream, need, fn, head):
     """Checks the tensors of a product call, makes y and the workspace where
-    they are not given, and hands the C arguments to `call`."""
-    torch = _torch()
-    xp, ldx = _matrix(x, "x")
+    they are not given, and calls fn(*head, descriptor, tensors, stream)."""
+    xp, ldx = _matrix(x, "x", None, None, None)
     dev, dt = x.device, x.dtype
     wp, ldw = _matrix(w, "w", None, dt, dev)
     (T, k), (wide, kw) = x.shape, w.shape
@@ -156,20 +175,20 @@ def _linear_call(x, w, bias, act, glu, residual, y, ws, stream, need, call):
     if glu and wide % 2:
         raise ValueError(f"w must hold a gate and an up of the same rows, got {wide}")
     n = wide // 2 if glu else wide
+    shape = (T, n)
+    desc = _linear_desc(T, n, k, _dtype_code(dt, "x"), bool(glu), act)
     bp = _vector(bias, "bias", wide, dt, dev)
-    rp, ldr = _matrix(residual, "residual", (T, n), dt, dev) if residual is not None else (0, n)
+    rp, ldr = _matrix(residual, "residual", shape, dt, dev) if residual is not None else (0, n)
     if y is None:
-        y = _new((T, n), dt, dev, stream)
-    yp, ldy = _matrix(y, "y", (T, n), dt, dev)
-    desc = _linear_desc(T, n, k, _dtype_code(x, "x"), glu, act)
+        y = _new(shape, dt, dev, stream)
+    yp, ldy = _matrix(y, "y", shape, dt, dev)
     if ws is None:
         size = need(desc)
         ws = _new((size,), torch.uint8, dev, stream) if size else None
     elif not ws.is_cuda or ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on {dev}")
-    wsp, wsn = (ws.data_ptr(), ws.numel() * ws.element_size()) if ws is not None else (0, 0)
-    with _on(dev):
-        check(call(desc, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, wsp, wsn, _stream_handle(stream)))
+    wsp, wsn = (ws.data_ptr(), ws.nbytes) if ws is not None else (0, 0)
+    _enqueue(fn, (*head, desc, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, wsp, wsn), dev, stream)
     return y
 
 
@@ -187,10 +206,8 @@ def frozen_linear(x, w, *, bias=None, act="none", glu=False, residual=None, y=No
     workspace of linear_workspace_bytes (made per call if not given).
     Inference only.  Returns y."""
     lib = load()
-    return _linear_call(
-        x, w, bias, act, glu, residual, y, ws, stream,
-        lambda d: lib.frozen_linear_workspace_bytes(ctypes.byref(d)),
-        lambda d, *a: lib.frozen_linear(ctypes.byref(d), *a))
+    return _linear_call(x, w, bias, act, glu, residual, y, ws, stream,
+                        lib.frozen_linear_workspace_bytes, lib.frozen_linear, ())
 
 
 def sgmv_linear(pool, plan, layer, projs, y_offsets, x, w, *, bias=None, act="none", glu=False,
@@ -201,11 +218,9 @@ def sgmv_linear(pool, plan, layer, projs, y_offsets, x, w, *, bias=None, act="no
     then the up's n).  plan: a plain or weighted plan of x's tokens."""
     lib = pool.lib
     count, parr = _projs(projs)
-    offs = _offsets(y_offsets)
-    if len(tuple(y_offsets)) != count:
+    if len(y_offsets) != count:
         raise ValueError("y_offsets must have one entry per projection")
     return _linear_call(
         x, w, bias, act, glu, residual, y, ws, stream,
-        lambda d: lib.sgmv_linear_workspace_bytes(pool.handle, ctypes.byref(d), count),
-        lambda d, *a: lib.sgmv_linear(pool.handle, plan.handle, layer, count, parr, offs,
-                                      ctypes.byref(d), *a))
+        lambda d: lib.sgmv_linear_workspace_bytes(pool.handle, d, count), lib.sgmv_linear,
+        (pool.handle, plan.handle, layer, count, parr, _offsets(y_offsets)))
