@@ -41,7 +41,10 @@ struct DeltaArgs {
     const int32_t *order;        // [T] token row of each plan position; null: no adapters
     const GroupRow *groups;      // adapter groups, in plan order
     const PosRow *pos;           // [T] the plan positions
-    const uint8_t *v;            // the operand: [T positions][nproj][pieces][r_max]
+    const uint8_t *v;            // the operand: [T positions][nproj][pieces][r_max],
+    const float *partial;        // or (non-null) the shrink's partials it is summed from
+    uint32_t partial_bytes;
+    int32_t c0;                  // chunks of the partials
     const uint8_t *slab;
     int64_t coef_b[LORA_MAX_PROJ];  // B block offset = extent + r_pad * esize * coef_b[i]
     int32_t h_out[LORA_MAX_PROJ];
@@ -67,6 +70,13 @@ struct OperandArgs {
     int32_t nb, nb_long, nproj, c0, r_max;
     DebugBounds dbg;
 };
+// The largest padded rank whose delta is one K-step of the matrix cores.  Up
+// to it the joins (and the product of a few tokens) sum a lane's partials
+// themselves, which spares a launch (q/k/v of a decode batch, rank 16: 44.7 us
+// against 46.5 of kernels); beyond it every join wave would sum several steps'
+// (a gated batch of ranks 8 to 64: the join 63.7 us against 43.4 with the
+// operand formed once).
+constexpr int one_step_rank(int dtype) { return dtype == LORA_BF16 ? 32 : 16; }
 // bytes of one operand entry: three bf16 pieces, or the float32 value
 constexpr int operand_bytes(int dtype) { return dtype == LORA_BF16 ? 6 : 4; }
 hipError_t launch_operand(int dtype, const OperandArgs &a, hipStream_t s);

@@ -274,24 +274,41 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
     if (p0 >= d.n_active) return;                // uniform
     const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
     const int pos = p0 + n;
-    PosRow pr{0u, 0u, 0, -1};
+    PosRow pr{};
+    pr.group = -1;
     if (pos < d.n_active) pr = d.pos[pos];
     const int vrow = P * d.r_max * int(sizeof(T));
     for (int p = 0; p < d.nproj; ++p) {
         const int lo = d.y_off[p], ho = d.h_out[p];
         if (f0 + 16 * G <= lo || f0 >= lo + ho) continue;
-        u32x4 vo[KS][P];
-        const uint8_t *vp = d.v + (int64_t(pos) * d.nproj + p) * vrow;
+        VOperand<T> vo[KS];
+        if (KS == 1 && d.partial) {              // uniform
+            const rsrc_t parts = make_rsrc(d.partial, d.partial_bytes);
+            const int j = q * E;
+            float f[E];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+            for (int h = 0; h < E / 4; ++h) {
+                f32x4 s4{0.f, 0.f, 0.f, 0.f};
+                if (j + 4 * h < pr.r_pad)
+                    s4 = chunk_sum(parts, partial_off(pr.rt, j + 4 * h, pr.slot, p, d.nproj, d.c0, 1),
+                                   uint32_t(d.nproj * kTile * kTile), d.c0);
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                vo[ks][i] = u32x4{0u, 0u, 0u, 0u};
-                const int j = ks * SPAN + q * E;
-                if (pos < d.n_active && j < d.r_max)
-                    vo[ks][i] = *reinterpret_cast<const u32x4 *>(
-                        vp + (i * d.r_max + j) * int(sizeof(T)));
+                for (int k = 0; k < 4; ++k) f[4 * h + k] = pr.scale * s4[k];
             }
+            vo[0].set(f);
+        } else {
+            const uint8_t *vp = d.v + (int64_t(pos) * d.nproj + p) * vrow;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    vo[ks].piece[i] = u32x4{0u, 0u, 0u, 0u};
+                    const int j = ks * SPAN + q * E;
+                    if (pos < d.n_active && j < d.r_max)
+                        vo[ks].piece[i] = *reinterpret_cast<const u32x4 *>(
+                            vp + (i * d.r_max + j) * int(sizeof(T)));
+                }
+        }
         // the first position of each group in the tile, one bit a lane
         const int before = __shfl_up(pr.group, 1, 16);
         uint32_t todo = uint32_t(__builtin_amdgcn_ballot_w64(
@@ -341,7 +358,7 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
                         if (ks * SPAN < rp[b]) {         // uniform
 #pragma unroll
                             for (int i = P - 1; i >= 0; --i)
-                                s4 = mma<T>(bf[b][j][ks], vo[ks][i], s4);
+                                s4 = mma<T>(bf[b][j][ks], vo[ks].piece[i], s4);
                         }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = mine ? acc[j][i] + s4[i] : acc[j][i];
@@ -867,54 +884,65 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
 }
 
 // ----------------------------------------------------------------- join -----
-// One wave per 16 tokens (with adapters: plan positions) x 16 G outputs of a
-// product in parts: the parts' sum, the delta, and the end of the outputs,
-// with nothing shared between waves.  A wave's chain of dependent loads is
-// what it waits for, so small waves, many of them resident, beat fewer that
-// share a tile through LDS (G 4 and the parts and groups dealt to 4 or 8
-// waves: 12.4 and 17.7 us for a decode batch's q/k/v, 66 and 69 for its
-// gated pair of mixed ranks).
+// One wave per 16 tokens (with adapters: plan positions) x 16 G columns of a
+// product in parts: the parts' sum and the delta.  With a gated pair gate's
+// and up's columns are two waves', which meet in LDS; else waves share
+// nothing.  A wave's chain of dependent loads is what it waits for, so small
+// waves, many of them resident, beat fewer that share a tile through LDS (64
+// columns, the parts and groups dealt to 4 or 8 waves: 12.4 and 17.7 us for
+// a decode batch's q/k/v, 66 and 69 for its gated pair of mixed ranks).
 template <typename T, bool GLU, int KS, int G>
 __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
-    constexpr int NR = GLU ? 2 : 1, N = 4 * G, Z = 4;
+    constexpr int NR = GLU ? 2 : 1, N = 4 * G, Z = 4, TILES = 4 / NR;   // column tiles a workgroup
+    __shared__ f32x4 up[GLU ? 2 * G : 1][kWaveSize];
     const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+    const int w = wave_id(), r = GLU ? w & 1 : 0, tile = w / NR;
     const int tiles_t = (a.T + 15) / 16;
     const int p0 = blockIdx.x % tiles_t * 16;
-    const int f0 = (blockIdx.x / tiles_t * 4 + wave_id()) * 16 * G;
-    if (f0 >= a.n) return;
+    const int f0 = (blockIdx.x / tiles_t * TILES + tile) * 16 * G;
     const int pos = p0 + n;
     const int t = pos < a.T ? (KS ? a.delta.order[pos] : pos) : -1;
-    float v[NR][N];
+    const int c0 = r * a.n + f0;                 // column before the activation
+    f32x4 s[G];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        const int c0 = r * a.n + f0;             // column before the activation
-        f32x4 s[G];
-#pragma unroll
-        for (int j = 0; j < G; ++j) s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < G; ++j) s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (f0 < a.n) {                              // uniform
         if constexpr (KS > 0) add_delta<T, G, KS>(a.delta, p0, c0, 0, 1, s);
         // the parts in order, Z of them in flight
         const float *p = a.partial + int64_t(t) * a.ldp + c0 + q * N;
         const int64_t step = int64_t(a.T) * a.ldp;
         for (int z = 0; z < a.splits; z += Z) {
-            u32x4 w[Z][G];
+            u32x4 v[Z][G];
 #pragma unroll
             for (int k = 0; k < Z; ++k)
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    w[k][j] = u32x4{0u, 0u, 0u, 0u};
+                    v[k][j] = u32x4{0u, 0u, 0u, 0u};
                     // (any alignment: the second half of a pair starts at column n)
                     if (t >= 0 && z + k < a.splits && c0 + q * N + 4 * j < a.wide)
-                        w[k][j] = *reinterpret_cast<const u32x4_any *>(p + (z + k) * step + 4 * j);
+                        v[k][j] = *reinterpret_cast<const u32x4_any *>(p + (z + k) * step + 4 * j);
                 }
 #pragma unroll
             for (int k = 0; k < Z; ++k)
 #pragma unroll
-                for (int j = 0; j < G; ++j) s[j] += __builtin_bit_cast(f32x4, w[k][j]);
+                for (int j = 0; j < G; ++j) s[j] += __builtin_bit_cast(f32x4, v[k][j]);
         }
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[r][k] = s[k / 4][k % 4];
     }
-    finish<T, GLU>(a, t, f0 + q * N, a.n - f0 - q * N, v[0], v[NR - 1]);
+    if constexpr (GLU) {
+        if (r == 1) {
+#pragma unroll
+            for (int j = 0; j < G; ++j) up[tile * G + j][lane] = s[j];
+        }
+        __syncthreads();
+        if (r == 1) return;
+    }
+    float v[N], u[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        v[k] = s[k / 4][k % 4];
+        u[k] = GLU ? up[tile * G + k / 4][lane][k % 4] : 0.f;
+    }
+    finish<T, GLU>(a, t, f0 + q * N, a.n - f0 - q * N, v, u);
 }
 
 // ------------------------------------------------------------- launches -----
@@ -923,7 +951,8 @@ dim3 grid_of(int units) { return dim3((units + kXcds - 1) / kXcds * kXcds); }
 // K-steps of the delta's largest rank, as the kernels are built for it
 template <typename T> int delta_steps(const LinearArgs &a) {
     if (!a.delta.order) return 0;
-    return a.delta.max_rpad <= 4 * Elem<T>::E ? 1 : LORA_MAX_RANK / (4 * Elem<T>::E);
+    return a.delta.max_rpad <= one_step_rank(sizeof(T) == 2 ? LORA_BF16 : LORA_F32)
+               ? 1 : LORA_MAX_RANK / (4 * Elem<T>::E);
 }
 
 template <typename T, bool GLU, int NW>
@@ -944,7 +973,8 @@ hipError_t rows_launch(const LinearArgs &a, hipStream_t s) {
 template <typename T, bool GLU> void join_launch(const LinearArgs &a, hipStream_t s) {
     constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E), GM = sizeof(T) == 2 ? 2 : 1;
     const int ks = delta_steps<T>(a), g = ks > 1 ? GM : 1;
-    const dim3 grid(((a.T + 15) / 16) * ((a.n + 64 * g - 1) / (64 * g))), block(256);
+    const int cols = (GLU ? 32 : 64) * g;        // outputs of a workgroup
+    const dim3 grid(((a.T + 15) / 16) * ((a.n + cols - 1) / cols)), block(256);
     if (ks == 0) hipLaunchKernelGGL((k_linear_join<T, GLU, 0, 1>), grid, block, 0, s, a);
     else if (ks == 1) hipLaunchKernelGGL((k_linear_join<T, GLU, 1, 1>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((k_linear_join<T, GLU, KM, GM>), grid, block, 0, s, a);

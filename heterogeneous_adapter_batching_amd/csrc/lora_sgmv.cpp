@@ -759,7 +759,7 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
     // block's rt_before counting within its own kind
     std::vector<lora::TileDesc> long_tiles, short_tiles;
     int32_t max_sblock = 0;
-    std::vector<int32_t> ssz, esz;
+    std::vector<int32_t> ssz, esz, row_rt, row_slot;
     auto add_group = [&](const std::vector<std::pair<int32_t, int32_t>> &rows, int32_t g,
                          const Slot *sl) {
         const int32_t base = int32_t(pl->token_order.size());
@@ -771,6 +771,8 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
         const int32_t smax = lg ? lora::kMaxBlockTokens : lora::kTile;
         const int32_t emax = lg ? lora::kMaxBlockTokens : lora::kDecodeBlockTokens;
         cut_sizes(int32_t(rows.size()), smax, &ssz);
+        row_rt.clear();
+        row_slot.clear();
         int32_t s0 = 0;
         std::vector<lora::TileDesc> &tiles = lg ? long_tiles : short_tiles;
         for (int32_t sn : ssz) {
@@ -787,6 +789,10 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
                 tiles.push_back(td);
             }
             max_sblock = std::max(max_sblock, sn);
+            for (int32_t i = 0; i < sn; ++i) {
+                row_rt.push_back(rt_before);
+                row_slot.push_back(i);
+            }
             cut_sizes(sn, emax, &esz);
             int32_t e0 = 0;
             for (int32_t en : esz) {
@@ -811,10 +817,19 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
             pl->token_sigma.push_back(rn ? rn->sigma : -1);
             pl->token_weight.push_back(rn ? rn->weight : 1.0f);
             pl->token_slot.push_back(rn ? rn->slot : -1);
-            pl->positions.push_back(
-                sl ? lora::PosRow{uint32_t(sl->off & 0xffffffffu), uint32_t(sl->off >> 32),
-                                  sl->r_pad, g}
-                   : lora::PosRow{0u, 0u, 0, -1});
+            lora::PosRow pr{};
+            pr.group = -1;
+            if (sl) {
+                const size_t at = pl->positions.size() - size_t(base);
+                pr.ext_lo = uint32_t(sl->off & 0xffffffffu);
+                pr.ext_hi = uint32_t(sl->off >> 32);
+                pr.r_pad = sl->r_pad;
+                pr.group = g;
+                pr.rt = row_rt[at];
+                pr.slot = row_slot[at];
+                pr.scale = sl->scale * (rn ? rn->weight : 1.0f);
+            }
+            pl->positions.push_back(pr);
             if (rn) pl->max_sigma = std::max(pl->max_sigma, rn->sigma);
         }
     };
@@ -1682,17 +1697,22 @@ uint64_t linear_v_bytes(const lora_pool *p, int32_t T, int32_t nproj, int32_t en
     return round_up(uint64_t(entry) * uint64_t(T) * uint64_t(nproj) * uint64_t(p->d.r_max), 256);
 }
 
-// The product's right operand of the delta: scale * (A x) of every plan
-// position with an adapter (short groups from the shrink's partials, long
-// ones from the prompt kernel's v).
+// The product's right operand of the delta, scale * (A x) of every plan
+// position with an adapter: the shrink's partials, which the product sums
+// itself, or (`formed`) formed by a launch from them and the prompt kernel's v.
 lora_status run_operand(const lora_pool *p, const lora_plan *pl, int32_t layer, int32_t nproj,
                         const int32_t *projs, const void *x, int64_t ldx, const CallCheck &cc,
-                        float *v, uint8_t *operand, hipStream_t hs) {
-    lora::OperandArgs a{};
+                        float *v, uint8_t *operand, bool formed, lora::DeltaArgs *da,
+                        hipStream_t hs) {
     const Partials pt = workspace_partials(pl);
-    lora_status st = run_shrink(p, pl, layer, nproj, projs, x, ldx, cc, hs, &a.c0, pt);
+    lora_status st = run_shrink(p, pl, layer, nproj, projs, x, ldx, cc, hs, &da->c0, pt);
     if (st != LORA_OK) return st;
     pl->part_long = false;
+    da->partial_bytes = uint32_t(std::min<uint64_t>(pt.bytes, lora::kMaxTensorBytes));
+    if (!formed) {
+        da->partial = pt.ptr;
+        return LORA_OK;
+    }
     PrefillIO io;
     io.mode = lora::kPrefillShrink;
     io.x = x;
@@ -1703,9 +1723,11 @@ lora_status run_operand(const lora_pool *p, const lora_plan *pl, int32_t layer, 
     st = run_prefill(p, pl, layer, nproj, projs, nullptr, cc, io, hs);
     if (st != LORA_OK) return st;
     const uint8_t *ws = static_cast<const uint8_t *>(pl->ws);
+    lora::OperandArgs a{};
+    a.c0 = da->c0;
     a.blocks = reinterpret_cast<const BlockDesc *>(ws + pl->lay.off_blocks);
     a.partial = pt.ptr;
-    a.partial_bytes = uint32_t(std::min<uint64_t>(pt.bytes, lora::kMaxTensorBytes));
+    a.partial_bytes = da->partial_bytes;
     a.v = v;
     a.tok_w = pl->weighted ? reinterpret_cast<const float *>(ws + pl->lay.off_tw) : nullptr;
     a.out = operand;
@@ -2006,7 +2028,9 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
         // position's scaled v as the product's operand
         float *v = static_cast<float *>(ws);
         uint8_t *operand = static_cast<uint8_t *>(ws) + linear_v_bytes(p, pl->T, nproj, 4);
-        st = run_operand(p, pl, layer, nproj, projs, x, ldx, cc, v, operand,
+        const bool formed = pl->prefill() || pl->max_rpad > lora::one_step_rank(d->dtype) ||
+                            (lp.kind == lora::kLinearTile && !lp.joined);
+        st = run_operand(p, pl, layer, nproj, projs, x, ldx, cc, v, operand, formed, &da,
                          static_cast<hipStream_t>(stream));
         if (st != LORA_OK) return st;
         const uint8_t *pw = static_cast<const uint8_t *>(pl->ws);

@@ -106,13 +106,17 @@ struct GroupRow {
 static_assert(sizeof(GroupRow) == 16, "GroupRow is one 16-byte load");
 
 // One plan position: its group (-1: no adapter) with the group's extent and
-// padded rank, so that a lane has them in one load.
+// padded rank, and where its row is in the shrink's partials (short groups:
+// first rank tile, token slot) with its scale (times its weight).
 struct PosRow {
     uint32_t ext_lo, ext_hi;
     int32_t r_pad;
     int32_t group;
+    int32_t rt, slot;
+    float scale;
+    int32_t pad;
 };
-static_assert(sizeof(PosRow) == 16, "PosRow is one 16-byte load");
+static_assert(sizeof(PosRow) == 32, "PosRow is two 16-byte loads");
 
 // What the debug build checks every unit against (see LORA_SGMV_DEBUG in
 // kernels.hip): the slab's bytes (every adapter block a unit addresses lies
