@@ -98,19 +98,6 @@ __device__ __forceinline__ int xcd_unit(int gs) {
     return (i / gs) * (kXcds * gs) + x * gs + (i % gs);
 }
 
-// Workgroup g runs on XCD g % kXcds; here each XCD takes one contiguous range
-// of ceil(units / kXcds) units, in order.  For the MFMA expand, whose units
-// run block by block (token slices, then projections and row chunks), the
-// units that read one token tile's shrink partials then share an L2, and so
-// do the blocks of one adapter, which read the same B rows: with units dealt
-// round-robin, a tile's partials were fetched once per XCD its units ran on
-// (the prefill q/k/v expand fetched 1.4x its bytes).  Indices past `units`
-// (at most kXcds - 1 of them, on the last XCDs) are idle.
-__device__ __forceinline__ int xcd_range_unit(int units) {
-    const int g = blockIdx.x;
-    return (g % kXcds) * ((units + kXcds - 1) / kXcds) + g / kXcds;
-}
-
 // Brings the whole kernel-argument block into the scalar cache in one
 // round: one dword of every 32 bytes, loaded together and waited for once.
 // The unit decode then reads its arguments in several dependent steps, each

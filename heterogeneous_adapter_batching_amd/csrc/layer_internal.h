@@ -14,8 +14,8 @@
 namespace lora {
 
 // ------------------------------------------------------------ block norm ----
-// One row of the residual stream per 1 (narrow rows), 4, 8 or 16 waves, held
-// in registers from its loads to its stores.
+// One row of the residual stream per 1 (narrow rows) to 16 waves, held in
+// registers from its loads to its stores.
 struct NormArgs {
     const void *h, *o;              // o null: no block output (h' = beta h)
     const void *post_w, *post_b;    // null: ones, zeros

@@ -368,13 +368,6 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
     }
 }
 
-// The plain remap of launch order to units: each XCD takes one contiguous
-// range, so that neighbouring units share an L2.
-__device__ __forceinline__ int xcd_range(int units) {
-    const int g = blockIdx.x;
-    return (g % kXcds) * ((units + kXcds - 1) / kXcds) + g / kXcds;
-}
-
 // ----------------------------------------------------------------- rows -----
 // One workgroup per 16 outputs (rows of W; with a gated pair 16 of gate and
 // the same 16 of up); wave w takes its share of K for all of them and all of
@@ -386,7 +379,7 @@ template <typename T, bool GLU, int KS, int NW>
 __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs a) {
     constexpr int E = Elem<T>::E, SPAN = 4 * E, NR = GLU ? 2 : 1, F = 4;
     __shared__ f32x4 red[NW][NR][kWaveSize];
-    const int unit = xcd_range(a.units);
+    const int unit = xcd_range_unit(a.units);
     if (unit >= a.units) return;                 // whole workgroup
     const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
     const int w = wave_id();
@@ -616,7 +609,7 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
     static_assert(!GLU || TJ % 2 == 0, "gate and up tiles in pairs");
     __shared__ __align__(1024) uint8_t lds[S * STAGE];
 
-    const int unit = xcd_range(a.units);
+    const int unit = xcd_range_unit(a.units);
     if (unit >= a.units) return;
     const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, q = lane >> 4;
     const int wave = wave_id();

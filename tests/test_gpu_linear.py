@@ -418,3 +418,174 @@ def test_refused_calls():
         with pytest.raises(err):
             call(**bad)
     assert torch.equal(call(), y)
+
+
+def test_sequence_of_a_decoder_layer():
+    """The operators as a decoder layer runs them around its attention (here
+    the identity on the value columns), captured into one graph and replayed
+    on new inputs: norms, the adapted q/k/v, o onto the stream through the
+    next norms, the gated MLP and its down projection.  Every stage is held to
+    its formula in 64 bits on the inputs the run gave it."""
+    import heterogeneous_adapter_batching_amd as hab
+    from test_gpu_norm import check as check_norm
+    h, kv, ffn, T = 512, 128, 1032, 150
+    dt = BF16
+    starts, ids = segments(11, T, 5, 9)
+    g = torch.Generator().manual_seed(11)
+    r = lambda *s, std=1.0, mean=0.0: (torch.randn(*s, generator=g) * std + mean).to(dt).cuda()  # noqa: E731
+    shapes = {"q": (h, h), "k": (h, kv), "v": (h, kv), "o": (kv, h), "gate": (h, ffn),
+              "up": (h, ffn), "down": (ffn, h)}
+    pool = hab.Pool(1, [s[0] for s in shapes.values()], [s[1] for s in shapes.values()], 64,
+                    "bf16", slab_bytes=32 << 20)
+    ads = {}
+    for a, rank in enumerate((8, 16, 64, 24, 40)):
+        A = [r(1, rank, k, std=1 / math.sqrt(3 * k)) for k, _ in shapes.values()]
+        B = [r(1, n, rank, std=0.05) for _, n in shapes.values()]
+        ads[a] = (A, B)
+        pool.register(a, rank, 2.0, A, B)
+    plan = hab.Plan(pool, T, starts, ids).upload(max_proj=3)
+    w = {"qkv": r(h + 2 * kv, h, std=1 / math.sqrt(h)), "o": r(h, kv, std=1 / math.sqrt(kv)),
+         "gu": r(2 * ffn, h, std=1 / math.sqrt(h)), "down": r(h, ffn, std=1 / math.sqrt(ffn))}
+    n1, n2, n3, post, gate = (r(h, std=0.1, mean=1.0) for _ in range(5))
+    stream, first = r(T, h), {}
+
+    def layer():
+        s = {}
+        _, s["x1"] = hab.block_norm(stream, pre_weight=n1)
+        s["qkv"] = hab.sgmv_linear(pool, plan, 0, (0, 1, 2), (0, h, h + kv), s["x1"], w["qkv"])
+        s["val"] = s["qkv"][:, h + kv:]
+        s["att"] = hab.sgmv_linear(pool, plan, 0, (3,), (0,), s["val"], w["o"])
+        s["h1"], s["x2"] = hab.block_norm(stream, s["att"], post="rms", post_weight=post, gate=gate,
+                                          alpha=0.7, pre_weight=n2)
+        s["mid"] = hab.sgmv_linear(pool, plan, 0, (4, 5), (0, ffn), s["x2"], w["gu"], act="silu",
+                                   glu=True)
+        s["h2"] = hab.sgmv_linear(pool, plan, 0, (6,), (0,), s["mid"], w["down"], residual=s["h1"])
+        _, s["x3"] = hab.block_norm(s["h2"], pre="layer", pre_weight=n3)
+        return s
+
+    def delta(x, wide, projs, offs):
+        z = torch.zeros(T, wide, dtype=torch.float64, device="cuda")
+        mag = torch.zeros_like(z)
+        for s, i in enumerate(ids):
+            lo, hi = int(starts[s]), int(starts[s + 1])
+            if i < 0:
+                continue
+            for p, off in zip(projs, offs):
+                A, B = (m[p][0].double() for m in ads[int(i)])
+                n = B.shape[0]
+                z[lo:hi, off:off + n] += 2 * (x[lo:hi].double() @ A.t()) @ B.t()
+                mag[lo:hi, off:off + n] += 2 * (x[lo:hi].double().abs() @ A.abs().t()) @ B.abs().t()
+        return z, mag
+
+    def check_product(what, got, x, wt, projs, offs, act="none", glu=False, residual=None):
+        k = x.shape[1]
+        d, dmag = delta(x, wt.shape[0], projs, offs)
+        z = x.double() @ wt.double().t() + d
+        dz = (k / 4 + 256) * U * (x.double().abs() @ wt.double().abs().t() + dmag)
+        ref = end64(z, act, glu, residual)
+        if glu:
+            n = z.shape[1] // 2
+            a = act64(z[:, :n], act)
+            da = 1.13 * dz[:, :n] + 2.0 ** -19 * z[:, :n].abs()
+            err = da * (z[:, n:].abs() + dz[:, n:]) + a.abs() * dz[:, n:] + U * (a * z[:, n:]).abs()
+        else:
+            err = dz
+        if residual is not None:
+            err = err + 2 * U * (ref.abs() + residual.double().abs())
+        bad = ((got.double() - ref).abs() / (err + torch.finfo(dt).eps / 2 * (ref.abs() + err))).max()
+        print(f"[layer] {what}: {bad.item():.3f} of the bound", flush=True)
+        assert bad <= 1.0, what
+
+    def check_all(s):
+        check_norm(stream, None, dict(pre_weight=n1), stream, s["x1"], "first norm")
+        check_product("qkv", s["qkv"], s["x1"], w["qkv"], (0, 1, 2), (0, h, h + kv))
+        check_product("o", s["att"], s["val"], w["o"], (3,), (0,))
+        check_norm(stream, s["att"], dict(post="rms", post_weight=post, gate=gate, alpha=0.7,
+                                          pre_weight=n2), s["h1"], s["x2"], "both norms")
+        check_product("gate and up", s["mid"], s["x2"], w["gu"], (4, 5), (0, ffn), "silu", True)
+        check_product("down", s["h2"], s["mid"], w["down"], (6,), (0,), residual=s["h1"])
+        check_norm(s["h2"], None, dict(pre="layer", pre_weight=n3), s["h2"], s["x3"], "last norm")
+
+    first = layer()
+    check_all(first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = layer()
+    for _ in range(3):
+        stream.copy_(r(T, h))
+        eager = layer()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in out:
+            assert torch.equal(out[name], eager[name]), name
+    check_all(out)
+
+
+def test_two_streams_at_once():
+    """Products and norms on two streams at once, each with its own plan and
+    workspaces, give the bits of the calls alone."""
+    import heterogeneous_adapter_batching_amd as hab
+    T = 96
+    runs = []
+    for seed in (21, 22):
+        starts, ids = segments(seed, T, 4, 3)
+        m = Adapted(seed, T, 520, [264], [8, 16, 64, 32], ids, starts)
+        g = torch.Generator().manual_seed(seed)
+        x, w = torch.randn(T, 520, generator=g).to(BF16).cuda(), torch.randn(264, 520, generator=g).to(BF16).cuda()
+        want = hab.sgmv_linear(m.pool, m.plan, 0, [0], [0], x, w, act="silu")
+        runs.append((m, x, w, want, torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for m, x, w, _, s, got in runs:
+            got.append(hab.sgmv_linear(m.pool, m.plan, 0, [0], [0], x, w, act="silu", stream=s))
+    torch.cuda.synchronize()
+    for _, _, _, want, _, got in runs:
+        assert all(torch.equal(y, want) for y in got)
+
+
+def test_rows_behind_a_padded_batch():
+    """A batch padded to a captured size: rows without a segment of their own
+    take no adapter, and the rows behind num_tokens are left alone."""
+    import heterogeneous_adapter_batching_amd as hab
+    T, pad = 37, 64
+    starts, ids = segments(31, T, 3, 4)
+    m = Adapted(31, T, 136, [72], [8, 24, 64], ids, starts)
+    g = torch.Generator().manual_seed(3)
+    xb, w = ints(g, pad, 136, top=1), ints(g, 72, 136, top=1)
+    yb = torch.full((pad, 72), 3.0, dtype=BF16, device="cuda")
+    hab.sgmv_linear(m.pool, m.plan, 0, [0], [0], xb[:T], w, y=yb[:T])
+    assert bool((yb[T:] == 3.0).all())
+    padded = hab.Plan(m.pool, pad, np.append(starts, pad), np.append(ids, -1)).upload(1)
+    y = hab.sgmv_linear(m.pool, padded, 0, [0], [0], xb, w)
+    assert torch.equal(y[:T], yb[:T])
+    assert torch.equal(y[T:], (xb[T:].double() @ w.double().t()).to(BF16))
+
+
+@pytest.mark.parametrize("rmax, granule", [(8, 8), (16, 16), (48, 16)])
+def test_adapted_pool_shapes(rmax, granule):
+    """Pools of other largest ranks and rank granules."""
+    import heterogeneous_adapter_batching_amd as hab
+    for dtype in (BF16, F32):
+        g = torch.Generator().manual_seed(rmax)
+        T, k, n = 30, 72, 40
+        pool = hab.Pool(2, [k, 64], [n, 8], rmax, NAMES[dtype], rank_granule=granule, slab_bytes=4 << 20)
+        ads = []
+        for a, rank in enumerate((1, rmax // 2, rmax)):
+            A = [ints(g, 2, rank, i, top=1, dtype=dtype) for i in (k, 64)]
+            B = [ints(g, 2, o, rank, top=1, dtype=dtype) for o in (n, 8)]
+            pool.register(a, rank, 1.0, A, B)
+            ads.append((A, B))
+        ids = np.arange(T, dtype=np.int32) % 4 - 1
+        plan = hab.Plan(pool, T, np.arange(T + 1, dtype=np.int32), ids).upload(1)
+        x, w = ints(g, T, k, top=1, dtype=dtype), ints(g, n + 5, k, top=1, dtype=dtype)
+        y = hab.sgmv_linear(pool, plan, 1, [0], [5], x, w)
+        z = x.double() @ w.double().t()
+        for t, a in enumerate(ids):
+            if a >= 0:
+                z[t, 5:] += (x[t].double() @ ads[a][0][0][1].double().t()) @ ads[a][1][0][1].double().t()
+        assert torch.equal(y, z.to(dtype))
