@@ -592,10 +592,20 @@ template <typename T, int HALVES> struct DeltaTiles {
 
 // One workgroup per BT tokens x BN rows of W (with a gated pair BN / 2 of
 // gate and the same BN / 2 of up), WT x WN waves, over the K tiles of its
-// split.  A K tile is 128 bytes of every row; S of them are in LDS or on
-// their way.  A row's 8 vectors are stored rotated by (row / 2) % 8
-// (exclusive or), so that the 16 rows a fragment read touches spread over
-// all banks.  W's rows sit in LDS in the order that gives a lane consecutive
+// part.  A K tile is 128 bytes of every row, whole cache lines; S of them are
+// in LDS or on their way.  A row's 8 vectors are stored exchanged by
+// (row / 2) % 8 (exclusive or), so that the 16 rows a fragment read touches
+// spread over all banks (no conflicts counted).
+// What bounds it: prompts the matrix cores, at the clock they leave (1.7 GHz
+// under this load: a 256 x 256 tile keeps them busy three quarters of its
+// cycles, LDS reads most of the rest); 4096 x 4096 x 4096 bf16 107 us, 4096
+// tokens through a gated 28672 x 4096 pair 714 us, 1.35 PFLOP/s.  8 waves of
+// 128 x 64 beat 4 of 128 x 128 (713 against 907 us), whose single wave a SIMD
+// has nothing to run at a barrier, and the products spelled out between reads
+// and copies beat the compiler's order (833 against 890).  Decode batches are
+// bound by W from HBM: 128 x 4096 x 14336 33 us in 8 parts, 3.5 TB/s; their
+// K tiles rotated by workgroup, or dealt in turn to the parts, measured the
+// same and a fifth slower.  W's rows sit in LDS in the order that gives a lane consecutive
 // outputs: LDS row 16 j + r of a wave's share is output (r / 4) 4 G + 4 j +
 // r % 4, G tiles of 16 wide.
 template <typename T, int BT, int BN, int WT, int WN, int S, bool GLU, bool SPLIT, bool ADAPT>

@@ -2022,7 +2022,12 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
                              linear_v_bytes(p, pl->T, nproj, lora::operand_bytes(d->dtype));
     st = lora::check_linear(c, v_bytes + lp.ws_bytes);
     if (st != LORA_OK) return st;
+    const uintptr_t wl = reinterpret_cast<uintptr_t>(ws), pw0 = reinterpret_cast<uintptr_t>(pl->ws);
+    if (wl < pw0 + pl->lay.ws_bytes && pw0 < wl + v_bytes + lp.ws_bytes)
+        return fail(LORA_EINVAL, "the workspace overlaps the plan's");
     lora::DeltaArgs da{};
+    const hipError_t e = lora::debug_word(&da.dbg_word);
+    if (e != hipSuccess) return hip_fail(e, "debug word");
     if (pl->nb_act > 0) {
         // v (float32, by plan position) of the long groups, then every
         // position's scaled v as the product's operand
@@ -2049,8 +2054,6 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
         da.nproj = nproj;
         da.r_max = p->d.r_max;
         da.dbg = debug_bounds(p, pl);
-        const hipError_t e = lora::debug_word(&da.dbg_word);
-        if (e != hipSuccess) return hip_fail(e, "debug word");
     }
     return lora::run_linear(c, lp, static_cast<uint8_t *>(ws) + v_bytes, da,
                             static_cast<hipStream_t>(stream));

@@ -666,8 +666,10 @@ lora_status frozen_linear(const lora_linear_desc *d, const void *x, int64_t ldx,
  * projections; a merge plan and one with cores are refused.  Tokens without
  * an adapter get the plain product.  The pool's dtype is d's, h_in of the
  * listed projections is d->k, and their slices lie in the n (2 n with glu)
- * columns of z.  v = A x goes through `ws` (sgmv_linear_workspace_bytes); the
- * shrink uses the plan's workspace as sgmv_shrink does.  Other arguments and
+ * columns of z.  v = A x goes through `ws` (sgmv_linear_workspace_bytes, apart
+ * from the plan's workspace); the shrink leaves its partials in the plan's
+ * workspace as sgmv_shrink does, and the product may read them there, so
+ * calls that share a plan's workspace must not overlap.  Other arguments and
  * errors as frozen_linear and sgmv_shrink (x spans at most 2 GiB). */
 uint64_t sgmv_linear_workspace_bytes(const lora_pool *p, const lora_linear_desc *d, int32_t nproj);
 lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, int32_t nproj,

@@ -413,7 +413,7 @@ def test_refused_calls():
                      (dict(x=x.float(), w=w.float()), hab.LoraError), (dict(w=w.float()), TypeError),
                      (dict(w=w[:, :56]), ValueError), (dict(glu=True, w=w[:63]), ValueError),
                      (dict(ws=torch.empty(256, dtype=torch.uint8, device="cuda")), hab.LoraError),
-                     (dict(y=x), hab.LoraError), (dict(act="sin"), ValueError),
+                     (dict(ws=m.plan.ws), hab.LoraError), (dict(y=x), hab.LoraError), (dict(act="sin"), ValueError),
                      (dict(residual=x[:, :63]), ValueError)):
         with pytest.raises(err):
             call(**bad)
