@@ -256,9 +256,9 @@ template <typename T> __global__ __launch_bounds__(256) void k_operand(const Ope
 }
 
 // ---------------------------------------------------------------- delta -----
-// Adds the delta to the accumulators of 16 plan positions: rows of the left
-// operand are outputs f(j, r) = f0 + (r / 4) 4 G + 4 j + r % 4, so a lane
-// holds outputs f0 + 4 G q .. + 4 G of its position.  Positions are in plan
+// Adds the delta to the accumulators of 16 plan positions and 16 G outputs,
+// in order (row r of tile j is output f0 + 16 j + r: neighbouring rows of B
+// are what its block keeps together).  Positions are in plan
 // order, so a group's are neighbours: each group's B rows multiply every
 // position's operand and are kept in the columns of the group's own (so one
 // adapter's infinities stay with its tokens).  Of `nw` waves that share the
@@ -338,7 +338,7 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
                 const BLayout bl = b_layout(rp[b], int(sizeof(T)));
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    const int o = f0 + (n >> 2) * 4 * G + 4 * j + (n & 3) - lo;
+                    const int o = f0 + 16 * j + n - lo;
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
                         const int v = ks * 4 + q;
@@ -603,9 +603,12 @@ template <typename T, int HALVES> struct DeltaTiles {
 // 128 x 64 beat 4 of 128 x 128 (713 against 907 us), whose single wave a SIMD
 // has nothing to run at a barrier, and the products spelled out between reads
 // and copies beat the compiler's order (833 against 890).  Decode batches are
-// bound by W from HBM: 128 x 4096 x 14336 33 us in 8 parts, 3.5 TB/s; their
-// K tiles rotated by workgroup, or dealt in turn to the parts, measured the
-// same and a fifth slower.  W's rows sit in LDS in the order that gives a lane consecutive
+// bound by what enters the CUs: 43 bytes a nanosecond each whatever the tile,
+// 11 TB/s in all, of which x is half where 128 tokens meet 128 rows (128 x
+// 4096 x 14336 33 us in 8 parts, W at 3.5 TB/s).  K tiles rotated by
+// workgroup or of 256 bytes a row measured the same, dealt in turn to the
+// parts a fifth slower, streaming loads of W 1 to 4% faster for one token
+// tile (not taken: where token tiles share W it has to stay in L2).  W's rows sit in LDS in the order that gives a lane consecutive
 // outputs: LDS row 16 j + r of a wave's share is output (r / 4) 4 G + 4 j +
 // r % 4, G tiles of 16 wide.
 template <typename T, int BT, int BN, int WT, int WN, int S, bool GLU, bool SPLIT, bool ADAPT>
@@ -896,7 +899,7 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
 // a decode batch's q/k/v, 66 and 69 for its gated pair of mixed ranks).
 template <typename T, bool GLU, int KS, int G>
 __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
-    constexpr int NR = GLU ? 2 : 1, N = 4 * G, Z = 4, TILES = 4 / NR;   // column tiles a workgroup
+    constexpr int NR = GLU ? 2 : 1, Z = 4, TILES = 4 / NR;   // column tiles a workgroup
     __shared__ f32x4 up[GLU ? 2 * G : 1][kWaveSize];
     const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
     const int w = wave_id(), r = GLU ? w & 1 : 0, tile = w / NR;
@@ -912,7 +915,7 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
     if (f0 < a.n) {                              // uniform
         if constexpr (KS > 0) add_delta<T, G, KS>(a.delta, p0, c0, 0, 1, s);
         // the parts in order, Z of them in flight
-        const float *p = a.partial + int64_t(t) * a.ldp + c0 + q * N;
+        const float *p = a.partial + int64_t(t) * a.ldp + c0 + q * 4;
         const int64_t step = int64_t(a.T) * a.ldp;
         for (int z = 0; z < a.splits; z += Z) {
             u32x4 v[Z][G];
@@ -922,8 +925,8 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
                 for (int j = 0; j < G; ++j) {
                     v[k][j] = u32x4{0u, 0u, 0u, 0u};
                     // (any alignment: the second half of a pair starts at column n)
-                    if (t >= 0 && z + k < a.splits && c0 + q * N + 4 * j < a.wide)
-                        v[k][j] = *reinterpret_cast<const u32x4_any *>(p + (z + k) * step + 4 * j);
+                    if (t >= 0 && z + k < a.splits && c0 + q * 4 + 16 * j < a.wide)
+                        v[k][j] = *reinterpret_cast<const u32x4_any *>(p + (z + k) * step + 16 * j);
                 }
 #pragma unroll
             for (int k = 0; k < Z; ++k)
@@ -939,13 +942,14 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
         __syncthreads();
         if (r == 1) return;
     }
-    float v[N], u[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        v[k] = s[k / 4][k % 4];
-        u[k] = GLU ? up[tile * G + k / 4][lane][k % 4] : 0.f;
+    for (int j = 0; j < G; ++j) {
+        const f32x4 u4 = GLU ? up[GLU ? tile * G + j : 0][lane] : f32x4{0.f, 0.f, 0.f, 0.f};
+        float v[4] = {s[j][0], s[j][1], s[j][2], s[j][3]};
+        float u[4] = {u4[0], u4[1], u4[2], u4[3]};
+        const int f = f0 + 16 * j + 4 * q;
+        finish<T, GLU>(a, t, f, a.n - f, v, u);
     }
-    finish<T, GLU>(a, t, f0 + q * N, a.n - f0 - q * N, v, u);
 }
 
 // ------------------------------------------------------------- launches -----
@@ -969,12 +973,12 @@ hipError_t rows_launch(const LinearArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Outputs of a join wave: 16, and 32 for bf16 adapters beyond one K-step,
-// whose operand (6 vectors a lane) then serves twice the rows of B (a gated
-// decode batch of ranks 8 to 64: 43 us against 55; rank 16 q/k/v 13.4
-// against 12.7).
+// Outputs of a join wave: 16, and 64 for bf16 adapters beyond one K-step,
+// whose operand (6 vectors a lane) then serves more rows of B (a gated decode
+// batch of ranks 8 to 64: 53.6, 42.2 and 40.7 us with 16, 32 and 64; rank 16
+// q/k/v 12.7 us with 16, 13.4 with 32).
 template <typename T, bool GLU> void join_launch(const LinearArgs &a, hipStream_t s) {
-    constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E), GM = sizeof(T) == 2 ? 2 : 1;
+    constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E), GM = sizeof(T) == 2 ? 4 : 1;
     const int ks = delta_steps<T>(a), g = ks > 1 ? GM : 1;
     const int cols = (GLU ? 32 : 64) * g;        // outputs of a workgroup
     const dim3 grid(((a.T + 15) / 16) * ((a.n + cols - 1) / cols)), block(256);
