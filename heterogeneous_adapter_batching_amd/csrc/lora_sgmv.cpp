@@ -1713,15 +1713,18 @@ lora_status run_operand(const lora_pool *p, const lora_plan *pl, int32_t layer, 
         da->partial = pt.ptr;
         return LORA_OK;
     }
-    PrefillIO io;
-    io.mode = lora::kPrefillShrink;
-    io.x = x;
-    io.ldx = ldx;
-    io.v = v;
-    io.ldv = int64_t(nproj) * p->d.r_max;
-    io.v_by_pos = true;
-    st = run_prefill(p, pl, layer, nproj, projs, nullptr, cc, io, hs);
-    if (st != LORA_OK) return st;
+    // (the prompt kernel takes up to 3 projections a launch)
+    for (int32_t p0 = 0; p0 < nproj; p0 += 3) {
+        PrefillIO io;
+        io.mode = lora::kPrefillShrink;
+        io.x = x;
+        io.ldx = ldx;
+        io.v = v + int64_t(p0) * p->d.r_max;
+        io.ldv = int64_t(nproj) * p->d.r_max;
+        io.v_by_pos = true;
+        st = run_prefill(p, pl, layer, std::min(nproj - p0, 3), projs + p0, nullptr, cc, io, hs);
+        if (st != LORA_OK) return st;
+    }
     const uint8_t *ws = static_cast<const uint8_t *>(pl->ws);
     lora::OperandArgs a{};
     a.c0 = da->c0;

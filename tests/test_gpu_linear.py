@@ -310,6 +310,27 @@ def test_adapted_long_groups():
         run_adapted(m, 3, 328, [0, 264], what="long groups")
 
 
+@pytest.mark.parametrize("opts", [dict(long_group=1, long_batch=1), dict(long_group=6, long_batch=12),
+                                  dict(long_group=10 ** 6), dict(shrink_groups=4096)])
+@pytest.mark.parametrize("T", [7, 60, 300])
+def test_adapted_plan_options(T, opts):
+    """Plans whose groups are long or short by other thresholds, beside each
+    other, at ranks of one K-step and more; many chunks of the shrink."""
+    starts, ids = segments(T + 40, T, 4, 8)
+    for ranks in ((8, 16, 24, 32), (8, 64, 48, 16)):
+        for dtype in (BF16, F32):
+            m = Adapted(T, T, 1032, [136, 72], ranks, ids, starts, dtype, opts=opts)
+            run_adapted(m, T, 208, [0, 136], what=f"{opts}")
+
+
+def test_adapted_many_projections():
+    """Five projections in one call, short groups and long ones."""
+    for T, longest in ((40, 3), (1400, 500)):
+        starts, ids = segments(T, T, 3, longest)
+        m = Adapted(T, T, 72, [8, 40, 16, 24, 64], [16, 8, 40], ids, starts)
+        run_adapted(m, T, 152, [0, 8, 48, 64, 88], what="five projections")
+
+
 def test_adapted_layers_weights_and_subsets():
     T = 90
     starts, ids = segments(8, T, 4, 5)
