@@ -465,11 +465,18 @@ __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs
 // wait for every copy before the next LDS read, and the kernel counts them
 // itself.  Out-of-range lanes write zeros.  (The wait states cover a resource
 // word that a vector instruction wrote just before: 5; m0 needs 1.)
+// ONCE: the bytes are read by no other workgroup, and streamed past the L2.
+template <bool ONCE = false>
 __device__ __forceinline__ void copy_to_lds(u32x4 rsrc, uint32_t voff, uint32_t soff,
                                             uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds),
-                 "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory");
+    if constexpr (ONCE)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                     ::"s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     ::"s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                     : "memory");
 }
 template <int N> __device__ __forceinline__ void wait_copies() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -607,11 +614,16 @@ template <typename T, int HALVES> struct DeltaTiles {
 // 11 TB/s in all, of which x is half where 128 tokens meet 128 rows (128 x
 // 4096 x 14336 33 us in 8 parts, W at 3.5 TB/s).  K tiles rotated by
 // workgroup or of 256 bytes a row measured the same, dealt in turn to the
-// parts a fifth slower, streaming loads of W 1 to 4% faster for one token
-// tile (not taken: where token tiles share W it has to stay in L2).  W's rows sit in LDS in the order that gives a lane consecutive
-// outputs: LDS row 16 j + r of a wave's share is output (r / 4) 4 G + 4 j +
-// r % 4, G tiles of 16 wide.
-template <typename T, int BT, int BN, int WT, int WN, int S, bool GLU, bool SPLIT, bool ADAPT>
+// parts a fifth slower.  ONCE (one token tile: a row of W is one workgroup's)
+// streams W past the L2, which keeps x there and leaves nothing behind for the
+// next product's W to push out: in a loop over changing weights 36.7 us
+// against 41.5 with the join (128 x 4096 x 14336), 124 against 131 (the gated
+// batch of 256 with adapters); where token tiles share W it has to stay.
+// W's rows sit in LDS in the order that gives a lane consecutive outputs: LDS
+// row 16 j + r of a wave's share is output (r / 4) 4 G + 4 j + r % 4, G tiles
+// of 16 wide.
+template <typename T, int BT, int BN, int WT, int WN, int S, bool GLU, bool SPLIT, bool ADAPT,
+          bool ONCE = false>
 __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearArgs a) {
     constexpr int NW = WT * WN, NTH = NW * kWaveSize;
     constexpr int TI = BT / WT / 16, TJ = BN / WN / 16, G = GLU ? TJ / 2 : TJ;
@@ -683,8 +695,8 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
         if constexpr (at < XL)
             copy_to_lds(xr, in ? xo[at] : kOOB, soff, base + uint32_t(at * NTH * 16));
         else
-            copy_to_lds(up_rows(at - XL) ? wr2 : wr, in ? wo[at - XL] : kOOB, soff,
-                        base + uint32_t(BT * kKBytes + (at - XL) * NTH * 16));
+            copy_to_lds<ONCE>(up_rows(at - XL) ? wr2 : wr, in ? wo[at - XL] : kOOB, soff,
+                              base + uint32_t(BT * kKBytes + (at - XL) * NTH * 16));
     };
     auto fetch = [&](int kt, int st) {
         each<XL + WL>([&](auto at) { fetch_one(kt, st, at); });
@@ -996,23 +1008,32 @@ hipError_t rows_dispatch(const LinearArgs &a, hipStream_t s) {
     return rows_launch<T, GLU, 4>(a, s);
 }
 
+template <typename T, int BT, int BN, int WT, int WN, int S, bool GLU>
+void direct_launch(const LinearArgs &a, dim3 grid, dim3 block, hipStream_t s) {
+    if (a.delta.order)
+        hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, GLU, false, true>), grid, block, 0, s, a);
+    else if (a.tiles_t == 1)
+        hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, GLU, false, false, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, GLU, false, false>), grid, block, 0, s, a);
+}
+
 template <typename T, int BT, int BN, int WT, int WN, int S>
 hipError_t tile_launch(const LinearPlan &pl, bool glu, const LinearArgs &a, hipStream_t s) {
     const dim3 grid = grid_of(a.units), block(WT * WN * 64);
-    const bool adapt = a.delta.order != nullptr;
-    if (pl.joined) {
-        hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, true, false>), grid, block, 0, s, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        if (glu) join_launch<T, true>(a, s);
-        else join_launch<T, false>(a, s);
-    } else if (glu) {
-        if (adapt) hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, true, false, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, true, false, false>), grid, block, 0, s, a);
-    } else {
-        if (adapt) hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, false, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, false, false>), grid, block, 0, s, a);
+    if (!pl.joined) {
+        if (glu) direct_launch<T, BT, BN, WT, WN, S, true>(a, grid, block, s);
+        else direct_launch<T, BT, BN, WT, WN, S, false>(a, grid, block, s);
+        return hipGetLastError();
     }
+    if (a.tiles_t == 1)
+        hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, true, false, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, true, false>), grid, block, 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (glu) join_launch<T, true>(a, s);
+    else join_launch<T, false>(a, s);
     return hipGetLastError();
 }
 
