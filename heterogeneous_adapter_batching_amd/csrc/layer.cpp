@@ -72,18 +72,20 @@ namespace lora {
 // What the plan of a product chooses from, and what it goes by: the time of
 // one K tile (128 bytes of every row) of one workgroup with a CU to itself,
 // measured on MI355X with W from HBM (bf16 over 1024..28672 rows of W, K 4096
-// and 14336, 17..4096 tokens; float32 is bound by its matrix rate).  Small
-// tiles cost little each and keep every CU busy; large ones read less per
-// product.  At 128 x 4096 x 14336 (bf16) the plan's 64 x 128 tiles in 4
-// splits take 36 us, 256 x 128 in 2 splits 85, 128 x 128 unsplit 140; at
-// 4096 x 4096 x 4096 256 x 256 takes 102 and 128 x 128 160.
+// and 14336, 17..4096 tokens; float32 is bound by its matrix rate), and the
+// stages that fill before the first.  Small tiles cost little each and keep
+// every CU busy; large ones read less per product.  Estimated and measured
+// (bf16, us, without the launch): 128 x 4096 x 6144 in 2 parts of 128 x 64
+// 23.0 and 21.5, in 4 of 128 x 128 23.1 and 23.4; 1024 x 4096 x 4096 in 2
+// parts of 256 x 128 55 and 48, unsplit 128 x 128 58 and 49; 4096 x 4096 x
+// 4096 256 x 256 99 and 102, 128 x 128 231 and 216.
 struct TileCost {
-    int bt, bn;
+    int bt, bn, stages;
     float us[2];                 // float32, bf16 (0: not built)
 };
-constexpr TileCost kTiles[] = {{32, 64, {0.35f, 0.30f}},   {64, 128, {0.85f, 0.55f}},
-                               {128, 64, {0.f, 0.55f}},    {128, 128, {1.70f, 0.80f}},
-                               {256, 128, {0.f, 0.95f}},   {256, 256, {0.f, 1.50f}}};
+constexpr TileCost kTiles[] = {
+    {32, 64, 4, {0.35f, 0.30f}},  {64, 128, 4, {0.85f, 0.55f}},  {128, 64, 4, {0.f, 0.52f}},
+    {128, 128, 4, {1.70f, 0.85f}}, {256, 128, 3, {0.f, 0.95f}}, {256, 256, 2, {0.f, 1.50f}}};
 constexpr int kCus = 256;
 // A launch more (the join), and partial sums written and read at about this
 // rate (TB/s = bytes / us / 1e6).
@@ -120,7 +122,7 @@ Choice direct(int dtype, int T, int n, int k, bool glu, int groups, int max_rpad
         if (us == 0.f) continue;
         const int64_t tt = (T + t.bt - 1) / t.bt;
         const int feat = glu ? t.bn / 2 : t.bn;              // gate and up rows in pairs
-        float one = float(nk) * us;
+        float one = float(nk + t.stages) * us;
         if (groups) one += (float(groups) / float(tt) + 1.f) * float(per * (glu ? 2 : 1)) * kDeltaTileUs;
         c.offer(rounds(tt * ((int64_t(n) + feat - 1) / feat)) * one, t.bt, t.bn, 1, false, nk);
     }
@@ -139,7 +141,7 @@ Choice joined(int dtype, int T, int64_t wide, int k, int least) {
             const int kt = (nk + want - 1) / want;
             if (want > 1 && kt < 4) break;                   // too short to fill the pipeline
             const int splits = (nk + kt - 1) / kt;
-            c.offer(rounds(tiles * splits) * float(kt) * us + kJoinUs +
+            c.offer(rounds(tiles * splits) * float(kt + t.stages) * us + kJoinUs +
                         8.f * float(splits) * float(T) * float(wide) / kPartialBytesPerUs,
                     t.bt, t.bn, splits, true, kt);
         }

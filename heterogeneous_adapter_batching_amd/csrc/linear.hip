@@ -612,7 +612,7 @@ template <typename T, int HALVES> struct DeltaTiles {
 // and copies beat the compiler's order (833 against 890).  Decode batches are
 // bound by what enters the CUs: 43 bytes a nanosecond each whatever the tile,
 // 11 TB/s in all, of which x is half where 128 tokens meet 128 rows (128 x
-// 4096 x 14336 33 us in 8 parts, W at 3.5 TB/s).  K tiles rotated by
+// 4096 x 14336 33 us in 8 parts of 128 x 128, W at 3.5 TB/s).  K tiles rotated by
 // workgroup or of 256 bytes a row measured the same, dealt in turn to the
 // parts a fifth slower.  ONCE (one token tile: a row of W is one workgroup's)
 // streams W past the L2, which keeps x there and leaves nothing behind for the
