@@ -603,9 +603,9 @@ template <typename T, int HALVES> struct DeltaTiles {
 // in LDS or on their way.  A row's 8 vectors are stored exchanged by
 // (row / 2) % 8 (exclusive or), so that the 16 rows a fragment read touches
 // spread over all banks (no conflicts counted).
-// What bounds it: prompts the matrix cores, at the clock they leave (1.7 GHz
-// under this load: a 256 x 256 tile keeps them busy three quarters of its
-// cycles, LDS reads most of the rest); 4096 x 4096 x 4096 bf16 107 us, 4096
+// What bounds it: prompts the matrix cores, at the clock they leave (1.7 to
+// 1.9 GHz under this load: a 256 x 256 tile keeps them busy two thirds of its
+// cycles; LDS reads and copies fill as many); 4096 x 4096 x 4096 bf16 107 us, 4096
 // tokens through a gated 28672 x 4096 pair 714 us, 1.35 PFLOP/s.  8 waves of
 // 128 x 64 beat 4 of 128 x 128 (713 against 907 us), whose single wave a SIMD
 // has nothing to run at a barrier, and the products spelled out between reads
