@@ -78,12 +78,16 @@ def _enqueue(fn, args, device, stream):
 
 
 def _new(shape, dtype, device, stream):
-    """A tensor for a launch on `stream` (None: the current one).  Freed memory
-    is given out again in the order of the stream it was made on, so another
-    one's use is noted."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """A tensor for a launch on `stream` (None: the current one).  Memory is
+    given out again in the order of the stream it was made on, with its last
+    owner's work perhaps still queued there, so it is made on the launch's own
+    stream; and it goes back only behind the uses that the caller's current
+    stream has of it by then."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
