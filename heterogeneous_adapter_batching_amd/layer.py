@@ -15,6 +15,7 @@ import torch
 from ._lib import (ACTS, GATE_ACTS, LORA_BF16, LORA_F32, NORMS, LinearDesc, NormDesc, check, load)
 from .api import _DTYPES, _offsets, _projs
 
+_f32 = ctypes.c_float
 _CODES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
 
 
@@ -91,7 +92,9 @@ def _new(shape, dtype, device, stream):
     return t
 
 
-# (descriptors are only read by the library: one per distinct set of values)
+# (descriptors are only read by the library: one per distinct set of values,
+# which have to be plain ones: a tensor is remembered by what it is, not by
+# the value it holds)
 @functools.lru_cache(maxsize=1024)
 def _norm_desc(dtype, stream_dtype, T, d, post, pre, gate_act, unit_offset, alpha, beta, eps):
     return ctypes.byref(NormDesc(
@@ -123,6 +126,8 @@ def block_norm(h, o=None, *, post="none", post_weight=None, post_bias=None, gate
         if t is not None:
             dt = t.dtype
             break
+    # (the values now, also of scales that are held in tensors)
+    alpha, beta, eps = _f32(alpha).value, _f32(beta).value, _f32(eps).value
     desc = _norm_desc(_dtype_code(dt, "o"), _dtype_code(hdt, "h"), T, d, post, pre, gate_act,
                       bool(unit_offset), alpha, beta, eps)
     op, ldo = _matrix(o, "o", shape, dt, dev) if o is not None else (0, d)
