@@ -256,6 +256,15 @@ template <typename T> __global__ __launch_bounds__(256) void k_operand(const Ope
 }
 
 // ---------------------------------------------------------------- delta -----
+// The part of a lane's 4 consecutive rows that lies in a slice of ho rows, the
+// first of them row o: rows outside it have no delta, and a product of zeros
+// there would not do (times an infinite or NaN operand it is NaN).
+__device__ __forceinline__ f32x4 in_slice(f32x4 s, int o, int ho) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = uint32_t(o + i) < uint32_t(ho) ? s[i] : 0.f;
+    return s;
+}
+
 // Adds the delta to the accumulators of 16 plan positions and 16 G outputs,
 // in order (row r of tile j is output f0 + 16 j + r: neighbouring rows of B
 // are what its block keeps together).  Positions are in plan
@@ -281,6 +290,7 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
     for (int p = 0; p < d.nproj; ++p) {
         const int lo = d.y_off[p], ho = d.h_out[p];
         if (f0 + 16 * G <= lo || f0 >= lo + ho) continue;
+        const bool edge = f0 < lo || f0 + 16 * G > lo + ho;   // uniform
         VOperand<T> vo[KS];
         if (KS == 1 && d.partial) {              // uniform
             const rsrc_t parts = make_rsrc(d.partial, d.partial_bytes);
@@ -360,6 +370,7 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
                             for (int i = P - 1; i >= 0; --i)
                                 s4 = mma<T>(bf[b][j][ks], vo[ks].piece[i], s4);
                         }
+                    if (edge) s4 = in_slice(s4, f0 + 16 * j + 4 * q - lo, ho);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = mine ? acc[j][i] + s4[i] : acc[j][i];
                 }
@@ -505,9 +516,10 @@ struct DeltaTile {
 };
 
 // What a stage of the delta holds: the half of W's rows (1: gate, or all; 2:
-// up; 0: nothing) and the group's positions.
+// up; 0: nothing), the group's positions, and the slice's rows (the tile's
+// first output is row col0 of h_out).
 struct DeltaHeld {
-    int half, first, end;
+    int half, first, end, col0, h_out;
 };
 
 // The walk over a tile's delta K tiles: groups, projections, halves, then the
@@ -727,7 +739,7 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
                         base + uint32_t(BT * kKBytes + i * NTH * 16));
         }
         dt.next(d);
-        return DeltaHeld{e.half, e.first, e.end};
+        return DeltaHeld{e.half, e.first, e.end, e.col0, e.h_out};
     };
 
     f32x4 acc[TI][TJ];
@@ -786,9 +798,11 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
     };
     // acc += a stage of one group's delta, in the columns of its positions
     // only: other positions' tiles are passed over, and in a tile that holds
-    // both, a sum apart is kept or dropped by column (zeros in the operand
-    // would not do: an infinite or NaN adapter times zero is NaN)
+    // both, a sum apart is kept or dropped by column, and at the slice's edges
+    // by row (zeros in the operands would not do: an infinite or NaN adapter
+    // times zero is NaN)
     auto multiply_delta = [&](int st, const DeltaHeld &e) {
+        const bool edge = e.col0 < 0 || e.col0 + FEAT > e.h_out;   // uniform
         each<TI>([&](auto index) {
             constexpr int i = decltype(index)::value;
             const int p0 = t0 + (wt * TI + i) * 16;
@@ -799,6 +813,7 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
             for (int j = 0; j < G; ++j) {
                 f32x4 s4 = mma<T>(w_frag(st, (e.half - 1) * G + j, 0), x0, f32x4{0.f, 0.f, 0.f, 0.f});
                 s4 = mma<T>(w_frag(st, (e.half - 1) * G + j, 1), x1, s4);
+                if (edge) s4 = in_slice(s4, e.col0 + (wn * 16 + q * 4) * G + 4 * j, e.h_out);
                 // (both halves by selects: a branch would turn the
                 // accumulators into memory)
                 const bool lower = mine && e.half == 1, upper = mine && e.half == 2;
@@ -858,7 +873,10 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
         }
     }
     if constexpr (ADAPT) {
-        while (held[0].half) {                   // uniform
+        // (a tile without a delta runs it once, on a stage of no positions:
+        // with a way round the loop the accumulators are held twice, 75 to
+        // 114 registers too many for the largest tile)
+        do {
             wait_copies<(S - 1) * (XL + WL)>();
             __builtin_amdgcn_s_barrier();
             multiply_delta(st, held[0]);
@@ -866,7 +884,7 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
             __builtin_amdgcn_s_barrier();        // the stage is free
             next_delta(st);
             st = st + 1 == S ? 0 : st + 1;
-        }
+        } while (held[0].half);                  // uniform
     }
     wait_copies<0>();                            // none may land after the workgroup's end
 
