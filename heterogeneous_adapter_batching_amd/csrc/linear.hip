@@ -265,18 +265,41 @@ __device__ __forceinline__ f32x4 in_slice(f32x4 s, int o, int ho) {
     return s;
 }
 
-// Adds the delta to the accumulators of 16 plan positions and 16 G outputs,
-// in order (row r of tile j is output f0 + 16 j + r: neighbouring rows of B
-// are what its block keeps together).  Positions are in plan
-// order, so a group's are neighbours: each group's B rows multiply every
-// position's operand and are kept in the columns of the group's own (so one
-// adapter's infinities stay with its tokens).  Of `nw` waves that share the
-// tile, wave w takes every nw-th group.  What this costs is the chain of
-// dependent loads position -> B rows, so the positions bring their group's
-// extent with them and the B rows of NB groups are in flight together.
-// KS: K-steps of the plan's largest rank.
-template <typename T, int G, int KS>
-__device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, int w, int nw,
+// B's vector for the second and third piece of the operand: those are what
+// the first leaves of v, and zero where it holds all of it, so that an
+// infinite (or NaN) B times them would be NaN where B v is infinite.  B's
+// own value counts with the first piece alone, which has v's sign and is zero
+// where v is.
+__device__ __forceinline__ u32x4 finite_bf16(u32x4 b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((b[i] & 0x7f80u) == 0x7f80u) b[i] &= 0xffff0000u;
+        if ((b[i] & 0x7f800000u) == 0x7f800000u) b[i] &= 0xffffu;
+    }
+    return b;
+}
+// Whether any lane holds a value that is not finite (uniform).
+template <int N> __device__ __forceinline__ bool any_odd(const f32x4 (&s)[N]) {
+    float z = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z = __builtin_fmaf(s[j][i], 0.f, z);
+    return __builtin_amdgcn_ballot_w64(z != z) != 0;
+}
+
+// The delta of 16 plan positions and 16 G outputs, added to `acc`, in order
+// (row r of tile j is output f0 + 16 j + r: neighbouring rows of B are what
+// its block keeps together).  Positions are in plan order, so a group's are
+// neighbours: each group's B rows multiply every position's operand and are
+// kept in the columns of the group's own (so one adapter's infinities stay
+// with its tokens).  Of `nw` waves that share the tile, wave w takes every
+// nw-th group.  What this costs is the chain of dependent loads position -> B
+// rows, so the positions bring their group's extent with them and the B rows
+// of NB groups are in flight together.  KS: K-steps of the plan's largest
+// rank.
+template <typename T, int G, int KS, bool CAREFUL>
+__device__ __forceinline__ void add_groups(const DeltaArgs &d, int p0, int f0, int w, int nw,
                                           f32x4 (&acc)[G]) {
     constexpr int E = Elem<T>::E, SPAN = 4 * E, P = VOperand<T>::kPieces;
     constexpr int NB = G * KS >= 8 ? 1 : 8 / (G * KS);
@@ -290,7 +313,6 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
     for (int p = 0; p < d.nproj; ++p) {
         const int lo = d.y_off[p], ho = d.h_out[p];
         if (f0 + 16 * G <= lo || f0 >= lo + ho) continue;
-        const bool edge = f0 < lo || f0 + 16 * G > lo + ho;   // uniform
         VOperand<T> vo[KS];
         if (KS == 1 && d.partial) {              // uniform
             const rsrc_t parts = make_rsrc(d.partial, d.partial_bytes);
@@ -366,17 +388,34 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
                         if (ks * SPAN < rp[b]) {         // uniform
+                            const u32x4 low = CAREFUL && P > 1 ? finite_bf16(bf[b][j][ks])
+                                                               : bf[b][j][ks];
 #pragma unroll
                             for (int i = P - 1; i >= 0; --i)
-                                s4 = mma<T>(bf[b][j][ks], vo[ks].piece[i], s4);
+                                s4 = mma<T>(i ? low : bf[b][j][ks], vo[ks].piece[i], s4);
                         }
-                    if (edge) s4 = in_slice(s4, f0 + 16 * j + 4 * q - lo, ho);
+                    if constexpr (CAREFUL) s4 = in_slice(s4, f0 + 16 * j + 4 * q - lo, ho);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = mine ? acc[j][i] + s4[i] : acc[j][i];
                 }
             }
         }
     }
+}
+
+// The delta into `acc`.  Only where it is not finite does it matter that rows
+// outside the slice, and pieces that are zero, are left out rather than
+// multiplied: then it is formed again, in that careful form.
+template <typename T, int G, int KS>
+__device__ __forceinline__ void delta_of(const DeltaArgs &d, int p0, int f0, int w, int nw,
+                                         f32x4 (&acc)[G]) {
+#pragma unroll
+    for (int j = 0; j < G; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    add_groups<T, G, KS, false>(d, p0, f0, w, nw, acc);
+    if (!any_odd(acc)) return;
+#pragma unroll
+    for (int j = 0; j < G; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    add_groups<T, G, KS, true>(d, p0, f0, w, nw, acc);
 }
 
 // ----------------------------------------------------------------- rows -----
@@ -387,7 +426,7 @@ __device__ __forceinline__ void add_delta(const DeltaArgs &d, int p0, int f0, in
 // Bound by W's bytes: 235 MB of gate and up rows at K 4096 in 46 us (5.1
 // TB/s, as a plain copy's).  KS: K-steps of the delta, 0 without adapters.
 template <typename T, bool GLU, int KS, int NW>
-__global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs a) {
+__global__ __launch_bounds__(NW * kWaveSize, KS > 0 ? 3 : 1) void k_linear_rows(const LinearArgs a) {
     constexpr int E = Elem<T>::E, SPAN = 4 * E, NR = GLU ? 2 : 1, F = 4;
     __shared__ f32x4 red[NW][NR][kWaveSize];
     const int unit = xcd_range_unit(a.units);
@@ -442,8 +481,8 @@ __global__ __launch_bounds__(NW * kWaveSize) void k_linear_rows(const LinearArgs
     if constexpr (KS > 0) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            f32x4 d[1] = {acc[r]};
-            add_delta<T, 1, KS>(a.delta, 0, r * a.n + f0, w, NW, d);
+            f32x4 d[1];
+            delta_of<T, 1, KS>(a.delta, 0, r * a.n + f0, w, NW, d);
             acc[r] = d[0];
         }
     }
@@ -512,14 +551,16 @@ struct DeltaTile {
     int col0, h_out;             // row of B of the tile's first output
     int vec;                     // the lane's vector of a B row
     int half;                    // 1: gate (or all), 2: up
+    int head;                    // vectors of the first piece (none: at most 0)
     bool ok;                     // the lane has a vector
 };
 
 // What a stage of the delta holds: the half of W's rows (1: gate, or all; 2:
-// up; 0: nothing), the group's positions, and the slice's rows (the tile's
-// first output is row col0 of h_out).
+// up; 0: nothing), the group's positions, the slice's rows (the tile's first
+// output is row col0 of h_out), and how many of its vectors, the first ones,
+// are the operand's first piece.
 struct DeltaHeld {
-    int half, first, end, col0, h_out;
+    int half, first, end, col0, h_out, head;
 };
 
 // The walk over a tile's delta K tiles: groups, projections, halves, then the
@@ -593,6 +634,7 @@ template <typename T, int HALVES> struct DeltaTiles {
         e.end = end;
         e.col0 = h * n + f0 - d.y_off[p];
         e.half = h + 1;
+        e.head = e.bl.nv - s * 8;
         return e;
     }
     __device__ __forceinline__ void next(const DeltaArgs &d) {
@@ -739,7 +781,7 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
                         base + uint32_t(BT * kKBytes + i * NTH * 16));
         }
         dt.next(d);
-        return DeltaHeld{e.half, e.first, e.end, e.col0, e.h_out};
+        return DeltaHeld{e.half, e.first, e.end, e.col0, e.h_out, e.head};
     };
 
     f32x4 acc[TI][TJ];
@@ -802,6 +844,28 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
     // by row (zeros in the operands would not do: an infinite or NaN adapter
     // times zero is NaN)
     auto multiply_delta = [&](int st, const DeltaHeld &e) {
+        const bool upper_half = e.half == 2;
+        u32x4 b[2][G];                           // B's rows, for all of the positions
+        f32x4 probe[1] = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                b[kk][j] = w_frag(st, (upper_half ? G : 0) + j, kk);
+                if constexpr (VOperand<T>::kPieces > 1)
+                    probe[0] = mma<T>(b[kk][j], u32x4{0u, 0u, 0u, 0u}, probe[0]);
+            }
+        if (VOperand<T>::kPieces > 1 && any_odd(probe)) {
+            // pieces past the first: see finite_bf16
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const u32x4 f = finite_bf16(b[kk][j]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) b[kk][j][i] = kk * 4 + q >= e.head ? f[i] : b[kk][j][i];
+                }
+        }
         const bool edge = e.col0 < 0 || e.col0 + FEAT > e.h_out;   // uniform
         each<TI>([&](auto index) {
             constexpr int i = decltype(index)::value;
@@ -809,22 +873,29 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
             if (p0 >= e.end || p0 + 16 <= e.first) return;   // uniform
             const bool mine = p0 + n >= e.first && p0 + n < e.end;
             const u32x4 x0 = x_frag(st, i, 0), x1 = x_frag(st, i, 1);
+            // (both halves by selects: a branch would turn the accumulators
+            // into memory)
+            const bool lower = mine && !upper_half, upper = mine && upper_half;
+            f32x4 s4[G];
 #pragma unroll
             for (int j = 0; j < G; ++j) {
-                f32x4 s4 = mma<T>(w_frag(st, (e.half - 1) * G + j, 0), x0, f32x4{0.f, 0.f, 0.f, 0.f});
-                s4 = mma<T>(w_frag(st, (e.half - 1) * G + j, 1), x1, s4);
-                if (edge) s4 = in_slice(s4, e.col0 + (wn * 16 + q * 4) * G + 4 * j, e.h_out);
-                // (both halves by selects: a branch would turn the
-                // accumulators into memory)
-                const bool lower = mine && e.half == 1, upper = mine && e.half == 2;
+                s4[j] = mma<T>(b[0][j], x0, f32x4{0.f, 0.f, 0.f, 0.f});
+                s4[j] = mma<T>(b[1][j], x1, s4[j]);
+            }
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+                    s4[j] = in_slice(s4[j], e.col0 + (wn * 16 + q * 4) * G + 4 * j, e.h_out);
+            }
+#pragma unroll
+            for (int j = 0; j < G; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    acc[i][j][k] = lower ? acc[i][j][k] + s4[k] : acc[i][j][k];
+                    acc[i][j][k] = lower ? acc[i][j][k] + s4[j][k] : acc[i][j][k];
                     if constexpr (GLU)
-                        acc[i][TJ - G + j][k] = upper ? acc[i][TJ - G + j][k] + s4[k]
+                        acc[i][TJ - G + j][k] = upper ? acc[i][TJ - G + j][k] + s4[j][k]
                                                       : acc[i][TJ - G + j][k];
                 }
-            }
         });
     };
     int st = 0;
@@ -943,7 +1014,7 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
 #pragma unroll
     for (int j = 0; j < G; ++j) s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (f0 < a.n) {                              // uniform
-        if constexpr (KS > 0) add_delta<T, G, KS>(a.delta, p0, c0, 0, 1, s);
+        if constexpr (KS > 0) delta_of<T, G, KS>(a.delta, p0, c0, 0, 1, s);
         // the parts in order, Z of them in flight
         const float *p = a.partial + int64_t(t) * a.ldp + c0 + q * 4;
         const int64_t step = int64_t(a.T) * a.ldp;

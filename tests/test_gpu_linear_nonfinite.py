@@ -1,5 +1,10 @@
 """Infinities and NaN of one adapter's weights in sgmv_linear on the GPU: the
-delta is added on its projection's slice and nowhere else.
+delta is added on its projection's slice and nowhere else, and an infinite
+weight gives what the formula gives.
+
+The expected values are the formula's in 64 bits, whose infinities and NaN
+are IEEE's own: finite outputs come from whole numbers and must equal the
+reference's bits; the others must be the same infinity, or NaN where it is.
 """
 import numpy as np
 import pytest
@@ -15,6 +20,10 @@ INF, NAN = float("inf"), float("nan")
 SIZES = [(6, 256, 320, 1, (8, 16, 24)), (6, 256, 320, 1, (40, 64, 8)),
          (100, 2048, 320, 1, (16, 8, 24)), (100, 2048, 320, 1, (64, 40, 8)),
          (2048, 64, 4096, 512, (16, 16, 8)), (2048, 64, 4096, 512, (64, 40, 8))]
+
+
+def same(got, ref):
+    return (got == ref) | (got.isnan() & ref.isnan())
 
 
 def make(T, k, wide, seg, ranks, dtype, glu):
@@ -55,3 +64,57 @@ def test_other_columns_are_left_alone(T, k, wide, seg, ranks, glu, dtype):
         moved = (y != clean) & ~hit
         assert not bool(moved.any()), moved.nonzero()[:5].tolist()
         assert not bool(y[hit].isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T, k, wide, seg, ranks", SIZES)
+def test_infinite_b(T, k, wide, seg, ranks, dtype):
+    """Single infinities and NaN in B: s v_r times the infinity, NaN only where
+    v_r is zero, where infinities of both signs meet, or where B is NaN."""
+    import heterogeneous_adapter_batching_amd as hab
+    m, offsets, token = make(T, k, wide, seg, ranks, dtype, False)
+    g = torch.Generator().manual_seed(T + 1)
+    x, w = ints(g, T, k, top=1, dtype=dtype), ints(g, wide, k, top=1, dtype=dtype)
+    A, B, _ = m.ad[1]
+    for p in (0, 1):
+        Bp = B[p][0]
+        Bp[2, 0], Bp[5, -1], Bp[m.widths[p] - 1, 1] = INF, -INF, INF
+        Bp[9, 0], Bp[9, 2] = INF, -INF
+        Bp[11, 3] = NAN
+        m.pool.upload(1, 0, p, A[p][0], Bp)
+    y = hab.sgmv_linear(m.pool, m.plan, 0, [0, 1], offsets, x, w)
+    z = (x.double() @ w.double().t()).cpu()
+    token, xc = token.cpu(), x.double().cpu()
+    for a, (A, B, s) in m.ad.items():
+        rows = token == a
+        for p, off in enumerate(offsets):
+            v = s * (xc[rows] @ A[p][0].double().cpu().t())
+            z[rows, off:off + m.widths[p]] += (v[:, None, :] * B[p][0].double().cpu()[None]).sum(2) \
+                if a == 1 and T < 1000 else v @ B[p][0].double().cpu().t()
+    ref = z.to(dtype).cuda()
+    print(f"[nonfinite] {T} x {k} x {wide} ranks {ranks} {dtype}: {int(ref.isinf().sum())} infinities, "
+          f"{int(ref.isnan().sum())} NaN", flush=True)
+    assert bool(ref.isinf().any()) and bool(ref.isnan().any())
+    bad = (~same(y, ref)).nonzero()
+    assert bad.numel() == 0, (bad[:5].tolist(), len(bad))
+
+
+def test_infinite_b_of_real_values():
+    """The same where v fills all three bf16 pieces: the sign of v decides."""
+    import heterogeneous_adapter_batching_amd as hab
+    for T, k, wide, seg, ranks in SIZES:
+        m, offsets, token = make(T, k, wide, seg, ranks, BF16, False)
+        g = torch.Generator().manual_seed(T + 2)
+        x = torch.randn(T, k, generator=g).to(BF16).cuda()
+        w = torch.randn(wide, k, generator=g).to(BF16).cuda()
+        A, B, s = m.ad[1]
+        B[0][0][4, 1], B[0][0][7, -1] = INF, -INF
+        m.pool.upload(1, 0, 0, A[0][0], B[0][0])
+        y = hab.sgmv_linear(m.pool, m.plan, 0, [0, 1], offsets, x, w)
+        rows = token == 1
+        v = s * (x[rows].double() @ A[0][0].double().t())
+        print(f"[nonfinite] real values, {T} x {k} x {wide} ranks {ranks}", flush=True)
+        assert torch.equal(y[rows][:, offsets[0] + 4].double(), v[:, 1] * INF)
+        assert torch.equal(y[rows][:, offsets[0] + 7].double(), v[:, -1] * -INF)
+        y[rows.nonzero()[:, 0, None], torch.tensor([[offsets[0] + 4, offsets[0] + 7]], device="cuda")] = 0
+        assert bool(y.isfinite().all())
