@@ -55,7 +55,7 @@ __device__ uint32_t g_debug_errors;
 __device__ __forceinline__ uint32_t dbg_block(const DebugBounds &d, uint64_t off,
                                               uint64_t bytes) {
     if constexpr (kDebug) {
-        if (off + bytes > d.slab_bytes) {
+        if (!block_inside(d, off, bytes)) {
             atomicOr(&g_debug_errors, kDbgSlab);
             return 0u;
         }
@@ -67,7 +67,7 @@ __device__ __forceinline__ uint32_t dbg_block(const DebugBounds &d, uint64_t off
 // (debug build).
 __device__ __forceinline__ int dbg_token(const DebugBounds &d, int r) {
     if constexpr (kDebug) {
-        if (r < -1 || r >= d.num_tokens) {
+        if (!token_inside(d, r)) {
             atomicOr(&g_debug_errors, kDbgToken);
             return -1;
         }
@@ -79,7 +79,7 @@ __device__ __forceinline__ int dbg_token(const DebugBounds &d, int r) {
 // tables of the plan: n, or 0 when they leave the plan (debug build).
 __device__ __forceinline__ int dbg_rows(const DebugBounds &d, int off, int n) {
     if constexpr (kDebug) {
-        if (off < 0 || n < 0 || off + n > d.num_rows) {
+        if (!rows_inside(d, off, n)) {
             atomicOr(&g_debug_errors, kDbgRow);
             return 0;
         }

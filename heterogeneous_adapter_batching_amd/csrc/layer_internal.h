@@ -50,6 +50,7 @@ struct DeltaArgs {
     int32_t h_out[LORA_MAX_PROJ];
     int32_t y_off[LORA_MAX_PROJ];
     int32_t n_active;            // positions with an adapter (they come first)
+    int32_t num_groups;          // (with the group of positions without one)
     int32_t max_rpad;            // largest padded rank of the plan
     int32_t nproj;
     int32_t r_max;
@@ -68,6 +69,7 @@ struct OperandArgs {
     uint8_t *out;
     uint32_t partial_bytes;
     int32_t nb, nb_long, nproj, c0, r_max;
+    uint32_t *dbg_word;          // debug build: where failed checks are noted
     DebugBounds dbg;
 };
 // The largest padded rank whose delta is one K-step of the matrix cores.  Up

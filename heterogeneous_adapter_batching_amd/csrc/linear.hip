@@ -30,6 +30,29 @@ constexpr bool kDebug = true;
 constexpr bool kDebug = false;
 #endif
 
+// Debug build: whether a check held; one that failed is noted.
+[[maybe_unused]] __device__ __forceinline__ bool dbg_held(bool ok, uint32_t *word, uint32_t bit) {
+    if (!ok) atomicOr(word, bit);
+    return ok;
+}
+// The token row of a plan position: -1 (absent) when it is outside the batch
+// (debug build).
+__device__ __forceinline__ int token_row(const DeltaArgs &d, int pos) {
+    const int r = d.order[pos];
+    if constexpr (kDebug) {
+        if (!dbg_held(token_inside(d.dbg, r), d.dbg_word, kDbgToken)) return -1;
+    }
+    return r;
+}
+// The bytes of the adapter block at slab offset `off`: none when it would
+// leave the slab (debug build).
+__device__ __forceinline__ uint32_t block_bytes(const DeltaArgs &d, uint64_t off, uint64_t bytes) {
+    if constexpr (kDebug) {
+        if (!dbg_held(block_inside(d.dbg, off, bytes), d.dbg_word, kDbgSlab)) return 0u;
+    }
+    return uint32_t(bytes);
+}
+
 // fn(0), ..., fn(N - 1) with constant indexes, whatever the body's size.
 template <int N, typename Fn, int I = 0> __device__ __forceinline__ void each(Fn fn) {
     if constexpr (I < N) {
@@ -221,9 +244,8 @@ template <typename T> __global__ __launch_bounds__(256) void k_operand(const Ope
     const int b = blockIdx.x / a.nproj, p = blockIdx.x % a.nproj;
     BlockDesc blk = load_invariant(a.blocks + b);
     if constexpr (kDebug) {
-        const bool ok = blk.tok_off >= 0 && blk.n_tok >= 0 &&
-                        blk.tok_off + blk.n_tok <= a.dbg.num_rows;
-        blk.n_tok = ok ? min(blk.n_tok, kMaxBlockTokens) : 0;
+        blk.n_tok = dbg_held(rows_inside(a.dbg, blk.tok_off, blk.n_tok), a.dbg_word, kDbgRow)
+                        ? min(blk.n_tok, kMaxBlockTokens) : 0;
     }
     const rsrc_t pr = make_rsrc(a.partial, a.partial_bytes);
     const int vecs = a.r_max / E;
@@ -359,14 +381,8 @@ __device__ __forceinline__ void add_groups(const DeltaArgs &d, int p0, int f0, i
                 const uint64_t off = extent(__builtin_amdgcn_readlane(pr.ext_lo, l),
                                             __builtin_amdgcn_readlane(pr.ext_hi, l)) +
                                      uint64_t(rp[b]) * sizeof(T) * uint64_t(d.coef_b[p]);
-                uint64_t bytes = uint64_t(ho) * uint64_t(rp[b]) * sizeof(T);
-                if constexpr (kDebug) {
-                    if (off + bytes > d.dbg.slab_bytes) {
-                        atomicOr(d.dbg_word, uint32_t(kDbgSlab));
-                        bytes = 0;
-                    }
-                }
-                const rsrc_t br = make_rsrc(d.slab + off, uint32_t(bytes));
+                const rsrc_t br = make_rsrc(
+                    d.slab + off, block_bytes(d, off, uint64_t(ho) * uint64_t(rp[b]) * sizeof(T)));
                 const BLayout bl = b_layout(rp[b], int(sizeof(T)));
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
@@ -451,7 +467,7 @@ __global__ __launch_bounds__(NW * kWaveSize, KS > 0 ? 3 : 1) void k_linear_rows(
     const int s_lo = w * per, s_hi = min(s_lo + per, steps);
 
     // this lane's token row (with adapters: in plan order)
-    const int tok = n < a.T ? (KS ? a.delta.order[n] : n) : -1;
+    const int tok = n < a.T ? (KS ? token_row(a.delta, n) : n) : -1;
     f32x4 acc[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -581,6 +597,14 @@ template <typename T, int HALVES> struct DeltaTiles {
         gr = load_invariant(d.groups + g);
         first = gr.first;
         end = load_invariant(&d.groups[g + 1].first);
+        if constexpr (kDebug) {
+            if (!dbg_held(end >= first && rows_inside(d.dbg, first, end - first), d.dbg_word, kDbgRow))
+                first = end = 0;                 // no position's
+            if (!dbg_held(padded_rank(gr.r_pad), d.dbg_word, kDbgSlab)) {
+                gr.r_pad = 8;
+                gr.ext_hi = 0x7fffffffu;         // a block that leaves the slab
+            }
+        }
     }
     // on to the first (projection, half) from the current one that the tile meets
     __device__ __forceinline__ void settle(const DeltaArgs &d) {
@@ -608,6 +632,15 @@ template <typename T, int HALVES> struct DeltaTiles {
         if (last < t0 || !any) return;
         g = load_invariant(&d.pos[t0].group);
         g1 = load_invariant(&d.pos[last].group);
+        if constexpr (kDebug) {
+            // (the groups' table ends with a row of no adapter)
+            if (!dbg_held(group_inside(d.num_groups - 1, g) && group_inside(d.num_groups - 1, g1),
+                          d.dbg_word, kDbgRow)) {
+                g = 1;
+                g1 = 0;
+                return;
+            }
+        }
         load(d);
         settle(d);
     }
@@ -619,13 +652,7 @@ template <typename T, int HALVES> struct DeltaTiles {
         e.bl = b_layout(gr.r_pad, int(sizeof(T)));
         e.off = extent(gr.ext_lo, gr.ext_hi) + uint64_t(gr.r_pad) * sizeof(T) * uint64_t(d.coef_b[p]);
         e.h_out = d.h_out[p];
-        e.bytes = uint32_t(e.h_out) * uint32_t(gr.r_pad) * uint32_t(sizeof(T));
-        if constexpr (kDebug) {
-            if (e.off + e.bytes > d.dbg.slab_bytes) {
-                atomicOr(d.dbg_word, uint32_t(kDbgSlab));
-                e.bytes = 0;
-            }
-        }
+        e.bytes = block_bytes(d, e.off, uint64_t(e.h_out) * uint64_t(gr.r_pad) * sizeof(T));
         const int at = s * 8 + int(vec), piece = at / e.bl.nv;
         e.vec = at - piece * e.bl.nv;
         e.ok = piece < P;
@@ -721,8 +748,8 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
         const int row = (i * NTH + tid) >> 3;
-        const int t = ADAPT && row < xrows ? a.delta.order[t0 + row] : row;
-        xo[i] = row < xrows ? uint32_t(t) * xrow + vec * 16u : kOOB;
+        const int t = ADAPT && row < xrows ? token_row(a.delta, t0 + row) : row;
+        xo[i] = row < xrows && (!kDebug || t >= 0) ? uint32_t(t) * xrow + vec * 16u : kOOB;
     }
 #pragma unroll
     for (int i = 0; i < WL; ++i) {
@@ -972,7 +999,7 @@ __global__ __launch_bounds__(WT *WN *kWaveSize) void k_linear_tile(const LinearA
                     if (fw + q * 4 * G + 4 * j < a.ldp) *reinterpret_cast<f32x4 *>(p + 4 * j) = acc[i][j];
             }
         } else {
-            const int t = pos < a.T ? (ADAPT ? a.delta.order[pos] : pos) : -1;
+            const int t = pos < a.T ? (ADAPT ? token_row(a.delta, pos) : pos) : -1;
             constexpr int N = G % 2 == 0 ? 8 : 4;
             each<G * 4 / N>([&](auto run) {
                 constexpr int j0 = decltype(run)::value * (N / 4);
@@ -1008,7 +1035,7 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
     const int p0 = blockIdx.x % tiles_t * 16;
     const int f0 = (blockIdx.x / tiles_t * TILES + tile) * 16 * G;
     const int pos = p0 + n;
-    const int t = pos < a.T ? (KS ? a.delta.order[pos] : pos) : -1;
+    const int t = pos < a.T ? (KS ? token_row(a.delta, pos) : pos) : -1;
     const int c0 = r * a.n + f0;                 // column before the activation
     f32x4 s[G];
 #pragma unroll

@@ -1738,6 +1738,7 @@ lora_status run_operand(const lora_pool *p, const lora_plan *pl, int32_t layer, 
     a.nb_long = pl->nb_long;
     a.nproj = nproj;
     a.r_max = p->d.r_max;
+    a.dbg_word = da->dbg_word;
     a.dbg = debug_bounds(p, pl);
     const hipError_t e = lora::launch_operand(p->d.dtype, a, hs);
     if (e != hipSuccess) return hip_fail(e, "product operand launch");
@@ -2053,6 +2054,7 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
             da.y_off[i] = yoff[i];
         }
         da.n_active = pl->n_active;
+        da.num_groups = int32_t(pl->group_rows.size());
         da.max_rpad = pl->max_rpad;
         da.nproj = nproj;
         da.r_max = p->d.r_max;

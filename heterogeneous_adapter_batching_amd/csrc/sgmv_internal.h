@@ -128,6 +128,22 @@ struct DebugBounds {
     int32_t num_tokens;
     int32_t num_rows;
 };
+// The debug build's checks (no sum of theirs can overflow, whatever the plan's
+// memory holds): an adapter block inside the slab, a token row of the batch or
+// the -1 of an absent one, rows [off, off + n) of the plan, a group of `count`,
+// a padded rank.
+constexpr bool block_inside(const DebugBounds &d, uint64_t off, uint64_t bytes) {
+    return bytes <= d.slab_bytes && off <= d.slab_bytes - bytes;
+}
+constexpr bool token_inside(const DebugBounds &d, int32_t r) {
+    return r >= -1 && r < d.num_tokens;
+}
+constexpr bool rows_inside(const DebugBounds &d, int32_t off, int32_t n) {
+    return off >= 0 && n >= 0 && n <= d.num_rows && off <= d.num_rows - n;
+}
+constexpr bool group_inside(int32_t count, int32_t g) { return g >= 0 && g < count; }
+constexpr bool padded_rank(int32_t r) { return r >= 8 && r <= LORA_MAX_RANK && r % 8 == 0; }
+
 // bits of the debug build's error word (lora_debug_checks)
 enum : uint32_t { kDbgSlab = LORA_DEBUG_SLAB, kDbgToken = LORA_DEBUG_TOKEN,
                   kDbgRow = LORA_DEBUG_ROW };

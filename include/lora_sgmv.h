@@ -684,8 +684,10 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
  * that each adapter block it addresses lies inside the pool's slab
  * (LORA_DEBUG_SLAB), that each token row it reads from the plan lies in
  * [0, num_tokens) or is the -1 of an absent row (LORA_DEBUG_TOKEN), and that
- * each plan position it indexes a per-row table with lies inside the plan
- * (LORA_DEBUG_ROW).  A failed check sets its bit in a device-wide error word
+ * each plan position it indexes a per-row table with, and each adapter group
+ * that the product with adapters goes through, lies inside the plan
+ * (LORA_DEBUG_ROW; a group's padded rank that is none counts as a block
+ * outside the slab).  A failed check sets its bit in a device-wide error word
  * and switches that access off (the block reads as zeros, the row is taken
  * as absent), so the launch ends normally with a wrong result instead of
  * reading outside the slab or the caller's tensors.  The release build
