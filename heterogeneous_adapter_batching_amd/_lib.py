@@ -125,9 +125,12 @@ SIGNATURES = {
     "block_norm": (_i32, [ctypes.POINTER(NormDesc), _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
                           _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
     "frozen_linear_workspace_bytes": (_u64, [ctypes.POINTER(LinearDesc)]),
+    "frozen_linear_max_workspace_bytes": (_u64, [ctypes.POINTER(LinearDesc)]),
     "frozen_linear": (_i32, [ctypes.POINTER(LinearDesc), _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp,
                              _i64, _vp, _u64, _vp]),
     "sgmv_linear_workspace_bytes": (_u64, [_vp, ctypes.POINTER(LinearDesc), _i32]),
+    "sgmv_linear_max_workspace_bytes": (_u64, [_vp, ctypes.POINTER(LinearDesc), _i32]),
+    "sgmv_linear_plan_workspace_bytes": (_u64, [_vp, _vp, ctypes.POINTER(LinearDesc), _i32]),
     "sgmv_linear": (_i32, [_vp, _vp, _i32, _i32, _i32p, _i32p, ctypes.POINTER(LinearDesc), _vp,
                            _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _u64, _vp]),
 }

@@ -168,11 +168,14 @@ LinearPlan linear_plan(int dtype, int T, int n, int k, bool glu, int groups, int
     return pl;
 }
 
-uint64_t linear_ws_bound(int dtype, int T, int n, int k, bool glu) {
-    if (T <= kRowsTokens) return 0;
-    const int64_t wide = glu ? 2 * int64_t(n) : n;
-    return partial_bytes(std::max(joined(dtype, T, wide, k, 1).pl.splits,
-                                  joined(dtype, T, wide, k, 2).pl.splits), T, wide);
+uint64_t linear_ws_bound(int dtype, int T, int n, int k, bool glu, int max_groups, int max_rpad) {
+    // (the one launch's time grows with the groups and their rank, the parts'
+    // does not: the most of both tells whether any batch takes parts for its
+    // adapters' sake)
+    const uint64_t plain = linear_plan(dtype, T, n, k, glu, 0, 0).ws_bytes;
+    const int groups = std::min(T, max_groups);
+    return groups < 1 ? plain
+                      : std::max(plain, linear_plan(dtype, T, n, k, glu, groups, max_rpad).ws_bytes);
 }
 
 lora_status check_linear_desc(const lora_linear_desc *d) {
@@ -263,6 +266,14 @@ extern "C" {
 uint64_t frozen_linear_workspace_bytes(const lora_linear_desc *d) {
     if (lora::check_linear_desc(d) != LORA_OK || d->num_tokens == 0) return 0;
     return lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0, 0, 0).ws_bytes;
+}
+
+uint64_t frozen_linear_max_workspace_bytes(const lora_linear_desc *d) {
+    if (lora::check_linear_desc(d) != LORA_OK) return 0;
+    uint64_t most = 0;
+    for (int64_t t = 1; t <= d->num_tokens; ++t)
+        most = std::max(most, lora::linear_plan(d->dtype, int(t), d->n, d->k, d->glu != 0, 0, 0).ws_bytes);
+    return most;
 }
 
 lora_status frozen_linear(const lora_linear_desc *d, const void *x, int64_t ldx, const void *w,

@@ -115,8 +115,9 @@ constexpr int kRowsTokens = 12;  // most tokens of the rows kernel
 // groups, max_rpad: adapter groups of the batch and their largest padded rank
 // (0: no adapters)
 LinearPlan linear_plan(int dtype, int T, int n, int k, bool glu, int groups, int max_rpad);
-// the most workspace a plan of these sizes takes, whatever its adapters
-uint64_t linear_ws_bound(int dtype, int T, int n, int k, bool glu);
+// the most workspace a plan of these sizes takes with at most max_groups
+// adapters of padded ranks up to max_rpad
+uint64_t linear_ws_bound(int dtype, int T, int n, int k, bool glu, int max_groups, int max_rpad);
 // The arguments of a product call, as the entry points take them.
 struct LinearCall {
     const lora_linear_desc *d;

@@ -1697,6 +1697,22 @@ uint64_t linear_v_bytes(const lora_pool *p, int32_t T, int32_t nproj, int32_t en
     return round_up(uint64_t(entry) * uint64_t(T) * uint64_t(nproj) * uint64_t(p->d.r_max), 256);
 }
 
+// The v of the long groups, then every position's operand.
+uint64_t linear_operand_bytes(const lora_pool *p, const lora_linear_desc *d, int32_t nproj) {
+    return linear_v_bytes(p, d->num_tokens, nproj, 4) +
+           linear_v_bytes(p, d->num_tokens, nproj, lora::operand_bytes(d->dtype));
+}
+
+// Partial sums: the most that any batch over the pool takes, and how the
+// product over one plan runs.
+uint64_t linear_parts_bound(const lora_pool *p, const lora_linear_desc *d) {
+    return lora::linear_ws_bound(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0, p->d.max_slots, p->d.r_max);
+}
+lora::LinearPlan plan_of_product(const lora_plan *pl, const lora_linear_desc *d) {
+    return lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0,
+                             int32_t(pl->group_adapter.size()), pl->max_rpad);
+}
+
 // The product's right operand of the delta, scale * (A x) of every plan
 // position with an adapter: the shrink's partials, which the product sums
 // itself, or (`formed`) formed by a launch from them and the prompt kernel's v.
@@ -1987,9 +2003,27 @@ uint64_t sgmv_linear_workspace_bytes(const lora_pool *p, const lora_linear_desc 
     if (!p || lora::check_linear_desc(d) != LORA_OK || d->num_tokens == 0 || nproj < 1 ||
         nproj > LORA_MAX_PROJ)
         return 0;
-    return linear_v_bytes(p, d->num_tokens, nproj, 4) +
-           linear_v_bytes(p, d->num_tokens, nproj, lora::operand_bytes(d->dtype)) +
-           lora::linear_ws_bound(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0);
+    return linear_operand_bytes(p, d, nproj) + linear_parts_bound(p, d);
+}
+
+uint64_t sgmv_linear_max_workspace_bytes(const lora_pool *p, const lora_linear_desc *d,
+                                         int32_t nproj) {
+    if (!p || lora::check_linear_desc(d) != LORA_OK || nproj < 1 || nproj > LORA_MAX_PROJ) return 0;
+    uint64_t most = 0;
+    lora_linear_desc t = *d;
+    for (int64_t n = 1; n <= d->num_tokens; ++n) {
+        t.num_tokens = int32_t(n);
+        most = std::max(most, linear_operand_bytes(p, &t, nproj) + linear_parts_bound(p, &t));
+    }
+    return most;
+}
+
+uint64_t sgmv_linear_plan_workspace_bytes(const lora_pool *p, const lora_plan *pl,
+                                          const lora_linear_desc *d, int32_t nproj) {
+    if (!p || !pl || pl->pool != p || lora::check_linear_desc(d) != LORA_OK ||
+        d->num_tokens == 0 || d->num_tokens != pl->T || nproj < 1 || nproj > LORA_MAX_PROJ)
+        return 0;
+    return linear_operand_bytes(p, d, nproj) + plan_of_product(pl, d).ws_bytes;
 }
 
 lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, int32_t nproj,
@@ -2019,11 +2053,8 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
     if (ldx > 0 && tensor_bytes(pl->T, ldx, cc.h_in, cc.es) > lora::kMaxTensorBytes)
         return fail(LORA_EINVAL, "x spans more than 2 GiB");
     const lora::LinearCall c{d, x, ldx, w, ldw, bias, residual, ldr, y, ldy, ws, ws_bytes};
-    const int32_t groups = int32_t(pl->group_adapter.size());
-    const lora::LinearPlan lp = lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0,
-                                                  groups, pl->max_rpad);
-    const uint64_t v_bytes = linear_v_bytes(p, pl->T, nproj, 4) +
-                             linear_v_bytes(p, pl->T, nproj, lora::operand_bytes(d->dtype));
+    const lora::LinearPlan lp = plan_of_product(pl, d);
+    const uint64_t v_bytes = linear_operand_bytes(p, d, nproj);
     st = lora::check_linear(c, v_bytes + lp.ws_bytes);
     if (st != LORA_OK) return st;
     const uintptr_t wl = reinterpret_cast<uintptr_t>(ws), pw0 = reinterpret_cast<uintptr_t>(pl->ws);

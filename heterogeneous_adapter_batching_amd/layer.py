@@ -158,18 +158,30 @@ def _linear_desc(num_tokens, n, k, dtype, glu, act="none"):
 
 
 def linear_workspace_bytes(num_tokens: int, n: int, k: int, dtype: str = "bf16",
-                           glu: bool = False) -> int:
+                           glu: bool = False, up_to: bool = False) -> int:
     """Bytes of workspace a frozen_linear call of these sizes takes (0: none);
-    n is the width of y."""
-    return int(load().frozen_linear_workspace_bytes(
-        _linear_desc(num_tokens, n, k, _DTYPES[dtype], bool(glu))))
+    n is the width of y.  A smaller batch may take more (it runs in more parts
+    along k): with up_to, what is enough for every call of at most num_tokens
+    tokens, found by trying each of them (once, when a server starts)."""
+    lib = load()
+    ask = lib.frozen_linear_max_workspace_bytes if up_to else lib.frozen_linear_workspace_bytes
+    return int(ask(_linear_desc(num_tokens, n, k, _DTYPES[dtype], bool(glu))))
 
 
 def sgmv_linear_workspace_bytes(pool, num_tokens: int, n: int, k: int, nproj: int,
-                                glu: bool = False) -> int:
-    """The same for sgmv_linear over nproj projections of the pool."""
-    return int(load().sgmv_linear_workspace_bytes(
-        pool.handle, _linear_desc(num_tokens, n, k, pool.desc.dtype, bool(glu)), nproj))
+                                glu: bool = False, plan=None, up_to: bool = False) -> int:
+    """The same for sgmv_linear over nproj projections of the pool: what is
+    enough for any batch of num_tokens tokens over its adapters (with up_to,
+    for those of fewer tokens too), or what the given plan takes, which for a
+    prompt is a fraction of it."""
+    desc = _linear_desc(num_tokens, n, k, pool.desc.dtype, bool(glu))
+    lib = load()
+    if plan is not None:
+        if up_to:
+            raise ValueError("a plan is one batch: plan and up_to exclude each other")
+        return int(lib.sgmv_linear_plan_workspace_bytes(pool.handle, plan.handle, desc, nproj))
+    ask = lib.sgmv_linear_max_workspace_bytes if up_to else lib.sgmv_linear_workspace_bytes
+    return int(ask(pool.handle, desc, nproj))
 
 
 def _linear_call(x, w, bias, act, glu, residual, y, ws, stream, need, fn, head):
@@ -224,12 +236,15 @@ def sgmv_linear(pool, plan, layer, projs, y_offsets, x, w, *, bias=None, act="no
     """frozen_linear with every token's LoRA delta inside the activation:
     before it, columns y_offsets[i] .. + h_out of x w^T + bias get
     s B (A x) of projection projs[i] (with glu the columns are the gate's n,
-    then the up's n).  plan: a plain or weighted plan of x's tokens."""
+    then the up's n).  plan: a plain or weighted plan of x's tokens.  ws: a
+    workspace of sgmv_linear_workspace_bytes (made per call, of the plan's
+    size, if not given)."""
     lib = pool.lib
     count, parr = _projs(projs)
     if len(y_offsets) != count:
         raise ValueError("y_offsets must have one entry per projection")
     return _linear_call(
         x, w, bias, act, glu, residual, y, ws, stream,
-        lambda d: lib.sgmv_linear_workspace_bytes(pool.handle, d, count), lib.sgmv_linear,
+        lambda d: lib.sgmv_linear_plan_workspace_bytes(pool.handle, plan.handle, d, count),
+        lib.sgmv_linear,
         (pool.handle, plan.handle, layer, count, parr, _offsets(y_offsets)))

@@ -649,10 +649,15 @@ typedef struct {
  * A product with too few output tiles for the chip is split along k, through
  * float32 partial sums in `ws`: at least frozen_linear_workspace_bytes(d)
  * bytes, 256-byte aligned (0 bytes: ws may be NULL), overwritten by the
- * call; calls that share it must not overlap.
+ * call; calls that share it must not overlap.  A smaller batch may run in
+ * more parts and need more: frozen_linear_max_workspace_bytes(d) is enough
+ * for every batch of at most d->num_tokens tokens (it tries each of them: a
+ * fraction of a microsecond a token, for once at start).  0 for a bad
+ * descriptor.
  * Errors: LORA_EINVAL (null or misaligned pointers, sizes, strides, an output
  * that overlaps an input), LORA_EDTYPE, LORA_ESTATE (ws too small), LORA_EHIP. */
 uint64_t frozen_linear_workspace_bytes(const lora_linear_desc *d);
+uint64_t frozen_linear_max_workspace_bytes(const lora_linear_desc *d);
 lora_status frozen_linear(const lora_linear_desc *d, const void *x, int64_t ldx, const void *w,
                           int64_t ldw, const void *bias, const void *residual, int64_t ldr,
                           void *y, int64_t ldy, void *ws, uint64_t ws_bytes, void *stream);
@@ -666,12 +671,20 @@ lora_status frozen_linear(const lora_linear_desc *d, const void *x, int64_t ldx,
  * projections; a merge plan and one with cores are refused.  Tokens without
  * an adapter get the plain product.  The pool's dtype is d's, h_in of the
  * listed projections is d->k, and their slices lie in the n (2 n with glu)
- * columns of z.  v = A x goes through `ws` (sgmv_linear_workspace_bytes, apart
- * from the plan's workspace); the shrink leaves its partials in the plan's
+ * columns of z.  v = A x goes through `ws`, apart from the plan's workspace:
+ * sgmv_linear_workspace_bytes is enough for any plan of num_tokens tokens over
+ * the pool, sgmv_linear_max_workspace_bytes for those of fewer tokens too, and
+ * sgmv_linear_plan_workspace_bytes is what the given plan takes (a prompt's in
+ * one launch no partial sums; 0 for another pool's plan or another number of
+ * tokens).  The shrink leaves its partials in the plan's
  * workspace as sgmv_shrink does, and the product may read them there, so
  * calls that share a plan's workspace must not overlap.  Other arguments and
  * errors as frozen_linear and sgmv_shrink (x spans at most 2 GiB). */
 uint64_t sgmv_linear_workspace_bytes(const lora_pool *p, const lora_linear_desc *d, int32_t nproj);
+uint64_t sgmv_linear_max_workspace_bytes(const lora_pool *p, const lora_linear_desc *d,
+                                         int32_t nproj);
+uint64_t sgmv_linear_plan_workspace_bytes(const lora_pool *p, const lora_plan *pl,
+                                          const lora_linear_desc *d, int32_t nproj);
 lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, int32_t nproj,
                         const int32_t *projs, const int32_t *y_offsets, const lora_linear_desc *d,
                         const void *x, int64_t ldx, const void *w, int64_t ldw, const void *bias,
