@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from typing import Optional, Sequence
 
 import numpy as np
@@ -36,8 +37,17 @@ def _stream_handle(stream) -> int:
     return stream.cuda_stream
 
 
+def _i32(value, name: str) -> int:
+    """value as the library's 32-bit integer (ctypes keeps the low bits of a
+    larger one without a word)."""
+    v = operator.index(value)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} {v} does not fit 32 bits")
+    return v
+
+
 def _i32_array(values) -> ctypes.Array:
-    vals = [int(v) for v in values]
+    vals = [_i32(int(v), "value") for v in values]
     return (ctypes.c_int32 * max(len(vals), 1))(*vals)
 
 

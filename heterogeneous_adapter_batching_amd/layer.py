@@ -13,7 +13,7 @@ import functools
 import torch
 
 from ._lib import (ACTS, GATE_ACTS, LORA_BF16, LORA_F32, NORMS, LinearDesc, NormDesc, check, load)
-from .api import _DTYPES, _offsets, _projs
+from .api import _DTYPES, _i32, _offsets, _projs
 
 _f32 = ctypes.c_float
 _CODES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
@@ -98,7 +98,8 @@ def _new(shape, dtype, device, stream):
 @functools.lru_cache(maxsize=1024)
 def _norm_desc(dtype, stream_dtype, T, d, post, pre, gate_act, unit_offset, alpha, beta, eps):
     return ctypes.byref(NormDesc(
-        dtype, stream_dtype, T, d, _code(NORMS, post, "post norm"), _code(NORMS, pre, "pre norm"),
+        dtype, stream_dtype, _i32(T, "num_tokens"), _i32(d, "width"),
+        _code(NORMS, post, "post norm"), _code(NORMS, pre, "pre norm"),
         _code(GATE_ACTS, gate_act, "gate_act"), int(unit_offset), alpha, beta, eps))
 
 
@@ -154,7 +155,8 @@ def block_norm(h, o=None, *, post="none", post_weight=None, post_bias=None, gate
 
 @functools.lru_cache(maxsize=1024)
 def _linear_desc(num_tokens, n, k, dtype, glu, act="none"):
-    return ctypes.byref(LinearDesc(dtype, num_tokens, n, k, _code(ACTS, act, "act"), int(glu)))
+    return ctypes.byref(LinearDesc(dtype, _i32(num_tokens, "num_tokens"), _i32(n, "n"), _i32(k, "k"),
+                                   _code(ACTS, act, "act"), int(glu)))
 
 
 def linear_workspace_bytes(num_tokens: int, n: int, k: int, dtype: str = "bf16",
@@ -175,6 +177,7 @@ def sgmv_linear_workspace_bytes(pool, num_tokens: int, n: int, k: int, nproj: in
     for those of fewer tokens too), or what the given plan takes, which for a
     prompt is a fraction of it."""
     desc = _linear_desc(num_tokens, n, k, pool.desc.dtype, bool(glu))
+    nproj = _i32(nproj, "nproj")
     lib = load()
     if plan is not None:
         if up_to:
@@ -247,4 +250,4 @@ def sgmv_linear(pool, plan, layer, projs, y_offsets, x, w, *, bias=None, act="no
         x, w, bias, act, glu, residual, y, ws, stream,
         lambda d: lib.sgmv_linear_plan_workspace_bytes(pool.handle, plan.handle, d, count),
         lib.sgmv_linear,
-        (pool.handle, plan.handle, layer, count, parr, _offsets(y_offsets)))
+        (pool.handle, plan.handle, _i32(layer, "layer"), count, parr, _offsets(y_offsets)))

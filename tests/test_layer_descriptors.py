@@ -40,3 +40,32 @@ def test_scales_that_are_no_numbers_are_refused(monkeypatch):
         for name in ("alpha", "beta", "eps"):
             with pytest.raises((TypeError, ValueError, RuntimeError)):
                 hab.block_norm(h, h, u=h, h_out=h, **{name: bad})
+
+
+BIG = (1 << 32) + 4          # 4, if only 32 bits of it were kept
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """The C structures hold 32 bits, and ctypes drops the others."""
+    pool = hab.Pool(1, [64], [64], r_max=64, slab_ptr=1 << 20, slab_bytes=1 << 24)
+    for call in (lambda: hab.linear_workspace_bytes(BIG, 4096, 4096),
+                 lambda: hab.linear_workspace_bytes(128, BIG, 4096),
+                 lambda: hab.linear_workspace_bytes(128, 4096, BIG + 4),
+                 lambda: hab.sgmv_linear_workspace_bytes(pool, BIG, 64, 64, 1),
+                 lambda: hab.sgmv_linear_workspace_bytes(pool, 128, 64, 64, BIG - 3),
+                 lambda: hab.api._offsets([BIG]), lambda: hab.api._projs([BIG])):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    monkeypatch.setattr(layer, "_matrix", lambda t, *a: (0, t.shape[1]))
+    monkeypatch.setattr(layer, "_enqueue", lambda *a: pytest.fail("enqueued"))
+    row = torch.zeros(1, 8, dtype=torch.bfloat16)
+    tall = row.expand(BIG, 8)
+    with pytest.raises(ValueError, match="32 bits"):
+        hab.block_norm(tall, h_out=tall, u=tall)
+    with pytest.raises(ValueError, match="32 bits"):
+        hab.frozen_linear(tall, row, y=tall)
+    with pytest.raises(ValueError, match="32 bits"):
+        hab.frozen_linear(row, tall, y=tall)
+    plan = hab.Plan(pool, 1, [0, 1], [-1])
+    with pytest.raises(ValueError, match="32 bits"):
+        hab.sgmv_linear(pool, plan, BIG - 4, [0], [0], row, row, y=row)
