@@ -11,6 +11,8 @@
 // difference of sums, which would cancel for rows with a large mean.  u is
 // formed from the unrounded h': rounding h' first would put the stored
 // type's error into every element of u.
+#include <algorithm>
+
 #include <hip/hip_runtime.h>
 
 #include "device_ops.h"
@@ -256,12 +258,30 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64) void k_block_norm(const NormA
     }
 }
 
+// Row r of a matrix of E at stride ld; no matrix has none.
+template <typename E, typename P> P *from_row(P *p, int64_t r, int64_t ld) {
+    return p ? reinterpret_cast<P *>(reinterpret_cast<uintptr_t>(p) + uint64_t(r * ld) * sizeof(E)) : p;
+}
+
 template <typename T, typename S, int W, int C>
 hipError_t norm_launch(const NormArgs &a, hipStream_t s) {
-    constexpr int ROWS = W < 4 ? 4 / W : 1;
-    const dim3 grid((a.T + ROWS - 1) / ROWS), block(W < 4 ? 256 : W * 64);
-    hipLaunchKernelGGL((k_block_norm<T, S, W, C>), grid, block, 0, s, a);
-    return hipGetLastError();
+    constexpr int ROWS = W < 4 ? 4 / W : 1, THREADS = W < 4 ? 256 : W * 64;
+    // (a launch holds fewer than 2^32 threads)
+    constexpr int64_t MOST = (int64_t(1) << 31) / THREADS * ROWS;
+    for (int64_t r = 0; r < a.T; r += MOST) {
+        NormArgs b = a;
+        b.T = int32_t(std::min<int64_t>(a.T - r, MOST));
+        b.h = from_row<S>(a.h, r, a.ldh);
+        b.o = from_row<T>(a.o, r, a.ldo);
+        b.gate = from_row<T>(a.gate, r, a.ldg);
+        b.h_out = from_row<S>(a.h_out, r, a.ldho);
+        b.u = from_row<T>(a.u, r, a.ldu);
+        const dim3 grid((b.T + ROWS - 1) / ROWS), block(THREADS);
+        hipLaunchKernelGGL((k_block_norm<T, S, W, C>), grid, block, 0, s, b);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // Waves a row and chunks a lane, by the row's width: narrow rows one wave,
