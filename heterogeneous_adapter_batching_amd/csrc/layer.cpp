@@ -80,12 +80,12 @@ namespace lora {
 // parts of 256 x 128 55 and 48, unsplit 128 x 128 58 and 49; 4096 x 4096 x
 // 4096 256 x 256 99 and 102, 128 x 128 231 and 216.
 struct TileCost {
-    int bt, bn, stages;
+    int bt, bn, waves, stages;
     float us[2];                 // float32, bf16 (0: not built)
 };
 constexpr TileCost kTiles[] = {
-    {32, 64, 4, {0.35f, 0.30f}},  {64, 128, 4, {0.85f, 0.55f}},  {128, 64, 4, {0.f, 0.52f}},
-    {128, 128, 4, {1.70f, 0.85f}}, {256, 128, 3, {0.f, 0.95f}}, {256, 256, 2, {0.f, 1.50f}}};
+    {32, 64, 2, 4, {0.35f, 0.30f}},  {64, 128, 4, 4, {0.85f, 0.55f}},  {128, 64, 4, 4, {0.f, 0.52f}},
+    {128, 128, 4, 4, {1.70f, 0.85f}}, {256, 128, 8, 3, {0.f, 0.95f}}, {256, 256, 8, 2, {0.f, 1.50f}}};
 constexpr int kCus = 256;
 // A launch more (the join), and partial sums written and read at about this
 // rate (TB/s = bytes / us / 1e6).
@@ -106,7 +106,7 @@ struct Choice {
     void offer(float t, int bt, int bn, int splits, bool joined, int k_tiles) {
         if (us != 0.f && t >= us) return;
         us = t;
-        pl = LinearPlan{kLinearTile, bt, bn, splits, k_tiles, joined, 0};
+        pl = LinearPlan{kLinearTile, bt, bn, splits, k_tiles, joined, 0, 0};
     }
 };
 
@@ -120,7 +120,7 @@ Choice direct(int dtype, int T, int n, int k, bool glu, int groups, int max_rpad
     for (const TileCost &t : kTiles) {
         const float us = t.us[dtype == LORA_BF16 ? 1 : 0];
         if (us == 0.f) continue;
-        const int64_t tt = (T + t.bt - 1) / t.bt;
+        const int64_t tt = (int64_t(T) + t.bt - 1) / t.bt;
         const int feat = glu ? t.bn / 2 : t.bn;              // gate and up rows in pairs
         float one = float(nk + t.stages) * us;
         if (groups) one += (float(groups) / float(tt) + 1.f) * float(per * (glu ? 2 : 1)) * kDeltaTileUs;
@@ -136,7 +136,7 @@ Choice joined(int dtype, int T, int64_t wide, int k, int least) {
     for (const TileCost &t : kTiles) {
         const float us = t.us[dtype == LORA_BF16 ? 1 : 0];
         if (us == 0.f) continue;
-        const int64_t tiles = int64_t((T + t.bt - 1) / t.bt) * ((wide + t.bn - 1) / t.bn);
+        const int64_t tiles = (int64_t(T) + t.bt - 1) / t.bt * ((wide + t.bn - 1) / t.bn);
         for (int want = least; want <= 16; want = want < 4 ? want + 1 : want * 2) {
             const int kt = (nk + want - 1) / want;
             if (want > 1 && kt < 4) break;                   // too short to fill the pipeline
@@ -149,6 +149,27 @@ Choice joined(int dtype, int T, int64_t wide, int k, int least) {
     return c;
 }
 
+// Tokens with room for a tile's positions past the last in 32 bits.
+constexpr int32_t kMostTokens = INT32_MAX - 1023;
+
+// The threads of the plan's largest launch.
+uint64_t launch_threads(const LinearPlan &pl, int64_t T, int64_t n, bool glu, int cols) {
+    if (pl.kind == kLinearRows) {
+        const uint64_t units = uint64_t((n + 15) / 16);
+        return round_up(units, kXcds) * (units <= 128 ? 512 : 256);
+    }
+    int waves = 0;
+    for (const TileCost &t : kTiles)
+        if (t.bt == pl.bt && t.bn == pl.bn) waves = t.waves;
+    // (see launch_linear)
+    const int64_t feat = glu && !pl.joined ? pl.bn / 2 : pl.bn, rows = glu && pl.joined ? 2 * n : n;
+    const uint64_t units = uint64_t((T + pl.bt - 1) / pl.bt) * uint64_t((rows + feat - 1) / feat) *
+                           uint64_t(pl.splits);
+    const uint64_t tiles = round_up(units, kXcds) * uint64_t(waves) * 64;
+    if (!pl.joined) return tiles;
+    return std::max(tiles, uint64_t((T + 15) / 16) * uint64_t((n + cols - 1) / cols) * 256);
+}
+
 uint64_t partial_bytes(int splits, int T, int64_t wide) {
     return round_up(4ull * uint64_t(splits) * uint64_t(T) * uint64_t(partial_ld(wide)), 256);
 }
@@ -159,11 +180,16 @@ LinearPlan linear_plan(int dtype, int T, int n, int k, bool glu, int groups, int
     // A few tokens: W straight to registers, one launch.  Around 8 to 16
     // tokens it and the tile kernel meet (4096 x 4096: 11.4 us against 13.4
     // for one token, 14.1 against 14.0 for 16).
-    if (T <= kRowsTokens) return LinearPlan{kLinearRows, 16, 16, 1, k_tiles_of(dtype, k), false, 0};
+    LinearPlan pl{kLinearRows, 16, 16, 1, k_tiles_of(dtype, k), false, 0, 0};
+    if (T <= kRowsTokens) {
+        pl.threads = launch_threads(pl, T, n, glu, 0);
+        return pl;
+    }
     const int64_t wide = glu ? 2 * int64_t(n) : n;
     const Choice d = direct(dtype, T, n, k, glu, groups, max_rpad);
     const Choice j = joined(dtype, T, wide, k, groups ? 1 : 2);
-    LinearPlan pl = j.us != 0.f && j.us < d.us ? j.pl : d.pl;
+    pl = j.us != 0.f && j.us < d.us ? j.pl : d.pl;
+    pl.threads = launch_threads(pl, T, n, glu, join_cols(dtype, glu, groups ? max_rpad : 0));
     if (pl.joined) pl.ws_bytes = partial_bytes(pl.splits, T, wide);
     return pl;
 }
@@ -182,7 +208,8 @@ lora_status check_linear_desc(const lora_linear_desc *d) {
     if (!d) return set_errorf(LORA_EINVAL, "null product descriptor");
     if (!is_dtype(d->dtype))
         return set_errorf(LORA_EDTYPE, "dtype %d is neither LORA_F32 nor LORA_BF16", d->dtype);
-    if (d->num_tokens < 0) return set_errorf(LORA_EINVAL, "num_tokens %d < 0", d->num_tokens);
+    if (d->num_tokens < 0 || d->num_tokens > kMostTokens)
+        return set_errorf(LORA_EINVAL, "num_tokens %d not in 0..%d", d->num_tokens, kMostTokens);
     if (d->n < 1 || d->n > (1 << 28)) return set_errorf(LORA_EINVAL, "n %d not in 1..2^28", d->n);
     if (d->k < 8 || d->k % 8 || d->k > LORA_LINEAR_MAX_K)
         return set_errorf(LORA_EINVAL, "k %d is not a multiple of 8 in 8..%d", d->k,
@@ -190,15 +217,18 @@ lora_status check_linear_desc(const lora_linear_desc *d) {
     if (d->act < LORA_ACT_NONE || d->act > LORA_ACT_GELU_TANH)
         return set_errorf(LORA_EINVAL, "act %d is not a lora_act", d->act);
     if (d->glu != 0 && d->glu != 1) return set_errorf(LORA_EINVAL, "glu %d is neither 0 nor 1", d->glu);
-    // tiles, and so workgroups, are counted in 32 bits
+    // tiles are counted in 32 bits
     if (int64_t(d->num_tokens / 64 + 1) * (int64_t(d->n) * (1 + d->glu) / 64 + 1) > (1 << 30))
         return set_errorf(LORA_EINVAL, "a product of %d x %d outputs is too large", d->num_tokens,
                           d->n);
     return LORA_OK;
 }
 
-lora_status check_linear(const LinearCall &c, uint64_t need) {
+lora_status check_linear(const LinearCall &c, const LinearPlan &pl, uint64_t need) {
     const lora_linear_desc &d = *c.d;
+    if (pl.threads >= (uint64_t(1) << 32))
+        return set_errorf(LORA_EINVAL, "a product of %d tokens x %d outputs is more than a launch "
+                          "holds: split it", d.num_tokens, d.n);
     const int32_t es = esize(d.dtype);
     const int64_t T = d.num_tokens, n = d.n, k = d.k, wide = n * (1 + d.glu);
     const Span x{"x", c.x, c.ldx, k, T, es}, w{"w", c.w, c.ldw, k, wide, es},
@@ -284,7 +314,7 @@ lora_status frozen_linear(const lora_linear_desc *d, const void *x, int64_t ldx,
     if (d->num_tokens == 0) return LORA_OK;   // empty batch: no tensor is looked at
     const lora::LinearCall c{d, x, ldx, w, ldw, bias, residual, ldr, y, ldy, ws, ws_bytes};
     const lora::LinearPlan pl = lora::linear_plan(d->dtype, d->num_tokens, d->n, d->k, d->glu != 0, 0, 0);
-    st = lora::check_linear(c, pl.ws_bytes);
+    st = lora::check_linear(c, pl, pl.ws_bytes);
     if (st != LORA_OK) return st;
     return lora::run_linear(c, pl, ws, lora::DeltaArgs{}, static_cast<hipStream_t>(stream));
 }

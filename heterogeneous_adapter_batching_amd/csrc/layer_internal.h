@@ -109,7 +109,19 @@ struct LinearPlan {
     int32_t splits, k_tiles;     // parts along K, and K tiles of one
     bool joined;
     uint64_t ws_bytes;           // of the partial products
+    uint64_t threads;            // of its largest launch
 };
+// Outputs of a workgroup of the join (max_rpad 0: no adapters).  A wave has 16
+// columns, and 64 for bf16 adapters beyond one K-step, whose operand (6
+// vectors a lane) then serves more rows of B (a gated decode batch of ranks 8
+// to 64: 53.6, 42.2 and 40.7 us with 16, 32 and 64; rank 16 q/k/v 12.7 us with
+// 16, 13.4 with 32).
+constexpr int join_tiles(int dtype, int max_rpad) {
+    return dtype == LORA_BF16 && max_rpad > one_step_rank(dtype) ? 4 : 1;
+}
+constexpr int join_cols(int dtype, bool glu, int max_rpad) {
+    return (glu ? 32 : 64) * join_tiles(dtype, max_rpad);
+}
 constexpr int kKBytes = 128;     // bytes of a row a K tile covers
 constexpr int kRowsTokens = 12;  // most tokens of the rows kernel
 // groups, max_rpad: adapter groups of the batch and their largest padded rank
@@ -134,7 +146,7 @@ struct LinearCall {
 };
 lora_status check_linear_desc(const lora_linear_desc *d);
 // `need`: the workspace bytes of the call
-lora_status check_linear(const LinearCall &c, uint64_t need);
+lora_status check_linear(const LinearCall &c, const LinearPlan &pl, uint64_t need);
 // Enqueues a checked call; partial sums at `partial` (of the plan's ws_bytes).
 lora_status run_linear(const LinearCall &c, const LinearPlan &pl, void *partial,
                        const DeltaArgs &delta, hipStream_t s);

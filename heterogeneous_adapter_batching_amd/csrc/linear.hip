@@ -1101,15 +1101,12 @@ hipError_t rows_launch(const LinearArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Outputs of a join wave: 16, and 64 for bf16 adapters beyond one K-step,
-// whose operand (6 vectors a lane) then serves more rows of B (a gated decode
-// batch of ranks 8 to 64: 53.6, 42.2 and 40.7 us with 16, 32 and 64; rank 16
-// q/k/v 12.7 us with 16, 13.4 with 32).
 template <typename T, bool GLU> void join_launch(const LinearArgs &a, hipStream_t s) {
-    constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E), GM = sizeof(T) == 2 ? 4 : 1;
-    const int ks = delta_steps<T>(a), g = ks > 1 ? GM : 1;
-    const int cols = (GLU ? 32 : 64) * g;        // outputs of a workgroup
-    const dim3 grid(((a.T + 15) / 16) * ((a.n + cols - 1) / cols)), block(256);
+    constexpr int DTYPE = sizeof(T) == 2 ? LORA_BF16 : LORA_F32;
+    constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E), GM = join_tiles(DTYPE, LORA_MAX_RANK);
+    const int ks = delta_steps<T>(a);
+    const int cols = join_cols(DTYPE, GLU, ks ? a.delta.max_rpad : 0);
+    const dim3 grid((a.T + 15) / 16 * ((a.n + cols - 1) / cols)), block(256);
     if (ks == 0) hipLaunchKernelGGL((k_linear_join<T, GLU, 0, 1>), grid, block, 0, s, a);
     else if (ks == 1) hipLaunchKernelGGL((k_linear_join<T, GLU, 1, 1>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((k_linear_join<T, GLU, KM, GM>), grid, block, 0, s, a);

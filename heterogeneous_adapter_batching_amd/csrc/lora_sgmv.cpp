@@ -2055,7 +2055,7 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
     const lora::LinearCall c{d, x, ldx, w, ldw, bias, residual, ldr, y, ldy, ws, ws_bytes};
     const lora::LinearPlan lp = plan_of_product(pl, d);
     const uint64_t v_bytes = linear_operand_bytes(p, d, nproj);
-    st = lora::check_linear(c, v_bytes + lp.ws_bytes);
+    st = lora::check_linear(c, lp, v_bytes + lp.ws_bytes);
     if (st != LORA_OK) return st;
     const uintptr_t wl = reinterpret_cast<uintptr_t>(ws), pw0 = reinterpret_cast<uintptr_t>(pl->ws);
     if (wl < pw0 + pl->lay.ws_bytes && pw0 < wl + v_bytes + lp.ws_bytes)

@@ -629,8 +629,8 @@ typedef enum {
 
 typedef struct {
     int32_t dtype;      /* lora_dtype of x, w, bias, residual and y */
-    int32_t num_tokens; /* T >= 0 */
-    int32_t n;          /* width of y, >= 1 */
+    int32_t num_tokens; /* T >= 0, less than 2^31 - 1023 */
+    int32_t n;          /* width of y, >= 1 (a few tokens: less than 2^28 - 127) */
     int32_t k;          /* width of x: a multiple of 8, at most LORA_LINEAR_MAX_K */
     int32_t act;        /* lora_act */
     int32_t glu;        /* 1: w holds 2 n rows, the gate's n, then the up's n */
