@@ -70,7 +70,12 @@ def _enqueue(fn, args, device, stream):
     """Calls the library with `stream` (None: the device's current one) as the
     last argument, with `device` current for the launches."""
     index = device.index
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, not on {device}")
+        handle = stream.cuda_stream
     if index == torch._C._cuda_getDevice():
         check(fn(*args, handle))
     else:
@@ -187,11 +192,15 @@ def sgmv_linear_workspace_bytes(pool, num_tokens: int, n: int, k: int, nproj: in
     return int(ask(pool.handle, desc, nproj))
 
 
-def _linear_call(x, w, bias, act, glu, residual, y, ws, stream, need, fn, head):
+def _linear_call(x, w, bias, act, glu, residual, y, ws, stream, need, fn, head, beside=()):
     """Checks the tensors of a product call, makes y and the workspace where
-    they are not given, and calls fn(*head, descriptor, tensors, stream)."""
+    they are not given, and calls fn(*head, descriptor, tensors, stream).
+    beside: what else the call reads, as (name, tensor or None)."""
     xp, ldx = _matrix(x, "x", None, None, None)
     dev, dt = x.device, x.dtype
+    for name, t in beside:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
     wp, ldw = _matrix(w, "w", None, dt, dev)
     (T, k), (wide, kw) = x.shape, w.shape
     if kw != k:
@@ -250,4 +259,5 @@ def sgmv_linear(pool, plan, layer, projs, y_offsets, x, w, *, bias=None, act="no
         x, w, bias, act, glu, residual, y, ws, stream,
         lambda d: lib.sgmv_linear_plan_workspace_bytes(pool.handle, plan.handle, d, count),
         lib.sgmv_linear,
-        (pool.handle, plan.handle, _i32(layer, "layer"), count, parr, _offsets(y_offsets)))
+        (pool.handle, plan.handle, _i32(layer, "layer"), count, parr, _offsets(y_offsets)),
+        (("the pool", pool.slab), ("the plan's workspace", plan.ws)))
