@@ -122,12 +122,33 @@ template <> struct Run4<float> {
     }
 };
 
-// 1 / (1 + exp(-v)).  For bf16 outputs the hardware's exponential and
-// reciprocal (a few 2^-22 relative, far inside half a bf16 step); float32
-// outputs take the full-precision functions.
-template <typename T> __device__ __forceinline__ float logistic(float v) {
-    if constexpr (sizeof(T) == 2) return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
-    return 1.0f / (1.0f + expf(-v));
+// v[i] / (1 + exp(-z[i])).  For bf16 outputs the hardware's exponential and
+// reciprocal (2^-22 relative each, and |z| 1.44 2^-24 for the exponent's
+// rounding, inside half a bf16 step); float32 outputs take the full-precision
+// functions.  Left of -87 the reciprocal would be flushed to zero, and beyond
+// -88 the exponential leaves float32, where silu's v e^v is still a normal
+// number (to -91): there v e / (1 + e) with e = exp(z) as the square of
+// exp(z / 2), in a branch that waves without such a z pass by (that form in
+// every wave took a gated prompt of 4096 tokens from 723 to 732 us).
+template <typename T, int N>
+__device__ __forceinline__ void times_logistic(float (&v)[N], const float (&z)[N]) {
+    float least = z[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) least = fminf(least, z[i]);
+    auto near_zero = [&](int i) {
+        if constexpr (sizeof(T) == 2) return v[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-z[i]));
+        return v[i] * (1.0f / (1.0f + expf(-z[i])));
+    };
+    if (__builtin_amdgcn_ballot_w64(least < -87.0f)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float h = expf(0.5f * z[i]);
+            v[i] = z[i] < -87.0f ? v[i] * h * h / (1.0f + h * h) : near_zero(i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = near_zero(i);
+    }
 }
 
 template <typename T, int N> __device__ __forceinline__ void activate(float (&v)[N], int act) {
@@ -136,19 +157,25 @@ template <typename T, int N> __device__ __forceinline__ void activate(float (&v)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // NaN stays NaN
         break;
-    case LORA_ACT_SILU:
+    case LORA_ACT_SILU: {
+        float z[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] *= logistic<T>(v[i]);
+        for (int i = 0; i < N; ++i) z[i] = v[i];
+        times_logistic<T, N>(v, z);
         break;
+    }
     case LORA_ACT_GELU:
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] *= 0.5f * erfcf(-0.70710678118654752f * v[i]);
         break;
-    case LORA_ACT_GELU_TANH:                         // (1 + tanh z) / 2 = logistic(2 z)
+    case LORA_ACT_GELU_TANH: {                       // (1 + tanh z) / 2 = logistic(2 z)
+        float z[N];
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            v[i] *= logistic<T>(1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+            z[i] = 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]);
+        times_logistic<T, N>(v, z);
         break;
+    }
     default: break;
     }
 }
