@@ -20,8 +20,9 @@ from .api import (  # noqa: F401
     sgmv_expand_partials, sgmv_expand_partials_sigma, sgmv_fused_static, plan_opts_default,
     debug_checks,
 )
-# The operators around the delta take torch tensors only, so their module is
-# imported on first use: the package itself loads without torch.
+# The operators around the delta take torch tensors only, so their module,
+# which imports torch, is loaded on first use (without torch the names are
+# there all the same, and their workspace sizes can be asked for).
 _LAYER = ("block_norm", "frozen_linear", "linear_workspace_bytes", "sgmv_linear",
           "sgmv_linear_workspace_bytes")
 

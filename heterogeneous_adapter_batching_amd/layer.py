@@ -10,13 +10,17 @@ from __future__ import annotations
 import ctypes
 import functools
 
-import torch
+try:
+    import torch
+except ImportError:                    # sizes can be asked for without it
+    torch = None
 
 from ._lib import (ACTS, GATE_ACTS, LORA_BF16, LORA_F32, NORMS, LinearDesc, NormDesc, check, load)
 from .api import _DTYPES, _i32, _offsets, _projs
 
 _f32 = ctypes.c_float
-_CODES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
+_CODES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32} if torch else {}
+_Tensor = torch.Tensor if torch else ()
 
 
 def _dtype_code(dtype, name):
@@ -29,7 +33,7 @@ def _dtype_code(dtype, name):
 def _matrix(t, name, shape, dtype, device):
     """A 2-D CUDA tensor with contiguous rows, as (pointer, row stride); None
     for shape, dtype or device: any."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     s = t.shape
     if s != shape and (shape is not None or len(s) != 2):
@@ -49,7 +53,7 @@ def _vector(t, name, n, dtype, device):
     """A contiguous vector of n elements, or None: its pointer (0 for None)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {n}, got {list(t.shape)}")
