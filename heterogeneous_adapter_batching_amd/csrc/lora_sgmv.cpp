@@ -165,7 +165,7 @@ struct PlanCounts {
     int64_t T = 0, nb = 0, rt = 0, mb = 0;   // rows (tokens, or (token, slot) rows), blocks,
     int32_t tt = 1;                          // rank tiles, merge blocks; tiles per block
     bool merge = false;                      // a merge plan (its shrink covers every tile)
-    int64_t ng = 0;                          // adapter groups
+    int64_t ng = 0, np = 0;                  // the product's tables: groups' rows, positions
     int64_t rt_long = 0;                     // a plain plan: rank tiles of long groups
     int64_t long_rows = 0;                   // ... and rows of the long groups' v region
 };
@@ -224,8 +224,8 @@ PlanLayout plan_layout(const lora_pool_desc &d, const PlanCounts &c, int32_t mp,
     L.off_tsig = o;    o = round_up(o + 4ull * T, 256);
     L.off_tw = o;      o = round_up(o + 4ull * T, 256);
     L.off_mblocks = o; o = round_up(o + sizeof(lora::MergeBlock) * uint64_t(c.mb), 256);
-    L.off_groups = o;  o = round_up(o + sizeof(lora::GroupRow) * uint64_t(c.ng + 1), 256);
-    L.off_pos = o;     o = round_up(o + sizeof(lora::PosRow) * T, 256);
+    L.off_groups = o;  o = round_up(o + sizeof(lora::GroupRow) * uint64_t(c.ng), 256);
+    L.off_pos = o;     o = round_up(o + sizeof(lora::PosRow) * uint64_t(c.np), 256);
     L.image_bytes = o;
     // the shrink's partial tiles: every rank tile at the plan's tiles per
     // block (a merge plan), or the short groups' tiles at one 16-token tile
@@ -257,7 +257,7 @@ struct lora_plan {
     std::vector<int32_t> token_sigma;    // core index per plan-order row (-1: none)
     std::vector<float> token_weight;     // weight per plan-order row (weighted plans)
     // the adapter groups and each plan position's (-1: none), for the product
-    // with adapters
+    // with adapters: empty in plans that it does not take (merges, cores)
     std::vector<lora::GroupRow> group_rows{lora::GroupRow{0u, 0u, 0, 0}};
     std::vector<lora::PosRow> positions;
     std::vector<int32_t> token_slot;     // merge slot per plan-order row (-1: none)
@@ -312,7 +312,8 @@ struct lora_plan {
         c.T = rows();
         c.mb = int64_t(mblocks.size());
         c.nb = nb_all();
-        c.ng = int64_t(group_rows.size()) - 1;
+        c.ng = int64_t(group_rows.size());
+        c.np = int64_t(positions.size());
         c.rt = rt_total();
         c.tt = tt;
         c.merge = merge_k > 0;
@@ -711,6 +712,11 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
     pl->token_group.assign(T, -1);
     pl->group_rows.clear();
     pl->positions.clear();
+    // whether the product with adapters takes the plan: one run a row (no
+    // merge), none with a core
+    const bool product = std::none_of(runs.begin(), runs.end(), [](const Run &r) {
+        return r.slot >= 0 || (r.sigma >= 0 && r.adapter >= 0 && r.end > r.start);
+    });
 
     // groups in first-appearance order (runs with rows only); a member is a
     // (row, run) pair
@@ -763,9 +769,10 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
     auto add_group = [&](const std::vector<std::pair<int32_t, int32_t>> &rows, int32_t g,
                          const Slot *sl) {
         const int32_t base = int32_t(pl->token_order.size());
-        pl->group_rows.push_back(lora::GroupRow{sl ? uint32_t(sl->off & 0xffffffffu) : 0u,
-                                                sl ? uint32_t(sl->off >> 32) : 0u,
-                                                sl ? sl->r_pad : 0, base});
+        if (product)
+            pl->group_rows.push_back(lora::GroupRow{sl ? uint32_t(sl->off & 0xffffffffu) : 0u,
+                                                    sl ? uint32_t(sl->off >> 32) : 0u,
+                                                    sl ? sl->r_pad : 0, base});
         const int32_t rt = sl ? (sl->r_pad + lora::kTile - 1) / lora::kTile : 0;
         const bool lg = sl && use_long && rows.size() >= long_group;
         const int32_t smax = lg ? lora::kMaxBlockTokens : lora::kTile;
@@ -817,19 +824,21 @@ void plan_build(lora_plan *pl, const lora_pool *p, int32_t T, const std::vector<
             pl->token_sigma.push_back(rn ? rn->sigma : -1);
             pl->token_weight.push_back(rn ? rn->weight : 1.0f);
             pl->token_slot.push_back(rn ? rn->slot : -1);
-            lora::PosRow pr{};
-            pr.group = -1;
-            if (sl) {
-                const size_t at = pl->positions.size() - size_t(base);
-                pr.ext_lo = uint32_t(sl->off & 0xffffffffu);
-                pr.ext_hi = uint32_t(sl->off >> 32);
-                pr.r_pad = sl->r_pad;
-                pr.group = g;
-                pr.rt = row_rt[at];
-                pr.slot = row_slot[at];
-                pr.scale = sl->scale * (rn ? rn->weight : 1.0f);
+            if (product) {
+                lora::PosRow pr{};
+                pr.group = -1;
+                if (sl) {
+                    const size_t at = pl->positions.size() - size_t(base);
+                    pr.ext_lo = uint32_t(sl->off & 0xffffffffu);
+                    pr.ext_hi = uint32_t(sl->off >> 32);
+                    pr.r_pad = sl->r_pad;
+                    pr.group = g;
+                    pr.rt = row_rt[at];
+                    pr.slot = row_slot[at];
+                    pr.scale = sl->scale * (rn ? rn->weight : 1.0f);
+                }
+                pl->positions.push_back(pr);
             }
-            pl->positions.push_back(pr);
             if (rn) pl->max_sigma = std::max(pl->max_sigma, rn->sigma);
         }
     };
@@ -1079,7 +1088,8 @@ uint64_t lora_workspace_bytes(const lora_pool *p, int32_t num_tokens, int32_t nu
     PlanCounts c;
     c.T = T;
     c.nb = T;
-    c.ng = std::min<int64_t>(num_segs, T);
+    c.ng = std::min<int64_t>(num_segs, T) + 1;
+    c.np = T;
     const int64_t sblocks = std::min<int64_t>(T, T / lora::kTile + 1 + std::min<int64_t>(num_segs, T));
     c.rt = sblocks * ((p->d.r_max + lora::kTile - 1) / lora::kTile);
     c.tt = long_ok ? lora::kMaxBlockTokens / lora::kTile : 1;
@@ -1124,9 +1134,12 @@ lora_status lora_plan_upload(lora_plan *pl, void *ws, uint64_t ws_bytes, int32_t
     if (R) std::memcpy(img + lay.off_tok, pl->token_order.data(), 4ull * R);
     if (R) std::memcpy(img + lay.off_tsig, pl->token_sigma.data(), 4ull * R);
     if (R && pl->weighted) std::memcpy(img + lay.off_tw, pl->token_weight.data(), 4ull * R);
-    std::memcpy(img + lay.off_groups, pl->group_rows.data(),
-                sizeof(lora::GroupRow) * pl->group_rows.size());
-    if (R) std::memcpy(img + lay.off_pos, pl->positions.data(), sizeof(lora::PosRow) * R);
+    if (!pl->group_rows.empty())
+        std::memcpy(img + lay.off_groups, pl->group_rows.data(),
+                    sizeof(lora::GroupRow) * pl->group_rows.size());
+    if (!pl->positions.empty())
+        std::memcpy(img + lay.off_pos, pl->positions.data(),
+                    sizeof(lora::PosRow) * pl->positions.size());
     if (!pl->mblocks.empty())
         std::memcpy(img + lay.off_mblocks, pl->mblocks.data(),
                     sizeof(lora::MergeBlock) * pl->mblocks.size());
