@@ -139,7 +139,6 @@ SIGNATURES = {
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
-LORA_NORM_MAX_WIDTH = 32768
 
 LORA_SIGMA_DIAG, LORA_SIGMA_FULL = 1, 2
 

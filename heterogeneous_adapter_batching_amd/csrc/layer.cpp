@@ -119,7 +119,7 @@ Choice direct(int dtype, int T, int n, int k, bool glu, int groups, int max_rpad
     const int per = ((dtype == LORA_BF16 ? 3 : 1) * max_rpad * esize(dtype) / 16 + 7) / 8;
     for (const TileCost &t : kTiles) {
         const float us = t.us[dtype == LORA_BF16 ? 1 : 0];
-        if (us == 0.f) continue;
+        if (us == 0.f || (!groups && !plain_tile(dtype, t.bt, t.bn))) continue;
         const int64_t tt = (int64_t(T) + t.bt - 1) / t.bt;
         const int feat = glu ? t.bn / 2 : t.bn;              // gate and up rows in pairs
         float one = float(nk + t.stages) * us;
@@ -135,7 +135,7 @@ Choice joined(int dtype, int T, int64_t wide, int k, int least) {
     const int nk = k_tiles_of(dtype, k);
     for (const TileCost &t : kTiles) {
         const float us = t.us[dtype == LORA_BF16 ? 1 : 0];
-        if (us == 0.f) continue;
+        if (us == 0.f || !plain_tile(dtype, t.bt, t.bn)) continue;
         const int64_t tiles = (int64_t(T) + t.bt - 1) / t.bt * ((wide + t.bn - 1) / t.bn);
         for (int want = least; want <= 16; want = want < 4 ? want + 1 : want * 2) {
             const int kt = (nk + want - 1) / want;

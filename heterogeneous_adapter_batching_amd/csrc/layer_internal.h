@@ -122,6 +122,11 @@ constexpr int join_tiles(int dtype, int max_rpad) {
 constexpr int join_cols(int dtype, bool glu, int max_rpad) {
     return (glu ? 32 : 64) * join_tiles(dtype, max_rpad);
 }
+// Whether a tile is built for products without adapters and for parts.
+// float32's 128 x 128 is not: its K tile takes twice 64 x 128's, so that it is
+// the better one only where the delta's K tiles, one set a token tile, weigh
+// (683 x 3597 x 32 with one adapter).
+constexpr bool plain_tile(int dtype, int bt, int bn) { return dtype == LORA_BF16 || bt * bn < 128 * 128; }
 constexpr int kKBytes = 128;     // bytes of a row a K tile covers
 constexpr int kRowsTokens = 12;  // most tokens of the rows kernel
 // groups, max_rpad: adapter groups of the batch and their largest padded rank

@@ -1108,12 +1108,14 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinearArgs a) {
 }
 
 // ------------------------------------------------------------- launches -----
+template <typename T> constexpr int dtype_of = sizeof(T) == 2 ? LORA_BF16 : LORA_F32;
+
 dim3 grid_of(int units) { return dim3((units + kXcds - 1) / kXcds * kXcds); }
 
 // K-steps of the delta's largest rank, as the kernels are built for it
 template <typename T> int delta_steps(const LinearArgs &a) {
     if (!a.delta.order) return 0;
-    return a.delta.max_rpad <= one_step_rank(sizeof(T) == 2 ? LORA_BF16 : LORA_F32)
+    return a.delta.max_rpad <= one_step_rank(dtype_of<T>)
                ? 1 : LORA_MAX_RANK / (4 * Elem<T>::E);
 }
 
@@ -1129,10 +1131,10 @@ hipError_t rows_launch(const LinearArgs &a, hipStream_t s) {
 }
 
 template <typename T, bool GLU> void join_launch(const LinearArgs &a, hipStream_t s) {
-    constexpr int DTYPE = sizeof(T) == 2 ? LORA_BF16 : LORA_F32;
-    constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E), GM = join_tiles(DTYPE, LORA_MAX_RANK);
+    constexpr int KM = LORA_MAX_RANK / (4 * Elem<T>::E);
+    constexpr int GM = join_tiles(dtype_of<T>, LORA_MAX_RANK);
     const int ks = delta_steps<T>(a);
-    const int cols = join_cols(DTYPE, GLU, ks ? a.delta.max_rpad : 0);
+    const int cols = join_cols(dtype_of<T>, GLU, ks ? a.delta.max_rpad : 0);
     const dim3 grid((a.T + 15) / 16 * ((a.n + cols - 1) / cols)), block(256);
     if (ks == 0) hipLaunchKernelGGL((k_linear_join<T, GLU, 0, 1>), grid, block, 0, s, a);
     else if (ks == 1) hipLaunchKernelGGL((k_linear_join<T, GLU, 1, 1>), grid, block, 0, s, a);
@@ -1149,32 +1151,36 @@ hipError_t rows_dispatch(const LinearArgs &a, hipStream_t s) {
 }
 
 template <typename T, int BT, int BN, int WT, int WN, int S, bool GLU>
-void direct_launch(const LinearArgs &a, dim3 grid, dim3 block, hipStream_t s) {
+hipError_t direct_launch(const LinearArgs &a, dim3 grid, dim3 block, hipStream_t s) {
     if (a.delta.order)
         hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, GLU, false, true>), grid, block, 0, s, a);
+    else if constexpr (!plain_tile(dtype_of<T>, BT, BN))
+        return hipErrorInvalidValue;
     else if (a.tiles_t == 1)
         hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, GLU, false, false, true>), grid, block, 0, s, a);
     else
         hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, GLU, false, false>), grid, block, 0, s, a);
+    return hipGetLastError();
 }
 
 template <typename T, int BT, int BN, int WT, int WN, int S>
 hipError_t tile_launch(const LinearPlan &pl, bool glu, const LinearArgs &a, hipStream_t s) {
     const dim3 grid = grid_of(a.units), block(WT * WN * 64);
-    if (!pl.joined) {
-        if (glu) direct_launch<T, BT, BN, WT, WN, S, true>(a, grid, block, s);
-        else direct_launch<T, BT, BN, WT, WN, S, false>(a, grid, block, s);
+    if (!pl.joined)
+        return glu ? direct_launch<T, BT, BN, WT, WN, S, true>(a, grid, block, s)
+                   : direct_launch<T, BT, BN, WT, WN, S, false>(a, grid, block, s);
+    if constexpr (plain_tile(dtype_of<T>, BT, BN)) {
+        if (a.tiles_t == 1)
+            hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, true, false, true>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, true, false>), grid, block, 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        if (glu) join_launch<T, true>(a, s);
+        else join_launch<T, false>(a, s);
         return hipGetLastError();
     }
-    if (a.tiles_t == 1)
-        hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, true, false, true>), grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL((k_linear_tile<T, BT, BN, WT, WN, S, false, true, false>), grid, block, 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (glu) join_launch<T, true>(a, s);
-    else join_launch<T, false>(a, s);
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 template <typename T>
