@@ -287,9 +287,13 @@ hipError_t norm_launch(const NormArgs &a, hipStream_t s) {
 // Waves a row and chunks a lane, by the row's width: narrow rows one wave,
 // else as many waves as leave a lane one or two chunks.  16384 rows of 4096
 // (bf16 blocks, float32 stream) take 138 us with 8 waves of one chunk and 144
-// with 4 of two (5.8 and 5.6 TB/s); 1021 float32 rows of 5003 27 us with 4
-// waves of four chunks, 29 with 8 of two and 36 with 16 of one (a third of
-// whose lanes idle).
+// with 4 of two (5.8 and 5.6 TB/s).  float32 rows of 4097 to 5120 leave a
+// third of 8 waves' second chunks idle: many of them go faster with 4 waves of
+// four chunks, few of them, and wider ones, with 8 of two (us, layer norms with
+// biases and gate rows, 4 of four against 8 of two: 1021 x 5003 29.4 and 30.6,
+// 700 x 5120 22.4 and 23.9; but 512 x 5003 19.5 and 17.9, 64 x 5003 13.0 and
+// 9.1, 4096 x 7000 128 and 120, 4096 x 8192 139 and 132; 16 of one are behind
+// at each: 39.1, 28.4, 21.6, 8.5, 167 and 182).
 template <typename T, typename S> hipError_t norm_types(const NormArgs &a, hipStream_t s) {
     const int lanes = (a.d + kNormChunk - 1) / kNormChunk;   // chunks of the row
     if (lanes <= 64) return norm_launch<T, S, 1, 1>(a, s);
@@ -297,10 +301,9 @@ template <typename T, typename S> hipError_t norm_types(const NormArgs &a, hipSt
     if (lanes <= 256) return norm_launch<T, S, 4, 1>(a, s);
     if (lanes <= 512) return norm_launch<T, S, 8, 1>(a, s);
     if constexpr (sizeof(T) == 4) {
-        if (lanes <= 1024) return norm_launch<T, S, 4, 4>(a, s);
-    } else {
-        if (lanes <= 1024) return norm_launch<T, S, 8, 2>(a, s);
+        if (lanes <= 640 && a.T > 512) return norm_launch<T, S, 4, 4>(a, s);
     }
+    if (lanes <= 1024) return norm_launch<T, S, 8, 2>(a, s);
     if (lanes <= 2048) return norm_launch<T, S, 16, 2>(a, s);
     return norm_launch<T, S, 16, 4>(a, s);
 }
