@@ -435,11 +435,19 @@ class Plan:
         return int(self.lib.lora_plan_workspace_bytes(self._h, max_proj))
 
     def upload(self, max_proj: int = 3, ws=None, stream=None):
-        """Copy the plan into a device workspace (allocated here unless given)."""
+        """Copy the plan into a device workspace (allocated here unless given:
+        on the pool's device, from the memory of the stream that the copy is
+        queued on, behind which it is given back)."""
         torch = _torch()
         need = self.workspace_bytes(max_proj)
         if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+            device = "cuda" if self.pool.slab is None else self.pool.slab.device
+            if stream is None:
+                ws = torch.empty(need, dtype=torch.uint8, device=device)
+            else:
+                with torch.cuda.stream(stream):
+                    ws = torch.empty(need, dtype=torch.uint8, device=device)
+                ws.record_stream(torch.cuda.current_stream(ws.device))
         check(self.lib.lora_plan_upload(self._h, ctypes.c_void_p(ws.data_ptr()),
                                         ws.numel() * ws.element_size(), max_proj,
                                         _stream_handle(stream)))

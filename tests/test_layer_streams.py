@@ -22,7 +22,7 @@ class Allocator:
         self.current = before
 
     def empty(self, shape, dtype=None, device=None):
-        t = types.SimpleNamespace(pool=self.current, uses=[])
+        t = types.SimpleNamespace(pool=self.current, uses=[], device=device)
         t.record_stream = t.uses.append
         self.made.append(t)
         return t
@@ -45,3 +45,28 @@ def test_no_stream_takes_the_current_one(monkeypatch):
     monkeypatch.setattr(layer, "torch", fake)
     t = layer._new((4, 8), "bf16", "cuda:0", None)
     assert t.pool == "the caller's" and t.uses == []
+
+
+def test_a_plans_workspace_comes_from_its_upload_stream(monkeypatch):
+    """The upload writes the workspace at once, on the stream it is given."""
+    import heterogeneous_adapter_batching_amd as hab
+    pool = hab.Pool(1, [64], [64], r_max=8, slab_ptr=1 << 30, slab_bytes=1 << 20)
+    plan = hab.Plan(pool, 4, [0, 4], [-1])
+    fake = Allocator()
+    fake.uint8 = "uint8"
+    empty = fake.empty
+
+    def sized(n, dtype=None, device=None):
+        t = empty(n, dtype, device)
+        t.data_ptr, t.numel, t.element_size = (lambda: 0), (lambda: n), (lambda: 1)
+        return t
+
+    fake.empty = sized
+    sent = []
+    plan.lib = types.SimpleNamespace(lora_plan_workspace_bytes=lambda *a: 512,
+                                     lora_plan_upload=lambda h, ws, n, mp, s: sent.append(s) or 0,
+                                     lora_plan_destroy=lambda h: 0)
+    monkeypatch.setattr(hab.api, "_torch", lambda: fake)
+    side = types.SimpleNamespace(cuda_stream=7)
+    ws = plan.upload(1, stream=side).ws
+    assert ws.pool is side and ws.uses == ["the caller's"] and sent == [7]
