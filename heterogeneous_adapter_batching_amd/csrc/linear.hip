@@ -122,33 +122,20 @@ template <> struct Run4<float> {
     }
 };
 
-// v[i] / (1 + exp(-z[i])).  For bf16 outputs the hardware's exponential and
+// v / (1 + exp(-z)).  For bf16 outputs the hardware's exponential and
 // reciprocal (2^-22 relative each, and |z| 1.44 2^-24 for the exponent's
-// rounding, inside half a bf16 step); float32 outputs take the full-precision
-// functions.  Left of -87 the reciprocal would be flushed to zero, and beyond
-// -88 the exponential leaves float32, where silu's v e^v is still a normal
-// number (to -91): there v e / (1 + e) with e = exp(z) as the square of
-// exp(z / 2), in a branch that waves without such a z pass by (that form in
-// every wave took a gated prompt of 4096 tokens from 723 to 732 us).
-template <typename T, int N>
-__device__ __forceinline__ void times_logistic(float (&v)[N], const float (&z)[N]) {
-    float least = z[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) least = fminf(least, z[i]);
-    auto near_zero = [&](int i) {
-        if constexpr (sizeof(T) == 2) return v[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-z[i]));
-        return v[i] * (1.0f / (1.0f + expf(-z[i])));
-    };
-    if (__builtin_amdgcn_ballot_w64(least < -87.0f)) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float h = expf(0.5f * z[i]);
-            v[i] = z[i] < -87.0f ? v[i] * h * h / (1.0f + h * h) : near_zero(i);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = near_zero(i);
+// rounding, inside half a bf16 step), of 2^-8 times the sum: the sum itself
+// leaves float32 left of -88 and its reciprocal is flushed to zero left of
+// -87, where silu's v e^v is still a normal number, to -91.  (v / 256 keeps 15
+// bits down to the least normal v.)  float32 outputs take the full-precision
+// functions, left of zero as v e / (1 + e) with e = exp(z).
+template <typename T> __device__ __forceinline__ float times_logistic(float v, float z) {
+    if constexpr (sizeof(T) == 2) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z, -1.4426950408889634f, -8.0f));
+        return v * 0x1p-8f * __builtin_amdgcn_rcpf(0x1p-8f + e);
     }
+    const float e = expf(-fabsf(z));
+    return (z < 0.f ? v * e : v) / (1.0f + e);
 }
 
 template <typename T, int N> __device__ __forceinline__ void activate(float (&v)[N], int act) {
@@ -157,25 +144,20 @@ template <typename T, int N> __device__ __forceinline__ void activate(float (&v)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // NaN stays NaN
         break;
-    case LORA_ACT_SILU: {
-        float z[N];
+    case LORA_ACT_SILU:
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = v[i];
-        times_logistic<T, N>(v, z);
+        for (int i = 0; i < N; ++i) v[i] = times_logistic<T>(v[i], v[i]);
         break;
-    }
     case LORA_ACT_GELU:
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] *= 0.5f * erfcf(-0.70710678118654752f * v[i]);
         break;
-    case LORA_ACT_GELU_TANH: {                       // (1 + tanh z) / 2 = logistic(2 z)
-        float z[N];
+    case LORA_ACT_GELU_TANH:                         // (1 + tanh z) / 2 = logistic(2 z)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            z[i] = 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]);
-        times_logistic<T, N>(v, z);
+            v[i] = times_logistic<T>(
+                v[i], 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
         break;
-    }
     default: break;
     }
 }
