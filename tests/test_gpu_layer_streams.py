@@ -70,3 +70,31 @@ def test_beside_work_on_the_current_stream():
     assert [float(v) for v in sums] == expect
     for _, _, _, want, _, got in runs:
         assert all(torch.equal(a, b) for ts in got for a, b in zip(ts, want))
+
+
+def test_captured_on_a_forked_stream():
+    """A capture whose calls make their outputs and workspaces, on the capturing
+    stream and on one forked from it; replayed on new inputs between eager
+    calls."""
+    T = 100
+    starts, ids = segments(5, T, 4, 3)
+    m = Adapted(5, T, 1032, [520], [8, 16, 64, 32], ids, starts)
+    g = torch.Generator().manual_seed(5)
+    x, w = torch.randn(T, 1032, generator=g).to(BF16).cuda(), torch.randn(520, 1032, generator=g).to(BF16).cuda()
+    calls(m, x, w, None)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        here = calls(m, x, w, main)
+        side.wait_stream(main)
+        forked = calls(m, x, w, side)
+        main.wait_stream(side)
+    for _ in range(3):
+        x.copy_(torch.randn(T, 1032, generator=g).to(BF16))
+        want = calls(m, x, w, None)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got in (here, forked):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
