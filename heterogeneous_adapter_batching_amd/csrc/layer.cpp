@@ -71,10 +71,11 @@ namespace lora {
 
 // What the plan of a product chooses from, and what it goes by: the time of
 // one K tile (128 bytes of every row) of one workgroup with a CU to itself,
-// measured on MI355X with W from HBM (bf16 over 1024..28672 rows of W, K 4096
-// and 14336, 17..4096 tokens; float32 is bound by its matrix rate), and the
-// stages that fill before the first.  Small tiles cost little each and keep
-// every CU busy; large ones read less per product.  Estimated and measured
+// and the stages that fill before the first.  bf16's are measured on MI355X
+// with W from HBM (1024..28672 rows of W, K 4096 and 14336, 17..4096 tokens);
+// float32's are what its nominal matrix rate gives (4096^3 estimated 898 us
+// takes 1148, 512 x 4096 x 4096 112 and 150).  Small tiles cost little each and
+// keep every CU busy; large ones read less per product.  Estimated and measured
 // (bf16, us, without the launch): 128 x 4096 x 6144 in 2 parts of 128 x 64
 // 23.0 and 21.5, in 4 of 128 x 128 23.1 and 23.4; 1024 x 4096 x 4096 in 2
 // parts of 256 x 128 55 and 48, unsplit 128 x 128 58 and 49; 4096 x 4096 x
@@ -87,8 +88,10 @@ constexpr TileCost kTiles[] = {
     {32, 64, 2, 4, {0.35f, 0.30f}},  {64, 128, 4, 4, {0.85f, 0.55f}},  {128, 64, 4, 4, {0.f, 0.52f}},
     {128, 128, 4, 4, {1.70f, 0.85f}}, {256, 128, 8, 3, {0.f, 0.95f}}, {256, 256, 8, 2, {0.f, 1.50f}}};
 constexpr int kCus = 256;
-// A launch more (the join), and partial sums written and read at about this
-// rate (TB/s = bytes / us / 1e6).
+// A launch more (the join), without what its sums take and what adapters add
+// to it (it measures 4 to 5 us with the sums of 128 x 4096, 15 and 41 with the
+// deltas of 68 adapters of rank 16 and 64 of ranks 8 to 64), and partial sums
+// written and read at about this rate (TB/s = bytes / us / 1e6).
 constexpr float kJoinUs = 2.5f, kPartialBytesPerUs = 3.5e6f;
 // One K tile of a delta (a dependent step of a small batch of work).
 constexpr float kDeltaTileUs = 0.6f;

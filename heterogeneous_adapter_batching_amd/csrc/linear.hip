@@ -446,10 +446,11 @@ __device__ __forceinline__ void delta_of(const DeltaArgs &d, int p0, int f0, int
 // ----------------------------------------------------------------- rows -----
 // One workgroup per 16 outputs (rows of W; with a gated pair 16 of gate and
 // the same 16 of up); wave w takes its share of K for all of them and all of
-// the up to 16 tokens, in batches of F vectors a lane whose loads are in
+// the up to 12 tokens, in batches of F vectors a lane whose loads are in
 // flight while the batch before multiplies.  The waves' sums meet in LDS.
-// Bound by W's bytes: 235 MB of gate and up rows at K 4096 in 46 us (5.1
-// TB/s, as a plain copy's).  KS: K-steps of the delta, 0 without adapters.
+// Bound by W's bytes: 235 MB of gate and up rows at K 4096 in 47.5 us (4.95
+// TB/s; a copy of 1 GiB reads and writes 5.15).  KS: K-steps of the delta, 0
+// without adapters.
 template <typename T, bool GLU, int KS, int NW>
 __global__ __launch_bounds__(NW * kWaveSize, KS > 0 ? 3 : 1) void k_linear_rows(const LinearArgs a) {
     constexpr int E = Elem<T>::E, SPAN = 4 * E, NR = GLU ? 2 : 1, F = 4;
@@ -695,20 +696,25 @@ template <typename T, int HALVES> struct DeltaTiles {
 // spread over all banks (no conflicts counted).
 // What bounds it: prompts the matrix cores, at the clock they leave (1.7 to
 // 1.9 GHz under this load: a 256 x 256 tile keeps them busy two thirds of its
-// cycles; LDS reads and copies fill as many); 4096 x 4096 x 4096 bf16 107 us, 4096
-// tokens through a gated 28672 x 4096 pair 714 us, 1.35 PFLOP/s.  8 waves of
-// 128 x 64 beat 4 of 128 x 128 (713 against 907 us), whose single wave a SIMD
-// has nothing to run at a barrier, and the products spelled out between reads
-// and copies beat the compiler's order (833 against 890).  Decode batches are
-// bound by what enters the CUs: 43 bytes a nanosecond each whatever the tile,
-// 11 TB/s in all, of which x is half where 128 tokens meet 128 rows (128 x
-// 4096 x 14336 33 us in 8 parts of 128 x 128, W at 3.5 TB/s).  K tiles rotated by
-// workgroup or of 256 bytes a row measured the same, dealt in turn to the
-// parts a fifth slower.  ONCE (one token tile: a row of W is one workgroup's)
-// streams W past the L2, which keeps x there and leaves nothing behind for the
-// next product's W to push out: in a loop over changing weights 36.7 us
-// against 41.5 with the join (128 x 4096 x 14336), 124 against 131 (the gated
-// batch of 256 with adapters); where token tiles share W it has to stay.
+// cycles; LDS reads and copies fill as many); 4096 x 4096 x 4096 bf16 107 us
+// in a loop, 120 from cold caches, 4096 tokens through a gated 28672 x 4096
+// pair 714 to 732 us in a loop (1.32 to 1.35 PFLOP/s).  8 waves of 128 x 64
+// beat 4 of 128 x 128 (713 against 907 us), whose single wave a SIMD has
+// nothing to run at a barrier, and the products spelled out between reads and
+// copies beat the compiler's order (833 against 890).
+// Decode batches get W at 3.2 to 3.6 TB/s in the best split of each tile (128
+// x 4096 x 14336 without the join, us: 128 x 128 in 8 parts 32.4, 128 x 64 in 4
+// 32.9, 64 x 128 in 4 34.6, 128 x 256 in 16 36.5), where the rows kernel gets
+// 4.9 from the same matrix.  What holds them there is not found: not HBM, not
+// what enters the CUs (x and W, 4.8 to 10.7 TB/s in these, 13.9 with 128 x 32
+// tiles), not a stage more or less (128 x 64 with 3 instead of 4: 34.0).  K
+// tiles rotated by workgroup or of 256 bytes a row measured the same, dealt in
+// turn to the parts a fifth slower.  ONCE (one token tile: a row of W is one
+// workgroup's) streams W past the L2, which keeps x there and leaves nothing
+// behind for the next product's W to push out: in a loop over changing weights
+// 36.7 us against 41.5 with the join (128 x 4096 x 14336), 124 against 131
+// (the gated batch of 256 with adapters); where token tiles share W it has to
+// stay.
 // W's rows sit in LDS in the order that gives a lane consecutive outputs: LDS
 // row 16 j + r of a wave's share is output (r / 4) 4 G + 4 j + r % 4, G tiles
 // of 16 wide.

@@ -37,7 +37,7 @@ import re
 from collections import defaultdict
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-_SOURCES = ("kernels.hip", "lora_sgmv.cpp", "sgmv_internal.h")
+_SOURCES = ("kernels.hip", "device_ops.h", "lora_sgmv.cpp", "sgmv_internal.h")
 _COPY = re.compile(r"copyBuffer")
 
 
