@@ -450,9 +450,13 @@ __device__ __forceinline__ void delta_of(const DeltaArgs &d, int p0, int f0, int
 // flight while the batch before multiplies.  The waves' sums meet in LDS.
 // Bound by W's bytes: 235 MB of gate and up rows at K 4096 in 47.5 us (4.95
 // TB/s; a copy of 1 GiB reads and writes 5.15).  KS: K-steps of the delta, 0
-// without adapters.
+// without adapters.  The compiler is left to its own count of registers but
+// for the gated bf16 pair with one K-step of delta, one register over what
+// three waves a SIMD have (4 tokens, 4096 x 28672, rank 16: 71.0 us held to
+// them, 72.6 without).
 template <typename T, bool GLU, int KS, int NW>
-__global__ __launch_bounds__(NW * kWaveSize, KS > 0 ? 3 : 1) void k_linear_rows(const LinearArgs a) {
+__global__ __launch_bounds__(NW * kWaveSize, sizeof(T) == 2 && GLU && KS == 1 ? 3 : 1) void
+k_linear_rows(const LinearArgs a) {
     constexpr int E = Elem<T>::E, SPAN = 4 * E, NR = GLU ? 2 : 1, F = 4;
     __shared__ f32x4 red[NW][NR][kWaveSize];
     const int unit = xcd_range_unit(a.units);
