@@ -25,12 +25,18 @@ from .api import (  # noqa: F401
 # there all the same, and their workspace sizes can be asked for).
 _LAYER = ("block_norm", "frozen_linear", "linear_workspace_bytes", "sgmv_linear",
           "sgmv_linear_workspace_bytes")
+# So do the attention's (a batch can be planned without torch).
+_ATTENTION = ("AttentionPlan", "paged_attention", "rotary_append", "rotary_frequencies")
 
 
 def __getattr__(name):
     if name in _LAYER:
         from . import layer
         globals()[name] = getattr(layer, name)
+        return globals()[name]
+    if name in _ATTENTION:
+        from . import attention
+        globals()[name] = getattr(attention, name)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
@@ -40,4 +46,5 @@ __all__ = ["Pool", "Plan", "sgmv_shrink", "sgmv_expand", "sgmv_fused", "sgmv_exp
            "sgmv_expand_partials_sigma", "sgmv_fused_static",
            "pool_bytes_for", "extent_bytes", "pack_adapter", "Cache", "LoraError", "load",
            "plan_opts_default", "debug_checks", "block_norm", "frozen_linear",
-           "linear_workspace_bytes", "sgmv_linear", "sgmv_linear_workspace_bytes"]
+           "linear_workspace_bytes", "sgmv_linear", "sgmv_linear_workspace_bytes", "AttentionPlan",
+           "paged_attention", "rotary_append", "rotary_frequencies"]

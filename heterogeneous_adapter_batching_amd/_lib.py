@@ -57,9 +57,27 @@ class LinearDesc(ctypes.Structure):
                 ("k", ctypes.c_int32), ("act", ctypes.c_int32), ("glu", ctypes.c_int32)]
 
 
+class AttnDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "heads", "kv_heads", "head_dim", "page_size",
+                                              "causal", "window", "max_kv")]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = ([("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] +
+                [(f"{t}_{n}_stride", ctypes.c_int64) for t in "kv" for n in ("page", "head", "token")] +
+                [("num_pages", ctypes.c_int32)])
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
+
+
 _i32, _i64, _u64, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
 _vp, _i32p = ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)
 _pp = ctypes.POINTER(ctypes.c_void_p)
+_f64 = ctypes.c_double
+_kvp = ctypes.POINTER(KvCache)
 
 # name: (restype, argtypes)
 SIGNATURES = {
@@ -133,12 +151,25 @@ SIGNATURES = {
     "sgmv_linear_plan_workspace_bytes": (_u64, [_vp, _vp, ctypes.POINTER(LinearDesc), _i32]),
     "sgmv_linear": (_i32, [_vp, _vp, _i32, _i32, _i32p, _i32p, ctypes.POINTER(LinearDesc), _vp,
                            _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _u64, _vp]),
+    "attn_plan_create": (_i32, [ctypes.POINTER(_vp), ctypes.POINTER(AttnDesc), _i32p, _i32p, _i32]),
+    "attn_plan_rebuild": (_i32, [_vp, _i32p, _i32p, _i32]),
+    "attn_plan_destroy": (_i32, [_vp]),
+    "attn_plan_workspace_bytes": (_u64, [_vp]),
+    "attn_plan_upload": (_i32, [_vp, _vp, _u64, _vp]),
+    "attn_plan_stats": (_i32, [_vp, _i32p, _i32p, _i32p, _i32p]),
+    "paged_attention": (_i32, [_vp, _vp, _i64, _kvp, _vp, _i64, _i32, _f32, _vp, _i64, _vp]),
+    "rotary_frequencies": (_i32, [ctypes.POINTER(_f64), _i32, _f64, _i32, _f64, _f64, _f64, _f64]),
+    "rotary_append": (_i32, [_vp, ctypes.POINTER(RotaryDesc), _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                             _i64, _kvp, _vp, _i64, _i32, _vp, _vp, _vp]),
 }
 
 # lora_norm_kind, lora_gate_act, lora_act
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
+# lora_rotary_layout, lora_rotary_scaling
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
 
 LORA_SIGMA_DIAG, LORA_SIGMA_FULL = 1, 2
 

@@ -1,0 +1,269 @@
+"""The attention between a layer's q/k/v product and its o product over the C
+ABI (argument marshalling only): the plan of a batch over a paged cache, rotary
+positions with the new keys and values into the pages, attention over them."""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import numpy as np
+
+try:
+    import torch
+except ImportError:                    # batches can be planned without it
+    torch = None
+
+from ._lib import (ROTARY_LAYOUTS, ROTARY_SCALINGS, AttnDesc, KvCache, RotaryDesc, check, load)
+from .api import _DTYPES, _i32, _torch_dtype
+from .layer import _code, _enqueue, _matrix, _new
+
+_i32p = ctypes.POINTER(ctypes.c_int32)
+
+
+def _lens(values, name):
+    """Lengths as the library's 32-bit integers, each of them checked."""
+    a = np.asarray(values)
+    if a.ndim != 1 or (a.size and a.dtype.kind not in "iu"):
+        raise ValueError(f"{name} must be a list of integers")
+    if a.size and (int(a.min()) < -(1 << 31) or int(a.max()) >= 1 << 31):
+        raise ValueError(f"{name} does not fit 32 bits")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
+class AttentionPlan:
+    """The plan of one batch's attention over a paged cache (built on the
+    host): new_lens[s] tokens of sequence s, in order, at the end of its
+    kv_lens[s] keys.
+
+    heads query heads share kv_heads key heads; a page holds page_size tokens
+    (a multiple of 16).  causal: a token sees the keys up to its own, the last
+    `window` of them unless that is 0; else all of its sequence's keys (an
+    encoder's states; new_lens and kv_lens are then independent).  max_kv: the
+    most keys of any later rebuild, so that a captured graph may be replayed
+    after rebuild(the same new_lens, other kv_lens).upload(the same ws)."""
+
+    def __init__(self, heads, kv_heads, head_dim, page_size, new_lens, kv_lens, *, dtype="bf16",
+                 causal=True, window=0, max_kv=0):
+        self.lib = load()
+        self._h = ctypes.c_void_p()
+        self.ws = None
+        self.dtype_name = dtype
+        self.heads, self.kv_heads, self.head_dim, self.page_size = heads, kv_heads, head_dim, page_size
+        self.desc = AttnDesc(_DTYPES[dtype], _i32(heads, "heads"), _i32(kv_heads, "kv_heads"),
+                             _i32(head_dim, "head_dim"), _i32(page_size, "page_size"),
+                             int(bool(causal)), _i32(window, "window"), _i32(max_kv, "max_kv"))
+        self._build(lambda *a: self.lib.attn_plan_create(ctypes.byref(self._h),
+                                                         ctypes.byref(self.desc), *a),
+                    new_lens, kv_lens)
+
+    def _build(self, fn, new_lens, kv_lens):
+        new, kv = _lens(new_lens, "new_lens"), _lens(kv_lens, "kv_lens")
+        if new.shape != kv.shape:
+            raise ValueError("new_lens and kv_lens must have one entry per sequence each")
+        check(fn(new.ctypes.data_as(_i32p), kv.ctypes.data_as(_i32p), len(new)))
+        self.num_seqs, self.num_tokens = len(new), int(new.sum())
+
+    def rebuild(self, new_lens, kv_lens):
+        """Re-plan for the next batch in place; upload again before the next
+        call."""
+        self._build(lambda *a: self.lib.attn_plan_rebuild(self._h, *a), new_lens, kv_lens)
+        return self
+
+    def close(self):
+        if getattr(self, "_h", None) and self._h.value:
+            self.lib.attn_plan_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def handle(self):
+        return self._h
+
+    @property
+    def dtype(self):
+        return _torch_dtype(self.dtype_name)
+
+    def workspace_bytes(self) -> int:
+        return int(self.lib.attn_plan_workspace_bytes(self._h))
+
+    def stats(self) -> dict:
+        vals = [ctypes.c_int32() for _ in range(4)]
+        check(self.lib.attn_plan_stats(self._h, *[ctypes.byref(v) for v in vals]))
+        return dict(zip(("tokens", "units", "joins", "max_kv"), [v.value for v in vals]))
+
+    def upload(self, ws=None, stream=None, device="cuda"):
+        """Copy the plan into a device workspace (made on `device` unless
+        given, from the memory of the stream that the copy is queued on)."""
+        if ws is None:
+            device = torch.device(device) if stream is None else stream.device
+            if device.index is None:
+                device = torch.device(device.type, torch.cuda.current_device())
+            ws = _new((self.workspace_bytes(),), torch.uint8, device, stream)
+        elif not ws.is_cuda or not ws.is_contiguous():
+            raise ValueError("ws must be a contiguous CUDA tensor")
+        _enqueue(self.lib.attn_plan_upload, (self._h, ws.data_ptr(), ws.nbytes), ws.device, stream)
+        self.ws = ws
+        return self
+
+
+@functools.lru_cache(maxsize=1024)
+def _rotary_desc(rotary_dim, layout, magnitude):
+    return ctypes.byref(RotaryDesc(_i32(rotary_dim, "rotary_dim"),
+                                   _code(ROTARY_LAYOUTS, layout, "layout"), magnitude))
+
+
+def rotary_frequencies(rotary_dim, *, base=10000.0, scaling="none", factor=1.0, original_length=0,
+                       low=1.0, high=32.0, device=None):
+    """Radians that each of a head's rotary_dim / 2 pairs turns by a position,
+    in 64 bits: base^(-2 i / rotary_dim), or scaled for long contexts.
+    scaling "linear" divides them by factor; "by_parts" leaves pairs that make
+    at least `high` turns in original_length positions, divides those of at
+    most `low`, and blends between them."""
+    f = np.empty(max(_i32(rotary_dim, "rotary_dim"), 2) // 2, np.float64)
+    check(load().rotary_frequencies(
+        f.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), rotary_dim, base,
+        _code(ROTARY_SCALINGS, scaling, "scaling"), factor, original_length, low, high))
+    return torch.from_numpy(f).to(device) if device is not None else torch.from_numpy(f)
+
+
+def _plan_device(plan):
+    if plan.ws is None:
+        return None                          # the library refuses the plan
+    return plan.ws.device
+
+
+def _heads(t, name, plan, heads, device):
+    """A matrix of the plan's tokens (and rows past them)."""
+    p, ld = _matrix(t, name, None, plan.dtype, device)
+    rows, cols = t.shape
+    if cols != heads * plan.head_dim or rows < plan.num_tokens:
+        raise ValueError(f"{name} must be [{plan.num_tokens} or more][{heads * plan.head_dim}], "
+                         f"got {list(t.shape)}")
+    return p, ld
+
+
+def _pages_of(t, name, plan, device):
+    """A cache's pointer and its page, head and token strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != plan.dtype:
+        raise TypeError(f"{name} must be {plan.dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != 4 or t.shape[1:] != (plan.kv_heads, plan.page_size, plan.head_dim):
+        raise ValueError(f"{name} must be [pages][{plan.kv_heads}][{plan.page_size}]"
+                         f"[{plan.head_dim}], got {list(t.shape)}")
+    page, head, tok, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}: a token's elements must be contiguous")
+    return (t.data_ptr(), 0 if t.shape[0] == 1 else page, 0 if plan.kv_heads == 1 else head, tok)
+
+
+def _cache(plan, k_cache, v_cache, pages, device):
+    """The library's arguments of a cache and its page table."""
+    k, v = _pages_of(k_cache, "k_cache", plan, device), _pages_of(v_cache, "v_cache", plan, device)
+    if k_cache.shape[0] != v_cache.shape[0]:
+        raise ValueError("k_cache and v_cache must have the same pages")
+    if not isinstance(pages, torch.Tensor) or not pages.is_cuda or pages.dtype != torch.int32:
+        raise TypeError("pages must be an int32 CUDA tensor")
+    if pages.device != device:
+        raise ValueError(f"pages is on {pages.device}, not on {device}")
+    if pages.dim() != 2 or pages.shape[0] < plan.num_seqs or \
+            (pages.shape[1] > 1 and pages.stride(1) != 1):
+        raise ValueError(f"pages must be [{plan.num_seqs} or more][pages of a sequence] with "
+                         f"contiguous rows, got {list(pages.shape)}")
+    ld = pages.stride(0) if pages.shape[0] > 1 else pages.shape[1]
+    desc = KvCache(k[0], v[0], *k[1:], *v[1:], _i32(k_cache.shape[0], "pages"))
+    return (ctypes.byref(desc), pages.data_ptr(), ld, _i32(pages.shape[1], "pages of a sequence"))
+
+
+def paged_attention(plan, q, k_cache, v_cache, pages, *, scale=None, o=None, stream=None):
+    """Attention of the plan's tokens over their sequences' keys in the cache:
+
+        o = softmax(scale q . k) v
+
+    for every query head, over the keys that the plan lets the token see; zeros
+    where there are none.  q and o are [tokens][heads * head_dim] (q may be a
+    slice of the q/k/v product; rows past the plan's tokens are not looked at
+    and stay as they are), k_cache and v_cache [pages][kv_heads][page_size]
+    [head_dim] with contiguous elements and any strides of multiples of 8,
+    pages int32 [sequences][pages of a sequence].  scale defaults to
+    head_dim^-0.5.  What a token does not see does not reach it, also where it
+    is infinite or NaN; a page outside the cache counts as absent.  Calls that
+    share a plan's workspace must not overlap.  Inference only.  Returns o."""
+    device = _plan_device(plan) or q.device
+    qp, ldq = _heads(q, "q", plan, plan.heads, device)
+    scale = plan.head_dim ** -0.5 if scale is None else float(scale)
+    if o is None:
+        o = _new(q.shape, q.dtype, device, stream)
+        if q.shape[0] > plan.num_tokens:
+            with torch.cuda.stream(stream):
+                o[plan.num_tokens:].zero_()
+    op, ldo = _heads(o, "o", plan, plan.heads, device)
+    _enqueue(plan.lib.paged_attention,
+             (plan.handle, qp, ldq, *_cache(plan, k_cache, v_cache, pages, device), scale, op, ldo),
+             device, stream)
+    return o
+
+
+def rotary_append(plan, q, k, v, k_cache, v_cache, pages, freqs, *, layout="half", magnitude=1.0,
+                  positions=None, q_out=None, stream=None):
+    """Rotary positions on the plan's tokens, and their keys and values into
+    the pages.  With angle a = position * freqs[i], pair (x, y) of a head's
+    first 2 len(freqs) elements becomes
+
+        magnitude * (x cos a - y sin a, y cos a + x sin a).
+
+    layout "half": the pair is elements i and i + len(freqs); "interleaved":
+    2 i and 2 i + 1.  q is returned rotated, in q_out (which may be q) or a new
+    tensor; k goes rotated, and v as it is, to the places of the plan's tokens
+    in the cache.  freqs: float64 on the device (rotary_frequencies), or None
+    to append alone.  positions: int32 [tokens], or None for the tokens' places
+    among their keys.  q may be None (an encoder's keys and values), or k, v,
+    both caches and pages together (queries alone).  Other arguments as
+    paged_attention."""
+    device = _plan_device(plan) or (k if q is None else q).device
+    qp = ldq = op = ldo = kp = ldk = vp = ldv = pp = fp = 0
+    if q is not None:
+        qp, ldq = _heads(q, "q", plan, plan.heads, device)
+        if q_out is None:
+            q_out = _new(q.shape, q.dtype, device, stream)
+            if q.shape[0] > plan.num_tokens:
+                with torch.cuda.stream(stream):
+                    q_out[plan.num_tokens:].zero_()
+        op, ldo = _heads(q_out, "q_out", plan, plan.heads, device)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    absent = [t is None for t in (k, v, k_cache, v_cache, pages)]
+    if all(absent):
+        cache = (None, 0, 0, 0)
+    elif any(absent):
+        raise ValueError("k, v, k_cache, v_cache and pages are given together or not at all")
+    else:
+        kp, ldk = _heads(k, "k", plan, plan.kv_heads, device)
+        vp, ldv = _heads(v, "v", plan, plan.kv_heads, device)
+        cache = _cache(plan, k_cache, v_cache, pages, device)
+    for t, name, dtype, rows in ((positions, "positions", torch.int32, plan.num_tokens),
+                                 (freqs, "freqs", torch.float64, 1)):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+            raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if t.dim() != 1 or t.shape[0] < rows or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous vector of {rows} or more")
+    if positions is not None:
+        pp = positions.data_ptr()
+    n = 0
+    if freqs is not None:
+        fp, n = freqs.data_ptr(), freqs.shape[0]
+    desc = _rotary_desc(2 * n, layout, ctypes.c_float(magnitude).value)
+    _enqueue(plan.lib.rotary_append,
+             (plan.handle, desc, qp, ldq, op, ldo, kp, ldk, vp, ldv, *cache, pp, fp), device, stream)
+    return q_out

@@ -23,7 +23,9 @@ ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, "lora_sgmv.cpp"), os.path.join(CSRC, "exchange.cpp"),
            os.path.join(CSRC, "layer.cpp"), os.path.join(CSRC, "kernels.hip"),
-           os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "linear.hip")]
+           os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "linear.hip"),
+           os.path.join(CSRC, "attend.cpp"), os.path.join(CSRC, "attend.hip"),
+           os.path.join(CSRC, "rotary.hip")]
 
 # Packed float32 ALU ops are switched off for all device code; the compiler's
 # host pass warns that it does not know the feature, which is harmless.
@@ -80,7 +82,8 @@ SANITIZE = ["-fsanitize=address,undefined", "-fno-omit-frame-pointer", "-fno-san
 
 def host_sanitized(out: str) -> str:
     srcs = [os.path.join(CSRC, "lora_sgmv.cpp"), os.path.join(CSRC, "exchange.cpp"),
-            os.path.join(CSRC, "layer.cpp"), os.path.join(CSRC, "host_only.cpp")]
+            os.path.join(CSRC, "layer.cpp"), os.path.join(CSRC, "attend.cpp"),
+            os.path.join(CSRC, "host_only.cpp")]
     cmd = ["g++", "-std=c++17", "-O1", "-g", "-fPIC", "-shared", *SANITIZE,
            "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I", INCLUDE, "-I", CSRC, *srcs,
            "-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib", "-o", out]

@@ -1,0 +1,616 @@
+// Host side of the attention around the products: the plan of a batch's
+// sequences over a paged cache, validation and launches of rotary_append and
+// paged_attention.  Nothing is enqueued unless every argument holds.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <initializer_list>
+#include <iterator>
+#include <memory>
+#include <mutex>
+#include <new>
+#include <unordered_map>
+#include <vector>
+
+#include <hip/hip_runtime.h>
+
+#include "attend_internal.h"
+#include "lora_sgmv.h"
+#include "sgmv_internal.h"
+
+using lora::AttnJoin;
+using lora::AttnToken;
+using lora::AttnUnit;
+using lora::set_errorf;
+
+namespace {
+
+int32_t esize(int32_t dtype) { return dtype == LORA_BF16 ? 2 : 4; }
+bool is_dtype(int32_t d) { return d == LORA_F32 || d == LORA_BF16; }
+uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
+
+constexpr int32_t kMostTokens = 1 << 23, kMostKeys = 1 << 30;
+
+// Units a launch aims for when it cuts the tiles' keys into parts, and the
+// fewest keys of a part.
+constexpr int kRowsUnits = 1024, kRowsKeys = 256;
+
+// One kernel's share of a plan: its tiles of rows, and their keys in parts.
+struct Side {
+    int32_t tile_rows = 0;                 // 0: no sequence is on this side
+    int64_t tiles = 0;                     // tiles of rows, over all key heads
+    std::vector<AttnUnit> units;
+    std::vector<AttnJoin> joins;
+    int64_t cap_units = 0, cap_joins = 0, cap_slots = 0;   // places in the workspace
+    uint64_t off_units = 0, off_joins = 0, off_partial = 0, off_lse = 0;
+};
+
+}  // namespace
+
+struct attn_plan {
+    lora_attn_desc d{};
+    int32_t group = 1;
+    std::vector<int32_t> new_lens, kv_lens;
+    std::vector<AttnToken> tokens;
+    int32_t most_kv = 0;
+    Side rows;
+    uint64_t off_tokens = 0, image_bytes = 0, ws_bytes = 0;
+
+    void *ws = nullptr;
+    // pinned staging, two buffers in turn: an upload waits only for the copy
+    // before last
+    void *staging[2] = {nullptr, nullptr};
+    uint64_t staging_bytes[2] = {0, 0};
+    hipEvent_t staged[2] = {nullptr, nullptr};
+    int32_t next_staging = 0;
+};
+
+namespace {
+
+// Which plan's tables each workspace holds: the last one uploaded into it.
+std::mutex g_mutex;
+std::unordered_map<const void *, const attn_plan *> g_owner;
+
+bool owns_workspace(const attn_plan *pl) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    const auto it = g_owner.find(pl->ws);
+    return it != g_owner.end() && it->second == pl;
+}
+
+lora_status check_attn_desc(const lora_attn_desc *d) {
+    if (!d) return set_errorf(LORA_EINVAL, "null attention descriptor");
+    if (!is_dtype(d->dtype))
+        return set_errorf(LORA_EDTYPE, "dtype %d is neither LORA_F32 nor LORA_BF16", d->dtype);
+    if (d->kv_heads < 1 || d->heads < d->kv_heads || d->heads > LORA_ATTN_MAX_HEADS ||
+        d->heads % d->kv_heads)
+        return set_errorf(LORA_EINVAL, "%d heads over %d key heads: a multiple of them, at most %d",
+                          d->heads, d->kv_heads, LORA_ATTN_MAX_HEADS);
+    if (d->head_dim < 8 || d->head_dim % 8 || d->head_dim > LORA_ATTN_MAX_HEAD_DIM)
+        return set_errorf(LORA_EINVAL, "head_dim %d is not a multiple of 8 in 8..%d", d->head_dim,
+                          LORA_ATTN_MAX_HEAD_DIM);
+    if (d->page_size < lora::kAttnPage || d->page_size % lora::kAttnPage ||
+        d->page_size > LORA_ATTN_MAX_PAGE)
+        return set_errorf(LORA_EINVAL, "page_size %d is not a multiple of %d in %d..%d",
+                          d->page_size, lora::kAttnPage, lora::kAttnPage, LORA_ATTN_MAX_PAGE);
+    if (d->causal != 0 && d->causal != 1)
+        return set_errorf(LORA_EINVAL, "causal %d is neither 0 nor 1", d->causal);
+    if (d->window < 0 || (d->window && !d->causal))
+        return set_errorf(LORA_EINVAL, "window %d: 0 or, with causal, a number of keys", d->window);
+    if (d->max_kv < 0 || d->max_kv > kMostKeys)
+        return set_errorf(LORA_EINVAL, "max_kv %d not in 0..%d", d->max_kv, kMostKeys);
+    return LORA_OK;
+}
+
+lora_status check_lens(const lora_attn_desc &d, const int32_t *new_lens, const int32_t *kv_lens,
+                       int32_t S) {
+    if (S < 0 || S > kMostTokens)
+        return set_errorf(LORA_EINVAL, "num_seqs %d not in 0..%d", S, kMostTokens);
+    if (S && (!new_lens || !kv_lens)) return set_errorf(LORA_EINVAL, "null table of lengths");
+    int64_t tokens = 0, tiles = 0;
+    for (int32_t s = 0; s < S; ++s) {
+        if (new_lens[s] < 0 || new_lens[s] > kMostTokens)
+            return set_errorf(LORA_EINVAL, "sequence %d: %d new tokens", s, new_lens[s]);
+        if (kv_lens[s] < 0 || kv_lens[s] > kMostKeys)
+            return set_errorf(LORA_EINVAL, "sequence %d: %d keys not in 0..%d", s, kv_lens[s],
+                              kMostKeys);
+        if (d.causal && kv_lens[s] < new_lens[s])
+            return set_errorf(LORA_EINVAL, "sequence %d: %d keys are fewer than its %d new tokens",
+                              s, kv_lens[s], new_lens[s]);
+        if (d.max_kv && kv_lens[s] > d.max_kv)
+            return set_errorf(LORA_EINVAL, "sequence %d: %d keys are more than the plan's max_kv %d",
+                              s, kv_lens[s], d.max_kv);
+        tokens += new_lens[s];
+        tiles += (int64_t(new_lens[s]) * (d.heads / d.kv_heads) + 15) / 16 * d.kv_heads;
+    }
+    if (tokens > kMostTokens || tiles > kMostTokens)
+        return set_errorf(LORA_EINVAL, "a batch of %lld tokens (%lld tiles of 16 rows) is too large: "
+                          "at most %d", (long long)tokens, (long long)tiles, kMostTokens);
+    return LORA_OK;
+}
+
+// The keys that rows row0 .. row1 - 1 see between them, from a whole block on.
+void tile_keys(const attn_plan &p, int32_t s, int64_t row0, int64_t row1, int32_t *lo, int32_t *hi) {
+    const int32_t kv = p.kv_lens[s], pos0 = kv - p.new_lens[s];
+    *lo = 0;
+    *hi = kv;
+    if (!p.d.causal) return;
+    *hi = std::min(kv, pos0 + int32_t((row1 - 1) / p.group) + 1);
+    if (p.d.window) {
+        const int32_t first = pos0 + int32_t(row0 / p.group) - p.d.window + 1;
+        *lo = std::max(first, 0) / lora::kAttnBlock * lora::kAttnBlock;
+    }
+}
+
+int64_t blocks_of(int32_t lo, int32_t hi) {
+    return hi > lo ? (int64_t(hi) - lo + lora::kAttnBlock - 1) / lora::kAttnBlock : 0;
+}
+
+// Cuts every tile's keys into parts, so that the launch has about `target`
+// units, none shorter than `least` keys, and lays them out one after another.
+// The cut is even: no more parts than tiles + target in all.
+void cut(const attn_plan &p, Side *side, int64_t target, int64_t least) {
+    side->units.clear();
+    side->joins.clear();
+    const int32_t S = int32_t(p.new_lens.size());
+    int64_t total = 0;
+    for (int32_t s = 0; s < S; ++s) {
+        const int64_t rows = int64_t(p.new_lens[s]) * p.group;
+        for (int64_t r = 0; r < rows; r += side->tile_rows) {
+            int32_t lo, hi;
+            tile_keys(p, s, r, std::min<int64_t>(rows, r + side->tile_rows), &lo, &hi);
+            total += blocks_of(lo, hi) * p.d.kv_heads;
+        }
+    }
+    const int64_t part = std::max(least / lora::kAttnBlock, (total + target - 1) / target);
+    int32_t tok0 = 0, slot = 0;
+    for (int32_t s = 0; s < S; ++s) {
+        const int64_t rows = int64_t(p.new_lens[s]) * p.group;
+        for (int64_t r = 0; r < rows; r += side->tile_rows) {
+            int32_t lo, hi;
+            tile_keys(p, s, r, std::min<int64_t>(rows, r + side->tile_rows), &lo, &hi);
+            const int64_t blocks = blocks_of(lo, hi);
+            const int64_t parts = std::max<int64_t>(1, (blocks + part - 1) / part);
+            for (int32_t h = 0; h < p.d.kv_heads; ++h) {
+                if (parts > 1)
+                    side->joins.push_back({tok0, h, int32_t(r), int32_t(rows), slot, int32_t(parts)});
+                for (int64_t i = 0; i < parts; ++i) {
+                    const int64_t k0 = lo + blocks * i / parts * lora::kAttnBlock;
+                    const int64_t k1 = lo + blocks * (i + 1) / parts * lora::kAttnBlock;
+                    side->units.push_back({s, h, int32_t(r), int32_t(rows), tok0,
+                                           p.kv_lens[s] - p.new_lens[s], int32_t(k0),
+                                           int32_t(std::min<int64_t>(k1, hi)),
+                                           parts > 1 ? slot++ : -1});
+                }
+            }
+        }
+        tok0 += p.new_lens[s];
+    }
+    side->cap_units = int64_t(side->units.size());
+    side->cap_joins = int64_t(side->joins.size());
+    side->cap_slots = slot;
+    if (p.d.max_kv) {
+        // room for any lengths up to max_kv, so that the launches stay the same
+        const int64_t most = (int64_t(p.d.max_kv) + lora::kAttnBlock - 1) / lora::kAttnBlock;
+        const int64_t low = least / lora::kAttnBlock, each = std::max<int64_t>(1, (most + low - 1) / low);
+        side->cap_units = std::min(side->tiles * each, side->tiles + target);
+        side->cap_joins = each > 1 ? side->tiles : 0;
+        side->cap_slots = each > 1 ? side->cap_units : 0;
+    }
+}
+
+void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, int32_t S) {
+    p->new_lens.assign(new_lens, new_lens + S);
+    p->kv_lens.assign(kv_lens, kv_lens + S);
+    p->tokens.clear();
+    p->most_kv = 0;
+    int64_t most_rows = 0;
+    for (int32_t s = 0; s < S; ++s) {
+        p->most_kv = std::max(p->most_kv, kv_lens[s]);
+        most_rows = std::max(most_rows, int64_t(new_lens[s]) * p->group);
+        for (int32_t i = 0; i < new_lens[s]; ++i)
+            p->tokens.push_back({s, kv_lens[s] - new_lens[s] + i});
+    }
+    Side &side = p->rows;
+    side = Side{};
+    side.tile_rows = most_rows <= 16 ? 16 : most_rows <= 32 ? 32 : 16 * lora::attn_rows_tiles(p->d.head_dim);
+    for (int32_t s = 0; s < S; ++s)
+        side.tiles += (int64_t(new_lens[s]) * p->group + side.tile_rows - 1) / side.tile_rows *
+                      p->d.kv_heads;
+    cut(*p, &side, kRowsUnits, kRowsKeys);
+
+    uint64_t at = 0;
+    auto place = [&](uint64_t bytes) {
+        const uint64_t off = at;
+        at += round_up(bytes, 256);
+        return off;
+    };
+    p->off_tokens = place(sizeof(AttnToken) * p->tokens.size());
+    side.off_units = place(sizeof(AttnUnit) * uint64_t(side.cap_units));
+    side.off_joins = place(sizeof(AttnJoin) * uint64_t(side.cap_joins));
+    p->image_bytes = at;
+    const uint64_t rows = uint64_t(side.cap_slots) * uint64_t(side.tile_rows);
+    side.off_partial = place(rows * 4 * uint64_t(lora::attn_dim(p->d.head_dim)));
+    side.off_lse = place(rows * 4);
+    p->ws_bytes = at;
+}
+
+bool aligned(const void *ptr, int64_t bytes) {
+    return reinterpret_cast<uintptr_t>(ptr) % uint64_t(bytes) == 0;
+}
+
+struct Rows {
+    const char *name;
+    const void *ptr;
+    int64_t ld, width;
+};
+// A matrix of whole 16-byte vectors.
+lora_status check_rows(const Rows &r, int32_t es) {
+    if (!r.ptr || !aligned(r.ptr, 16))
+        return set_errorf(LORA_EINVAL, "%s must be non-null and 16-byte aligned", r.name);
+    if (r.ld < r.width || r.ld % 8 || r.ld > (int64_t(1) << 40))
+        return set_errorf(LORA_EINVAL, "ld of %s (%lld) is not a multiple of 8 from its width %lld",
+                          r.name, (long long)r.ld, (long long)r.width);
+    return LORA_OK;
+}
+// Whether two matrices of T rows reach into each other: column slices of the
+// same rows do not.
+bool overlap(const Rows &a, const Rows &b, int64_t T, int32_t es) {
+    if (!a.ptr || !b.ptr || T <= 0) return false;
+    const uint64_t alo = reinterpret_cast<uintptr_t>(a.ptr), blo = reinterpret_cast<uintptr_t>(b.ptr);
+    const uint64_t ahi = alo + uint64_t((T - 1) * a.ld + a.width) * es;
+    const uint64_t bhi = blo + uint64_t((T - 1) * b.ld + b.width) * es;
+    if (ahi <= blo || bhi <= alo) return false;
+    if (T > 1 && a.ld == b.ld) {
+        const uint64_t l = uint64_t(a.ld) * es;
+        const uint64_t at = blo >= alo ? (blo - alo) % l : (l - (alo - blo) % l) % l;
+        if (at >= uint64_t(a.width) * es && at + uint64_t(b.width) * es <= l) return false;
+    }
+    return true;
+}
+
+// The cache and its page table; and whether the tensors beside them (T rows
+// each) lie apart from it.
+lora_status check_cache(const attn_plan &p, const lora_kv_cache *c, const int32_t *pages,
+                        int64_t ld_pages, int32_t pages_per_seq, std::initializer_list<Rows> beside) {
+    if (!c) return set_errorf(LORA_EINVAL, "null cache");
+    const int32_t es = esize(p.d.dtype);
+    if (c->num_pages < 1) return set_errorf(LORA_EINVAL, "a cache of %d pages", c->num_pages);
+    const struct {
+        const char *name;
+        const void *ptr;
+        int64_t page, head, tok;
+    } side[2] = {{"k_cache", c->k, c->k_page_stride, c->k_head_stride, c->k_token_stride},
+                 {"v_cache", c->v, c->v_page_stride, c->v_head_stride, c->v_token_stride}};
+    for (const auto &t : side) {
+        if (!t.ptr || !aligned(t.ptr, 16))
+            return set_errorf(LORA_EINVAL, "%s must be non-null and 16-byte aligned", t.name);
+        for (int64_t st : {t.page, t.head, t.tok})
+            if (st < 0 || st % 8 || st > (int64_t(1) << 40))
+                return set_errorf(LORA_EINVAL, "a stride of %s (%lld) is no multiple of 8 in 0..2^40",
+                                  t.name, (long long)st);
+        if (t.tok < p.d.head_dim || t.tok * es * 16 >= (int64_t(1) << 31))
+            return set_errorf(LORA_EINVAL, "%s: tokens %lld elements apart, heads of %d", t.name,
+                              (long long)t.tok, p.d.head_dim);
+        const uint64_t lo = reinterpret_cast<uintptr_t>(t.ptr);
+        const uint64_t hi = lo + uint64_t((c->num_pages - 1) * t.page + (p.d.kv_heads - 1) * t.head +
+                                          (p.d.page_size - 1) * t.tok + p.d.head_dim) * es;
+        for (const Rows &r : beside) {
+            const uint64_t at = reinterpret_cast<uintptr_t>(r.ptr);
+            const uint64_t end = at + uint64_t((int64_t(p.tokens.size()) - 1) * r.ld + r.width) * es;
+            if (r.ptr && at < hi && lo < end)
+                return set_errorf(LORA_EINVAL, "%s overlaps %s", r.name, t.name);
+        }
+    }
+    if (!pages || !aligned(pages, 4))
+        return set_errorf(LORA_EINVAL, "the page table must be non-null and 4-byte aligned");
+    if (ld_pages < pages_per_seq || ld_pages > (int64_t(1) << 40))
+        return set_errorf(LORA_EINVAL, "ld of the page table (%lld) is less than its %d pages",
+                          (long long)ld_pages, pages_per_seq);
+    if (int64_t(pages_per_seq) * p.d.page_size < p.most_kv)
+        return set_errorf(LORA_EINVAL, "%d pages of %d a sequence do not hold %d keys",
+                          pages_per_seq, p.d.page_size, p.most_kv);
+    return LORA_OK;
+}
+
+lora_status check_uploaded(const attn_plan *p) {
+    if (!p->ws) return set_errorf(LORA_ESTATE, "plan has not been uploaded");
+    if (!owns_workspace(p))
+        return set_errorf(LORA_ESTATE, "the plan's workspace holds another plan's tables since "
+                          "(upload this plan again)");
+    return LORA_OK;
+}
+
+lora::CacheArgs cache_args(const attn_plan &p, const lora_kv_cache &c) {
+    lora::CacheArgs a{};
+    a.k = static_cast<uint8_t *>(c.k);
+    a.v = static_cast<uint8_t *>(c.v);
+    a.k_page = c.k_page_stride;
+    a.k_head = c.k_head_stride;
+    a.k_tok = c.k_token_stride;
+    a.v_page = c.v_page_stride;
+    a.v_head = c.v_head_stride;
+    a.v_tok = c.v_token_stride;
+    a.num_pages = c.num_pages;
+    a.page_size = p.d.page_size;
+    return a;
+}
+
+// A C entry ends with a status whatever happens below it.
+template <typename Fn> lora_status guarded(Fn fn) {
+    try {
+        return fn();
+    } catch (const std::bad_alloc &) {
+        return set_errorf(LORA_ENOSPC, "out of host memory");
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+lora_status attn_plan_create(attn_plan **out, const lora_attn_desc *d, const int32_t *new_lens,
+                             const int32_t *kv_lens, int32_t num_seqs) {
+    if (!out) return set_errorf(LORA_EINVAL, "null output pointer");
+    lora_status st = check_attn_desc(d);
+    if (st != LORA_OK) return st;
+    if ((st = check_lens(*d, new_lens, kv_lens, num_seqs)) != LORA_OK) return st;
+    return guarded([&] {
+        std::unique_ptr<attn_plan> p(new attn_plan());
+        p->d = *d;
+        p->group = d->heads / d->kv_heads;
+        plan_build(p.get(), new_lens, kv_lens, num_seqs);
+        *out = p.release();
+        return LORA_OK;
+    });
+}
+
+lora_status attn_plan_rebuild(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens,
+                              int32_t num_seqs) {
+    if (!p) return set_errorf(LORA_EINVAL, "null plan");
+    const lora_status st = check_lens(p->d, new_lens, kv_lens, num_seqs);
+    if (st != LORA_OK) return st;
+    return guarded([&] {
+        plan_build(p, new_lens, kv_lens, num_seqs);
+        p->ws = nullptr;                   // its tables are the last batch's
+        return LORA_OK;
+    });
+}
+
+lora_status attn_plan_destroy(attn_plan *p) {
+    if (!p) return LORA_OK;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        for (auto it = g_owner.begin(); it != g_owner.end();)
+            it = it->second == p ? g_owner.erase(it) : std::next(it);
+    }
+    for (int i = 0; i < 2; ++i) {
+        // (a copy out of the buffer may still be queued)
+        if (p->staged[i]) {
+            (void)hipEventSynchronize(p->staged[i]);
+            (void)hipEventDestroy(p->staged[i]);
+        }
+        if (p->staging[i]) (void)hipHostFree(p->staging[i]);
+    }
+    delete p;
+    return LORA_OK;
+}
+
+uint64_t attn_plan_workspace_bytes(const attn_plan *p) {
+    return p ? std::max<uint64_t>(p->ws_bytes, 256) : 0;
+}
+
+lora_status attn_plan_stats(const attn_plan *p, int32_t *num_tokens, int32_t *num_units,
+                            int32_t *num_joins, int32_t *max_kv) {
+    if (!p) return set_errorf(LORA_EINVAL, "null plan");
+    if (num_tokens) *num_tokens = int32_t(p->tokens.size());
+    if (num_units) *num_units = int32_t(p->rows.units.size());
+    if (num_joins) *num_joins = int32_t(p->rows.joins.size());
+    if (max_kv) *max_kv = p->most_kv;
+    return LORA_OK;
+}
+
+lora_status attn_plan_upload(attn_plan *p, void *ws, uint64_t ws_bytes, void *stream) {
+    if (!p) return set_errorf(LORA_EINVAL, "null plan");
+    if (!ws || !aligned(ws, 256))
+        return set_errorf(LORA_EINVAL, "workspace must be a non-null, 256-byte aligned device pointer");
+    if (ws_bytes < attn_plan_workspace_bytes(p))
+        return set_errorf(LORA_ESTATE, "workspace of %llu bytes < %llu needed",
+                          (unsigned long long)ws_bytes,
+                          (unsigned long long)attn_plan_workspace_bytes(p));
+    return guarded([&] {
+        const int32_t k = p->next_staging;
+        hipError_t e = p->staged[k] ? hipEventSynchronize(p->staged[k])
+                                    : hipEventCreateWithFlags(&p->staged[k], hipEventDisableTiming);
+        if (e != hipSuccess)
+            return set_errorf(LORA_EHIP, "plan staging event: %s", hipGetErrorString(e));
+        const uint64_t bytes = std::max<uint64_t>(p->image_bytes, 256);
+        if (p->staging_bytes[k] < bytes) {
+            const uint64_t want = std::max(bytes, p->staging_bytes[k] * 3 / 2);
+            void *buf = nullptr;
+            e = hipHostMalloc(&buf, want, hipHostMallocDefault);
+            if (e != hipSuccess)
+                return set_errorf(LORA_EHIP, "plan staging buffer: %s", hipGetErrorString(e));
+            if (p->staging[k]) (void)hipHostFree(p->staging[k]);
+            p->staging[k] = buf;
+            p->staging_bytes[k] = want;
+        }
+        uint8_t *img = static_cast<uint8_t *>(p->staging[k]);
+        auto put = [&](uint64_t off, const auto &table) {
+            if (!table.empty()) std::memcpy(img + off, table.data(), sizeof(table[0]) * table.size());
+        };
+        put(p->off_tokens, p->tokens);
+        put(p->rows.off_units, p->rows.units);
+        put(p->rows.off_joins, p->rows.joins);
+        // places without work: no sequence, no parts
+        AttnUnit *u = reinterpret_cast<AttnUnit *>(img + p->rows.off_units);
+        for (int64_t i = int64_t(p->rows.units.size()); i < p->rows.cap_units; ++i)
+            u[i] = AttnUnit{-1, 0, 0, 0, 0, 0, 0, 0, -1};
+        AttnJoin *j = reinterpret_cast<AttnJoin *>(img + p->rows.off_joins);
+        for (int64_t i = int64_t(p->rows.joins.size()); i < p->rows.cap_joins; ++i) j[i] = AttnJoin{};
+        hipStream_t s = static_cast<hipStream_t>(stream);
+        e = hipMemcpyAsync(ws, img, p->image_bytes, hipMemcpyHostToDevice, s);
+        if (e == hipSuccess) e = hipEventRecord(p->staged[k], s);
+        if (e != hipSuccess) return set_errorf(LORA_EHIP, "plan upload: %s", hipGetErrorString(e));
+        p->next_staging = 1 - k;
+        p->ws = ws;
+        std::lock_guard<std::mutex> lock(g_mutex);
+        g_owner[ws] = p;
+        return LORA_OK;
+    });
+}
+
+lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
+                            const lora_kv_cache *cache, const int32_t *pages, int64_t ld_pages,
+                            int32_t pages_per_seq, float scale, void *o, int64_t ldo,
+                            void *stream) {
+    if (!p) return set_errorf(LORA_EINVAL, "null plan");
+    lora_status st;
+    if (!std::isfinite(scale)) return set_errorf(LORA_EINVAL, "scale must be finite");
+    const int64_t T = int64_t(p->tokens.size()), width = int64_t(p->d.heads) * p->d.head_dim;
+    if (T == 0) return LORA_OK;            // empty batch: no tensor is looked at
+    const int32_t es = esize(p->d.dtype);
+    const Rows rq{"q", q, ldq, width}, ro{"o", o, ldo, width};
+    for (const Rows *r : {&rq, &ro})
+        if ((st = check_rows(*r, es)) != LORA_OK) return st;
+    if (overlap(rq, ro, T, es)) return set_errorf(LORA_EINVAL, "o overlaps q");
+    if ((st = check_cache(*p, cache, pages, ld_pages, pages_per_seq, {ro})) != LORA_OK)
+        return st;
+    if ((st = check_uploaded(p)) != LORA_OK) return st;
+
+    uint8_t *ws = static_cast<uint8_t *>(p->ws);
+    lora::AttnArgs a{};
+    a.cache = cache_args(*p, *cache);
+    a.q = static_cast<const uint8_t *>(q);
+    a.o = static_cast<uint8_t *>(o);
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.pages = pages;
+    a.ld_pages = ld_pages;
+    a.group = p->group;
+    a.head_dim = p->d.head_dim;
+    a.causal = p->d.causal;
+    a.window = p->d.window;
+    a.scale2 = scale * 1.44269504088896340736f;
+    const Side &side = p->rows;
+    a.units = reinterpret_cast<const AttnUnit *>(ws + side.off_units);
+    a.joins = reinterpret_cast<const AttnJoin *>(ws + side.off_joins);
+    a.partial = reinterpret_cast<float *>(ws + side.off_partial);
+    a.lse = reinterpret_cast<float *>(ws + side.off_lse);
+    a.num_units = int32_t(side.cap_units);
+    a.num_joins = int32_t(side.cap_joins);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = lora::launch_attn_rows(p->d.dtype, side.tile_rows / 16, a, s);
+    if (e == hipSuccess) e = lora::launch_attn_join(p->d.dtype, side.tile_rows, a, s);
+    if (e != hipSuccess)
+        return set_errorf(LORA_EHIP, "attention launch: %s", hipGetErrorString(e));
+    return LORA_OK;
+}
+
+lora_status rotary_frequencies(double *out, int32_t rotary_dim, double base, int32_t scaling,
+                               double factor, double original_length, double low, double high) {
+    if (!out) return set_errorf(LORA_EINVAL, "null output pointer");
+    if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > LORA_ATTN_MAX_HEAD_DIM)
+        return set_errorf(LORA_EINVAL, "rotary_dim %d is not even in 2..%d", rotary_dim,
+                          LORA_ATTN_MAX_HEAD_DIM);
+    if (!(base > 0) || !std::isfinite(base))
+        return set_errorf(LORA_EINVAL, "base must be positive and finite");
+    if (scaling < LORA_ROTARY_UNSCALED || scaling > LORA_ROTARY_BY_PARTS)
+        return set_errorf(LORA_EINVAL, "scaling %d is not a lora_rotary_scaling", scaling);
+    if (scaling != LORA_ROTARY_UNSCALED && (!(factor > 0) || !std::isfinite(factor)))
+        return set_errorf(LORA_EINVAL, "factor must be positive and finite");
+    if (scaling == LORA_ROTARY_BY_PARTS &&
+        (!(original_length > 0) || !std::isfinite(original_length) || !std::isfinite(low) ||
+         !std::isfinite(high) || !(high > low)))
+        return set_errorf(LORA_EINVAL, "by parts: original_length must be positive, low less than high");
+    for (int32_t i = 0; i < rotary_dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rotary_dim);
+        double keep = scaling == LORA_ROTARY_UNSCALED ? 1.0 : 0.0;
+        if (scaling == LORA_ROTARY_BY_PARTS) {
+            const double turns = f * original_length / 6.283185307179586477;
+            keep = std::min(std::max((turns - low) / (high - low), 0.0), 1.0);
+        }
+        out[i] = scaling == LORA_ROTARY_UNSCALED ? f : f * keep + f / factor * (1.0 - keep);
+    }
+    return LORA_OK;
+}
+
+lora_status rotary_append(const attn_plan *p, const lora_rotary_desc *r, const void *q, int64_t ldq,
+                          void *q_out, int64_t ldqo, const void *k, int64_t ldk, const void *v,
+                          int64_t ldv, const lora_kv_cache *cache, const int32_t *pages,
+                          int64_t ld_pages, int32_t pages_per_seq, const int32_t *positions,
+                          const double *freqs, void *stream) {
+    if (!p) return set_errorf(LORA_EINVAL, "null plan");
+    lora_status st;
+    if (!r) return set_errorf(LORA_EINVAL, "null rotary descriptor");
+    if (r->layout != LORA_ROTARY_HALF && r->layout != LORA_ROTARY_INTERLEAVED)
+        return set_errorf(LORA_EINVAL, "layout %d is not a lora_rotary_layout", r->layout);
+    if (freqs && (r->rotary_dim < 2 || r->rotary_dim % 2 || r->rotary_dim > p->d.head_dim))
+        return set_errorf(LORA_EINVAL, "rotary_dim %d is not even in 2..%d", r->rotary_dim,
+                          p->d.head_dim);
+    if (!std::isfinite(r->magnitude)) return set_errorf(LORA_EINVAL, "magnitude must be finite");
+    if (!freqs && (r->rotary_dim || positions))
+        return set_errorf(LORA_EINVAL, "a rotary_dim or positions without frequencies");
+    if (!p->d.causal && cache)
+        for (size_t s = 0; s < p->kv_lens.size(); ++s)
+            if (p->kv_lens[s] < p->new_lens[s])
+                return set_errorf(LORA_EINVAL, "sequence %d: %d keys are fewer than its %d new tokens",
+                                  int(s), p->kv_lens[s], p->new_lens[s]);
+    if (!q && !cache) return set_errorf(LORA_EINVAL, "neither queries nor a cache");
+    const int64_t T = int64_t(p->tokens.size());
+    if (T == 0) return LORA_OK;            // empty batch: no tensor is looked at
+    const int32_t es = esize(p->d.dtype), D = p->d.head_dim;
+    const int64_t wq = int64_t(p->d.heads) * D, wk = int64_t(p->d.kv_heads) * D;
+    const Rows rq{"q", q, ldq, wq}, ro{"q_out", q_out, ldqo, wq}, rk{"k", k, ldk, wk},
+        rv{"v", v, ldv, wk};
+    if (q) {
+        for (const Rows *x : {&rq, &ro})
+            if ((st = check_rows(*x, es)) != LORA_OK) return st;
+        if (overlap(rq, ro, T, es) && !(q == q_out && (ldq == ldqo || T == 1)))
+            return set_errorf(LORA_EINVAL, "q_out overlaps q without being it");
+    } else if (q_out) {
+        return set_errorf(LORA_EINVAL, "q_out without q");
+    }
+    if (cache) {
+        for (const Rows *x : {&rk, &rv}) {
+            if ((st = check_rows(*x, es)) != LORA_OK) return st;
+            if (q && overlap(ro, *x, T, es)) return set_errorf(LORA_EINVAL, "q_out overlaps %s", x->name);
+        }
+        if ((st = check_cache(*p, cache, pages, ld_pages, pages_per_seq, {ro, rk, rv})) != LORA_OK)
+            return st;
+    } else if (k || v) {
+        return set_errorf(LORA_EINVAL, "keys or values without a cache");
+    }
+    if (positions && !aligned(positions, 4))
+        return set_errorf(LORA_EINVAL, "positions must be 4-byte aligned");
+    if (freqs && !aligned(freqs, 8)) return set_errorf(LORA_EINVAL, "freqs must be 8-byte aligned");
+    if ((st = check_uploaded(p)) != LORA_OK) return st;
+
+    lora::RotaryArgs a{};
+    if (cache) a.cache = cache_args(*p, *cache);
+    a.q = static_cast<const uint8_t *>(q);
+    a.k = static_cast<const uint8_t *>(k);
+    a.v = static_cast<const uint8_t *>(v);
+    a.q_out = static_cast<uint8_t *>(q_out);
+    a.ldq = ldq;
+    a.ldqo = ldqo;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.pages = pages;
+    a.ld_pages = ld_pages;
+    a.tokens = reinterpret_cast<const AttnToken *>(static_cast<uint8_t *>(p->ws) + p->off_tokens);
+    a.positions = positions;
+    a.freqs = freqs;
+    a.T = int32_t(T);
+    a.heads = p->d.heads;
+    a.kv_heads = p->d.kv_heads;
+    a.head_dim = D;
+    a.rotary_dim = freqs ? r->rotary_dim : 0;
+    a.layout = r->layout;
+    a.magnitude = r->magnitude;
+    const hipError_t e = lora::launch_rotary(p->d.dtype, a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return set_errorf(LORA_EHIP, "rotary launch: %s", hipGetErrorString(e));
+    return LORA_OK;
+}
+
+}  // extern "C"

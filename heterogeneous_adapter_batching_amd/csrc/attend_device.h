@@ -1,0 +1,80 @@
+// Device building blocks of the attention kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "attend_internal.h"
+#include "device_ops.h"
+
+namespace lora {
+namespace {
+
+constexpr float kNone = -__builtin_inff();   // the score of a key that a row does not see
+
+// fn over both halves of the wave's rows of 16 lanes: lanes l, l ^ 16, l ^ 32
+// and l ^ 48 end with the same value.
+template <typename Fn> __device__ __forceinline__ float over_groups(float v, Fn fn) {
+    auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fn(__uint_as_float(h[0]), __uint_as_float(h[1]));
+    h = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fn(__uint_as_float(h[0]), __uint_as_float(h[1]));
+}
+__device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float sum_of(float a, float b) { return a + b; }
+
+__device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// A maximum to subtract: a row that has seen no key yet subtracts nothing from
+// its scores, which are -inf.
+__device__ __forceinline__ float finite_max(float m) { return m == kNone ? 0.f : m; }
+
+// The parts of a word, two bf16 or a float32, that are not finite.
+template <typename T> __device__ __forceinline__ uint32_t odd_mask(uint32_t w);
+template <> __device__ __forceinline__ uint32_t odd_mask<uint16_t>(uint32_t w) {
+    return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
+           ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+template <> __device__ __forceinline__ uint32_t odd_mask<float>(uint32_t w) {
+    return (w & 0x7f800000u) == 0x7f800000u ? ~0u : 0u;
+}
+
+// A sequence's row of the page table, walked in tiles of 16 keys, each in one
+// page: the tile's rows of the cache as a buffer (of no bytes for a page
+// outside the cache, whose keys count as absent).
+struct PageWalk {
+    const int32_t *row;
+    int32_t page, slot, page_size;           // of the next tile
+    __device__ __forceinline__ PageWalk(const AttnArgs &a, int seq, int key)
+        : row(a.pages + int64_t(seq) * a.ld_pages), page(key / a.cache.page_size),
+          slot(key % a.cache.page_size), page_size(a.cache.page_size) {}
+    __device__ __forceinline__ void skip(int keys) {
+        slot += keys;
+        while (slot >= page_size) {
+            slot -= page_size;
+            ++page;
+        }
+    }
+};
+
+// N consecutive outputs (N 4, 8 or 16) of one row.
+template <int N> __device__ __forceinline__ void store_row(uint16_t *p, const float (&v)[N]) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = bf16x2_rne(v[2 * i], v[2 * i + 1]);
+    if constexpr (N == 4) {
+        *reinterpret_cast<u32x2 *>(p) = u32x2{w[0], w[1]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i)
+            reinterpret_cast<u32x4 *>(p)[i] =
+                u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+    }
+}
+template <int N> __device__ __forceinline__ void store_row(float *p, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+        reinterpret_cast<f32x4 *>(p)[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+}
+
+}  // namespace
+}  // namespace lora

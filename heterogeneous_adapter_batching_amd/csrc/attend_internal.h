@@ -1,0 +1,88 @@
+// Internal interface of the attention around the products (rotary positions
+// into a paged cache, attention over it): descriptors, argument blocks and
+// kernel launchers.  The public interface is include/lora_sgmv.h.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+#include "lora_sgmv.h"
+
+namespace lora {
+
+// A sequence's new tokens and the query heads of one key head make the rows of
+// its products with that head's keys: row r is token r / group, head r % group.
+// They are cut into tiles of rows, a tile's keys into parts (units): one
+// workgroup each.
+struct AttnUnit {
+    int32_t seq;                 // row of the page table; -1: no work
+    int32_t kv_head;
+    int32_t row0, rows;          // the tile's first row, and the rows of the sequence
+    int32_t tok0;                // the sequence's first token in the batch
+    int32_t pos0;                // and its position: kv_len - new tokens
+    int32_t key0, key1;          // the unit's keys; key0 a multiple of kAttnBlock
+    int32_t slot;                // its partial sums, or -1: it has all of the tile's keys
+};
+static_assert(sizeof(AttnUnit) == 36, "whole dwords");
+// A tile in several parts, for the launch that joins them (no parts: none).
+struct AttnJoin {
+    int32_t tok0, kv_head, row0, rows, slot0, slots;
+};
+static_assert(sizeof(AttnJoin) == 24, "whole dwords");
+struct AttnToken {
+    int32_t seq, pos;            // pos: of the token's key in the cache
+};
+
+constexpr int kAttnPage = 16;    // pages hold a multiple of this many tokens
+constexpr int kAttnBlock = 64;   // unit boundaries are multiples of this many keys
+
+// One head's rows of the cache, in elements.
+struct CacheArgs {
+    uint8_t *k, *v;
+    int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;
+    int32_t num_pages, page_size;
+};
+
+struct AttnArgs {
+    CacheArgs cache;
+    const uint8_t *q;            // [T][ldq]
+    uint8_t *o;                  // [T][ldo]
+    int64_t ldq, ldo;            // elements
+    const int32_t *pages;        // [seqs][ld_pages]
+    int64_t ld_pages;
+    const AttnUnit *units;
+    const AttnJoin *joins;
+    float *partial;              // [slots][rows of a tile][padded head]
+    float *lse;                  // [slots][rows of a tile], in powers of two
+    int32_t num_units, num_joins;
+    int32_t group, head_dim;
+    int32_t causal, window;      // window 0: all keys
+    float scale2;                // scale log2 e
+};
+
+// Tiles of rows: of the kernel for few rows (single tokens, short chunks and
+// every float32 batch) up to 16 * kRowsMost(...), and of the one for prompts.
+constexpr int attn_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+constexpr int attn_rows_tiles(int head_dim) { return head_dim <= 128 ? 4 : 2; }
+hipError_t launch_attn_rows(int dtype, int nq, const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn_join(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s);
+
+struct RotaryArgs {
+    CacheArgs cache;             // k null: nothing is appended
+    const uint8_t *q, *k, *v;    // [T][ld]; q null: keys and values only
+    uint8_t *q_out;
+    int64_t ldq, ldqo, ldk, ldv; // elements
+    const int32_t *pages;
+    int64_t ld_pages;
+    const AttnToken *tokens;
+    const int32_t *positions;    // null: the tokens' own
+    const double *freqs;         // [rotary_dim / 2] radians a position; null: no rotation
+    int32_t T, heads, kv_heads, head_dim, rotary_dim;
+    int32_t layout;              // lora_rotary_layout
+    float magnitude;
+};
+hipError_t launch_rotary(int dtype, const RotaryArgs &a, hipStream_t s);
+
+}  // namespace lora

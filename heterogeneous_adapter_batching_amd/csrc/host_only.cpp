@@ -3,6 +3,7 @@
 // exercises the pool, plan, validation and exchange bookkeeping under the
 // address and undefined-behaviour sanitizers on a machine without a GPU; no
 // call that launches a kernel can succeed in it.
+#include "attend_internal.h"
 #include "layer_internal.h"
 #include "sgmv_internal.h"
 
@@ -33,6 +34,9 @@ hipError_t launch_operand(int, const OperandArgs &, hipStream_t) { return hipErr
 hipError_t launch_linear(int, const LinearPlan &, bool, LinearArgs, hipStream_t) {
     return hipErrorInvalidValue;
 }
+hipError_t launch_attn_rows(int, int, const AttnArgs &, hipStream_t) { return hipErrorInvalidValue; }
+hipError_t launch_attn_join(int, int, const AttnArgs &, hipStream_t) { return hipErrorInvalidValue; }
+hipError_t launch_rotary(int, const RotaryArgs &, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t static_scratch(void **, uint64_t *) { return hipErrorInvalidValue; }
 bool debug_build() { return false; }
 hipError_t debug_errors(uint32_t *, bool) { return hipErrorInvalidValue; }

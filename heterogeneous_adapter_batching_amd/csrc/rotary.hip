@@ -1,0 +1,184 @@
+// Rotary positions on a batch's new queries and keys, and the new keys and
+// values into the pages of their sequences.  With a_i = p f_i for the pair i
+// of a head at position p:
+//
+//     x' = m (x cos a_i - y sin a_i),   y' = m (y cos a_i + x sin a_i),
+//
+// the pair being elements i and i + r / 2 (halves) or 2 i and 2 i + 1
+// (interleaved) of a head's first r.  A position's angles are the same for all
+// heads of a token, so a workgroup has a token: it forms them once, in 64 bits
+// (a far position's angle has lost its fraction of a turn in 32: at 10^6 the
+// first pair's by 0.06 radians) up to the fraction of a turn, whose sine and
+// cosine are float32's, and every row of q, k and v is read and written once.
+// HBM bounds it.
+#include <hip/hip_runtime.h>
+
+#include "attend_internal.h"
+#include "device_ops.h"
+
+namespace lora {
+namespace {
+
+constexpr int kThreads = 256;
+
+// 8 consecutive elements, 16-byte aligned
+template <typename T> struct Vec8;
+template <> struct Vec8<uint16_t> {
+    u32x4 r;
+    __device__ __forceinline__ void load(const uint16_t *p) { r = *reinterpret_cast<const u32x4 *>(p); }
+    __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<u32x4 *>(p) = r; }
+    __device__ __forceinline__ float get(int j) const {
+        return j % 2 ? bf16_hi(r[j / 2]) : bf16_lo(r[j / 2]);
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = bf16x2_rne(v[2 * j], v[2 * j + 1]);
+    }
+};
+template <> struct Vec8<float> {
+    f32x4 r[2];
+    __device__ __forceinline__ void load(const float *p) {
+        r[0] = reinterpret_cast<const f32x4 *>(p)[0];
+        r[1] = reinterpret_cast<const f32x4 *>(p)[1];
+    }
+    __device__ __forceinline__ void store(float *p) const {
+        reinterpret_cast<f32x4 *>(p)[0] = r[0];
+        reinterpret_cast<f32x4 *>(p)[1] = r[1];
+    }
+    __device__ __forceinline__ float get(int j) const { return r[j / 4][j % 4]; }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j / 4][j % 4] = v[j];
+    }
+};
+__device__ __forceinline__ float value(uint16_t v) { return __uint_as_float(uint32_t(v) << 16); }
+__device__ __forceinline__ float value(float v) { return v; }
+__device__ __forceinline__ void put(uint16_t *p, float v) { *p = uint16_t(bf16x2_rne(v, v)); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+
+enum RotaryItems : int {
+    kHalves,     // 8 pairs: two vectors, half the rotated part apart
+    kPairs,      // 4 pairs: one vector
+    kOnes,       // one pair: rotated parts that are not made of whole vectors
+};
+
+// What one thread does at a time in a head that is rotated: `turned` items of
+// the rotated part, then `plain` of the rest.  The same thread reads and writes
+// all of an item, so that q may be rotated in place.
+template <typename T, int ITEMS>
+__global__ __launch_bounds__(kThreads) void k_rotary(const RotaryArgs a) {
+    __shared__ float2 turn[LORA_ATTN_MAX_HEAD_DIM / 2];   // (m cos, m sin) of every pair
+    const int t = blockIdx.x, tid = threadIdx.x;
+    const AttnToken tok = load_invariant(a.tokens + t);
+    const int pairs = a.freqs ? a.rotary_dim / 2 : 0;
+    if (tid < pairs) {
+        const int pos = a.positions ? a.positions[t] : tok.pos;
+        const double turns = double(pos) * a.freqs[tid] * 0.15915494309189533577;   // / 2 pi
+        float s, c;
+        sincospif(2.0f * float(turns - rint(turns)), &s, &c);
+        turn[tid] = float2{a.magnitude * c, a.magnitude * s};
+    }
+
+    // the place of the token's key and value; none in a page that is none
+    T *kc = nullptr, *vc = nullptr;
+    if (a.cache.k) {
+        const int p = tok.pos / a.cache.page_size, slot = tok.pos % a.cache.page_size;
+        const int page = load_invariant(a.pages + int64_t(tok.seq) * a.ld_pages + p);
+        if (page >= 0 && page < a.cache.num_pages) {
+            kc = reinterpret_cast<T *>(a.cache.k) + int64_t(page) * a.cache.k_page +
+                 int64_t(slot) * a.cache.k_tok;
+            vc = reinterpret_cast<T *>(a.cache.v) + int64_t(page) * a.cache.v_page +
+                 int64_t(slot) * a.cache.v_tok;
+        }
+    }
+    const T *q = reinterpret_cast<const T *>(a.q) + int64_t(t) * a.ldq;
+    const T *k = reinterpret_cast<const T *>(a.k) + int64_t(t) * a.ldk;
+    const T *v = reinterpret_cast<const T *>(a.v) + int64_t(t) * a.ldv;
+    T *qo = reinterpret_cast<T *>(a.q_out) + int64_t(t) * a.ldqo;
+
+    constexpr int PER = ITEMS == kHalves ? 16 : ITEMS == kPairs ? 8 : 2;   // elements of an item
+    constexpr int REST = ITEMS == kOnes ? 1 : 8;
+    const int turned = 2 * pairs / PER, plain = (a.head_dim - 2 * pairs) / REST;
+    const int heads = (a.q ? a.heads : 0) + (kc ? a.kv_heads : 0), first_k = a.q ? a.heads : 0;
+    __syncthreads();
+    for (int i = tid; i < heads * (turned + plain); i += kThreads) {
+        const int h = i / (turned + plain), e = i % (turned + plain);
+        const T *src = h < first_k ? q + int64_t(h) * a.head_dim
+                                   : k + int64_t(h - first_k) * a.head_dim;
+        T *dst = h < first_k ? qo + int64_t(h) * a.head_dim
+                             : kc + int64_t(h - first_k) * a.cache.k_head;
+        if (e >= turned) {
+            const int at = 2 * pairs + (e - turned) * REST;
+            if constexpr (ITEMS == kOnes) {
+                dst[at] = src[at];
+            } else {
+                Vec8<T> x;
+                x.load(src + at);
+                x.store(dst + at);
+            }
+        } else if constexpr (ITEMS == kHalves) {
+            Vec8<T> x, y;
+            x.load(src + e * 8);
+            y.load(src + pairs + e * 8);
+            float f[8], g[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 cs = turn[e * 8 + j];
+                f[j] = x.get(j) * cs.x - y.get(j) * cs.y;
+                g[j] = y.get(j) * cs.x + x.get(j) * cs.y;
+            }
+            x.set(f);
+            y.set(g);
+            x.store(dst + e * 8);
+            y.store(dst + pairs + e * 8);
+        } else if constexpr (ITEMS == kPairs) {
+            Vec8<T> x;
+            x.load(src + e * 8);
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 cs = turn[e * 4 + j];
+                f[2 * j] = x.get(2 * j) * cs.x - x.get(2 * j + 1) * cs.y;
+                f[2 * j + 1] = x.get(2 * j + 1) * cs.x + x.get(2 * j) * cs.y;
+            }
+            x.set(f);
+            x.store(dst + e * 8);
+        } else {
+            const int at = a.layout == LORA_ROTARY_HALF ? e : 2 * e;
+            const int to = a.layout == LORA_ROTARY_HALF ? e + pairs : 2 * e + 1;
+            const float x = value(src[at]), y = value(src[to]);
+            const float2 cs = turn[e];
+            put(dst + at, x * cs.x - y * cs.y);
+            put(dst + to, y * cs.x + x * cs.y);
+        }
+    }
+    if (!vc) return;
+    const int vecs = a.head_dim / 8;
+    for (int i = tid; i < a.kv_heads * vecs; i += kThreads) {
+        const int h = i / vecs, e = i % vecs;
+        Vec8<T> x;
+        x.load(v + int64_t(h) * a.head_dim + e * 8);
+        x.store(vc + int64_t(h) * a.cache.v_head + e * 8);
+    }
+}
+
+template <typename T> hipError_t rotary_types(const RotaryArgs &a, hipStream_t s) {
+    const dim3 grid(a.T), block(kThreads);
+    const int r = a.freqs ? a.rotary_dim : 0;
+    if (a.layout == LORA_ROTARY_HALF && r % 16 == 0)
+        hipLaunchKernelGGL((k_rotary<T, kHalves>), grid, block, 0, s, a);
+    else if (a.layout == LORA_ROTARY_INTERLEAVED && r % 8 == 0)
+        hipLaunchKernelGGL((k_rotary<T, kPairs>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((k_rotary<T, kOnes>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rotary(int dtype, const RotaryArgs &a, hipStream_t s) {
+    if (a.T <= 0) return hipSuccess;
+    return dtype == LORA_F32 ? rotary_types<float>(a, s) : rotary_types<uint16_t>(a, s);
+}
+
+}  // namespace lora

@@ -691,6 +691,132 @@ lora_status sgmv_linear(const lora_pool *p, const lora_plan *pl, int32_t layer, 
                         const void *residual, int64_t ldr, void *y, int64_t ldy, void *ws,
                         uint64_t ws_bytes, void *stream);
 
+/* ----------------------------------------------------------- attention ---- */
+/* What lies between a layer's q/k/v product and its o product: rotary
+ * positions on the new queries and keys, the new keys and values into a paged
+ * cache, and attention over it.  Inference only: no gradients.
+ *
+ * The cache keeps keys and values in pages of page_size tokens, which belong
+ * to the sequences as a page table says: key j of sequence s is token
+ * j % page_size of page pages[s][j / page_size].  Pages are the caller's, in
+ * any order, with any strides. */
+#define LORA_ATTN_MAX_HEADS 1024
+#define LORA_ATTN_MAX_HEAD_DIM 256
+#define LORA_ATTN_MAX_PAGE 65536
+
+typedef struct {
+    int32_t dtype;       /* lora_dtype of q, k, v, the cache and o */
+    int32_t heads;       /* query heads: a multiple of kv_heads, at most LORA_ATTN_MAX_HEADS */
+    int32_t kv_heads;    /* key and value heads; query heads h * group .. share key head h */
+    int32_t head_dim;    /* a multiple of 8, at most LORA_ATTN_MAX_HEAD_DIM */
+    int32_t page_size;   /* tokens of a page: a multiple of 16, at most LORA_ATTN_MAX_PAGE */
+    int32_t causal;      /* 1: a token sees the keys up to its own; 0: all of the sequence's
+                            (an encoder's states) */
+    int32_t window;      /* with causal: the last `window` of them; 0: all */
+    int32_t max_kv;      /* 0, or the most keys of a sequence in any rebuild: see below */
+} lora_attn_desc;
+
+/* The plan of one batch: S sequences in order, new_lens[s] tokens of each
+ * (rows of q; 0 allowed) at the end of kv_lens[s] keys (causal: the new tokens'
+ * own among them, so at least as many).  Host only.  It cuts the work into
+ * parts of about equal size, also when one sequence is much longer than the
+ * others.  At most 2^23 tokens, and tiles of 16 rows (a token's query heads of
+ * one key head) over all key heads; at most 2^30 keys a sequence.
+ * attn_plan_rebuild re-plans in place; attn_plan_upload copies the tables into
+ * `ws` (256-byte aligned, attn_plan_workspace_bytes) on `stream`, from one of
+ * two pinned buffers in turn.  A call with a plan that was rebuilt since, or
+ * whose workspace another plan has been uploaded to, is refused (LORA_ESTATE).
+ * A captured graph keeps the launches it was captured with.  With max_kv they
+ * depend on new_lens (and max_kv) alone: such a graph may be replayed after a
+ * rebuild with the same new_lens and an upload into the same workspace.
+ * A workspace also holds partial sums: calls that share one must not overlap.
+ * attn_plan_stats: tokens, parts, tiles in several parts, the longest
+ * sequence's keys; pointers may be NULL.
+ * Errors: LORA_EINVAL, LORA_EDTYPE, LORA_ESTATE (ws too small), LORA_ENOSPC
+ * (host memory), LORA_EHIP. */
+typedef struct attn_plan attn_plan;
+lora_status attn_plan_create(attn_plan **out, const lora_attn_desc *d, const int32_t *new_lens,
+                             const int32_t *kv_lens, int32_t num_seqs);
+lora_status attn_plan_rebuild(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens,
+                              int32_t num_seqs);
+lora_status attn_plan_destroy(attn_plan *p);
+uint64_t attn_plan_workspace_bytes(const attn_plan *p);
+lora_status attn_plan_upload(attn_plan *p, void *ws, uint64_t ws_bytes, void *stream);
+lora_status attn_plan_stats(const attn_plan *p, int32_t *num_tokens, int32_t *num_units,
+                            int32_t *num_joins, int32_t *max_kv);
+
+/* Keys and values of num_pages pages: element e of token t of page p, head h,
+ * at k + p k_page_stride + h k_head_stride + t k_token_stride + e.  16-byte
+ * aligned; strides are multiples of 8 elements. */
+typedef struct {
+    void *k, *v;
+    int64_t k_page_stride, k_head_stride, k_token_stride;
+    int64_t v_page_stride, v_head_stride, v_token_stride;
+    int32_t num_pages;
+} lora_kv_cache;
+
+/* Attention of the plan's tokens over their sequences' keys:
+ *     o = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale q.k_j - M),
+ * M the largest score, for every query head; over the keys that the plan
+ * says the token sees.  Sums, maxima and (float32) products are float32;
+ * bfloat16 weights enter the second product as bfloat16, for tiles of few rows
+ * with the rounding's remainder in a second one; o is rounded once.  A token
+ * without a key gets zeros.  Keys and values that a token does not see do not
+ * reach it, whatever they hold; a key in a page that the table gives as less
+ * than 0 or num_pages and more counts as absent.  q, o: [T][ldq / ldo], head h
+ * at column h * head_dim, 16-byte aligned, leading dimensions multiples of 8;
+ * rows from the plan's last token on are not touched.  pages: [S][ld_pages]
+ * on the device, pages_per_seq of them for each sequence, enough for its keys.
+ * o may not overlap q or the cache.
+ * Errors: LORA_EINVAL, LORA_ESTATE (the plan), LORA_EHIP. */
+lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
+                            const lora_kv_cache *cache, const int32_t *pages, int64_t ld_pages,
+                            int32_t pages_per_seq, float scale, void *o, int64_t ldo,
+                            void *stream);
+
+/* Which elements of a head's first r make pair i: i and i + r / 2, or 2 i and
+ * 2 i + 1. */
+typedef enum { LORA_ROTARY_HALF = 0, LORA_ROTARY_INTERLEAVED = 1 } lora_rotary_layout;
+/* Radians a position, f_i = base^(-2 i / r): as they are; divided by `factor`;
+ * or by parts: a pair that makes at least `high` turns within original_length
+ * positions as it is, one of at most `low` turns divided, between them a blend
+ * linear in the turns.  out: r / 2 doubles on the host. */
+typedef enum {
+    LORA_ROTARY_UNSCALED = 0,
+    LORA_ROTARY_LINEAR = 1,
+    LORA_ROTARY_BY_PARTS = 2
+} lora_rotary_scaling;
+lora_status rotary_frequencies(double *out, int32_t rotary_dim, double base, int32_t scaling,
+                               double factor, double original_length, double low, double high);
+
+typedef struct {
+    int32_t rotary_dim;  /* r: even, at most head_dim; the rest of a head is left as it is */
+    int32_t layout;      /* lora_rotary_layout */
+    float magnitude;     /* m: scales the rotated part (1 for none) */
+} lora_rotary_desc;
+
+/* Rotary positions on the plan's tokens, and their keys and values into the
+ * cache: for pair (x, y) of a head and angle a = position * f_i,
+ *     (m (x cos a - y sin a), m (y cos a + x sin a)),
+ * q into q_out (which may be q itself), k into the pages, v into the pages as
+ * it is.  Angles are formed in 64 bits; values are rounded once.  positions:
+ * [T] on the device, or NULL for the tokens' places among their keys; where
+ * keys and values go is the plan's either way.  freqs: r / 2 doubles on the
+ * device (rotary_frequencies, or any other), or NULL: nothing is rotated
+ * (rotary_dim 0).  q and q_out may be NULL (keys and values only: an
+ * encoder's states), and so may k, v, cache and pages together (queries only).
+ * A token whose page the table gives as less than 0 or num_pages and more is
+ * not stored.  Two tokens of one batch must not share a place in the cache.
+ * Rows from the plan's last token on are not touched.  Sequences as the plan
+ * says, their last new_lens[s] keys being the new ones (a plan that is not
+ * causal too).  Alignment as paged_attention.
+ * Errors: LORA_EINVAL, LORA_ESTATE (the plan), LORA_EHIP. */
+lora_status rotary_append(const attn_plan *p, const lora_rotary_desc *r, const void *q, int64_t ldq,
+                          void *q_out, int64_t ldqo, const void *k, int64_t ldk, const void *v,
+                          int64_t ldv, const lora_kv_cache *cache, const int32_t *pages,
+                          int64_t ld_pages, int32_t pages_per_seq, const int32_t *positions,
+                          const double *freqs, void *stream);
+
 /* --------------------------------------------------------------- debug ---- */
 /* The library built with LORA_SGMV_DEBUG (libhab_lora_debug.so, for
  * debugging the kernels or a caller's plan memory) checks in every work unit
