@@ -25,7 +25,7 @@ SOURCES = [os.path.join(CSRC, "lora_sgmv.cpp"), os.path.join(CSRC, "exchange.cpp
            os.path.join(CSRC, "layer.cpp"), os.path.join(CSRC, "kernels.hip"),
            os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "linear.hip"),
            os.path.join(CSRC, "attend.cpp"), os.path.join(CSRC, "attend.hip"),
-           os.path.join(CSRC, "rotary.hip")]
+           os.path.join(CSRC, "attend_prompt.hip"), os.path.join(CSRC, "rotary.hip")]
 
 # Packed float32 ALU ops are switched off for all device code; the compiler's
 # host pass warns that it does not know the feature, which is harmless.

@@ -35,6 +35,7 @@ constexpr int32_t kMostTokens = 1 << 23, kMostKeys = 1 << 30;
 // Units a launch aims for when it cuts the tiles' keys into parts, and the
 // fewest keys of a part.
 constexpr int kRowsUnits = 1024, kRowsKeys = 256;
+constexpr int kPromptUnits = 512, kPromptKeys = 512;
 
 // One kernel's share of a plan: its tiles of rows, and their keys in parts.
 struct Side {
@@ -54,7 +55,7 @@ struct attn_plan {
     std::vector<int32_t> new_lens, kv_lens;
     std::vector<AttnToken> tokens;
     int32_t most_kv = 0;
-    Side rows;
+    Side rows, prompt;
     uint64_t off_tokens = 0, image_bytes = 0, ws_bytes = 0;
 
     void *ws = nullptr;
@@ -146,46 +147,68 @@ int64_t blocks_of(int32_t lo, int32_t hi) {
     return hi > lo ? (int64_t(hi) - lo + lora::kAttnBlock - 1) / lora::kAttnBlock : 0;
 }
 
+// Whether a sequence of so many rows is a prompt's.
+bool is_prompt(const attn_plan &p, int64_t rows) {
+    return p.d.dtype == LORA_BF16 && rows > lora::attn_rows_most(p.d.head_dim);
+}
+
+// fn(sequence, its first token, its rows) for the sequences of one side.
+template <typename Fn> void each_seq(const attn_plan &p, bool prompt, Fn fn) {
+    int32_t tok0 = 0;
+    for (size_t s = 0; s < p.new_lens.size(); ++s) {
+        const int64_t rows = int64_t(p.new_lens[s]) * p.group;
+        if (rows && is_prompt(p, rows) == prompt) fn(int32_t(s), tok0, rows);
+        tok0 += p.new_lens[s];
+    }
+}
+
 // Cuts every tile's keys into parts, so that the launch has about `target`
 // units, none shorter than `least` keys, and lays them out one after another.
 // The cut is even: no more parts than tiles + target in all.
-void cut(const attn_plan &p, Side *side, int64_t target, int64_t least) {
+void cut(const attn_plan &p, Side *side, bool prompt, int64_t target, int64_t least) {
     side->units.clear();
     side->joins.clear();
-    const int32_t S = int32_t(p.new_lens.size());
+    side->tiles = 0;
     int64_t total = 0;
-    for (int32_t s = 0; s < S; ++s) {
-        const int64_t rows = int64_t(p.new_lens[s]) * p.group;
+    each_seq(p, prompt, [&](int32_t s, int32_t, int64_t rows) {
         for (int64_t r = 0; r < rows; r += side->tile_rows) {
             int32_t lo, hi;
             tile_keys(p, s, r, std::min<int64_t>(rows, r + side->tile_rows), &lo, &hi);
             total += blocks_of(lo, hi) * p.d.kv_heads;
+            side->tiles += p.d.kv_heads;
         }
-    }
+    });
     const int64_t part = std::max(least / lora::kAttnBlock, (total + target - 1) / target);
-    int32_t tok0 = 0, slot = 0;
-    for (int32_t s = 0; s < S; ++s) {
-        const int64_t rows = int64_t(p.new_lens[s]) * p.group;
+    int32_t slot = 0;
+    each_seq(p, prompt, [&](int32_t s, int32_t tok0, int64_t rows) {
         for (int64_t r = 0; r < rows; r += side->tile_rows) {
             int32_t lo, hi;
             tile_keys(p, s, r, std::min<int64_t>(rows, r + side->tile_rows), &lo, &hi);
             const int64_t blocks = blocks_of(lo, hi);
             const int64_t parts = std::max<int64_t>(1, (blocks + part - 1) / part);
-            for (int32_t h = 0; h < p.d.kv_heads; ++h) {
-                if (parts > 1)
-                    side->joins.push_back({tok0, h, int32_t(r), int32_t(rows), slot, int32_t(parts)});
-                for (int64_t i = 0; i < parts; ++i) {
-                    const int64_t k0 = lo + blocks * i / parts * lora::kAttnBlock;
-                    const int64_t k1 = lo + blocks * (i + 1) / parts * lora::kAttnBlock;
+            if (parts > 1)
+                for (int32_t h = 0; h < p.d.kv_heads; ++h)
+                    side->joins.push_back({tok0, h, int32_t(r), int32_t(rows),
+                                           slot + int32_t(h * parts), int32_t(parts)});
+            // (key heads beside one another: each on an XCD of its own, whose L2
+            // then keeps its keys)
+            for (int64_t i = 0; i < parts; ++i) {
+                const int64_t k0 = lo + blocks * i / parts * lora::kAttnBlock;
+                const int64_t k1 = lo + blocks * (i + 1) / parts * lora::kAttnBlock;
+                for (int32_t h = 0; h < p.d.kv_heads; ++h)
                     side->units.push_back({s, h, int32_t(r), int32_t(rows), tok0,
                                            p.kv_lens[s] - p.new_lens[s], int32_t(k0),
                                            int32_t(std::min<int64_t>(k1, hi)),
-                                           parts > 1 ? slot++ : -1});
-                }
+                                           parts > 1 ? slot + int32_t(h * parts + i) : -1});
             }
+            if (parts > 1) slot += int32_t(parts * p.d.kv_heads);
         }
-        tok0 += p.new_lens[s];
-    }
+    });
+    // the longest parts first: the short ones fill the end
+    if (prompt)
+        std::stable_sort(side->units.begin(), side->units.end(), [](const AttnUnit &a, const AttnUnit &b) {
+            return a.key1 - a.key0 > b.key1 - b.key0;
+        });
     side->cap_units = int64_t(side->units.size());
     side->cap_joins = int64_t(side->joins.size());
     side->cap_slots = slot;
@@ -204,20 +227,19 @@ void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, i
     p->kv_lens.assign(kv_lens, kv_lens + S);
     p->tokens.clear();
     p->most_kv = 0;
-    int64_t most_rows = 0;
     for (int32_t s = 0; s < S; ++s) {
         p->most_kv = std::max(p->most_kv, kv_lens[s]);
-        most_rows = std::max(most_rows, int64_t(new_lens[s]) * p->group);
         for (int32_t i = 0; i < new_lens[s]; ++i)
             p->tokens.push_back({s, kv_lens[s] - new_lens[s] + i});
     }
-    Side &side = p->rows;
-    side = Side{};
-    side.tile_rows = most_rows <= 16 ? 16 : most_rows <= 32 ? 32 : 16 * lora::attn_rows_tiles(p->d.head_dim);
-    for (int32_t s = 0; s < S; ++s)
-        side.tiles += (int64_t(new_lens[s]) * p->group + side.tile_rows - 1) / side.tile_rows *
-                      p->d.kv_heads;
-    cut(*p, &side, kRowsUnits, kRowsKeys);
+    int64_t few = 0;
+    each_seq(*p, false, [&](int32_t, int32_t, int64_t rows) { few = std::max(few, rows); });
+    p->rows = Side{};
+    p->rows.tile_rows = few <= 16 ? 16 : few <= 32 ? 32 : lora::attn_rows_most(p->d.head_dim);
+    cut(*p, &p->rows, false, kRowsUnits, kRowsKeys);
+    p->prompt = Side{};
+    p->prompt.tile_rows = lora::kPromptRows;
+    cut(*p, &p->prompt, true, kPromptUnits, kPromptKeys);
 
     uint64_t at = 0;
     auto place = [&](uint64_t bytes) {
@@ -226,12 +248,16 @@ void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, i
         return off;
     };
     p->off_tokens = place(sizeof(AttnToken) * p->tokens.size());
-    side.off_units = place(sizeof(AttnUnit) * uint64_t(side.cap_units));
-    side.off_joins = place(sizeof(AttnJoin) * uint64_t(side.cap_joins));
+    for (Side *side : {&p->rows, &p->prompt}) {
+        side->off_units = place(sizeof(AttnUnit) * uint64_t(side->cap_units));
+        side->off_joins = place(sizeof(AttnJoin) * uint64_t(side->cap_joins));
+    }
     p->image_bytes = at;
-    const uint64_t rows = uint64_t(side.cap_slots) * uint64_t(side.tile_rows);
-    side.off_partial = place(rows * 4 * uint64_t(lora::attn_dim(p->d.head_dim)));
-    side.off_lse = place(rows * 4);
+    for (Side *side : {&p->rows, &p->prompt}) {
+        const uint64_t rows = uint64_t(side->cap_slots) * uint64_t(side->tile_rows);
+        side->off_partial = place(rows * 4 * uint64_t(lora::attn_dim(p->d.head_dim)));
+        side->off_lse = place(rows * 4);
+    }
     p->ws_bytes = at;
 }
 
@@ -404,8 +430,8 @@ lora_status attn_plan_stats(const attn_plan *p, int32_t *num_tokens, int32_t *nu
                             int32_t *num_joins, int32_t *max_kv) {
     if (!p) return set_errorf(LORA_EINVAL, "null plan");
     if (num_tokens) *num_tokens = int32_t(p->tokens.size());
-    if (num_units) *num_units = int32_t(p->rows.units.size());
-    if (num_joins) *num_joins = int32_t(p->rows.joins.size());
+    if (num_units) *num_units = int32_t(p->rows.units.size() + p->prompt.units.size());
+    if (num_joins) *num_joins = int32_t(p->rows.joins.size() + p->prompt.joins.size());
     if (max_kv) *max_kv = p->most_kv;
     return LORA_OK;
 }
@@ -440,14 +466,16 @@ lora_status attn_plan_upload(attn_plan *p, void *ws, uint64_t ws_bytes, void *st
             if (!table.empty()) std::memcpy(img + off, table.data(), sizeof(table[0]) * table.size());
         };
         put(p->off_tokens, p->tokens);
-        put(p->rows.off_units, p->rows.units);
-        put(p->rows.off_joins, p->rows.joins);
-        // places without work: no sequence, no parts
-        AttnUnit *u = reinterpret_cast<AttnUnit *>(img + p->rows.off_units);
-        for (int64_t i = int64_t(p->rows.units.size()); i < p->rows.cap_units; ++i)
-            u[i] = AttnUnit{-1, 0, 0, 0, 0, 0, 0, 0, -1};
-        AttnJoin *j = reinterpret_cast<AttnJoin *>(img + p->rows.off_joins);
-        for (int64_t i = int64_t(p->rows.joins.size()); i < p->rows.cap_joins; ++i) j[i] = AttnJoin{};
+        for (const Side *side : {&p->rows, &p->prompt}) {
+            put(side->off_units, side->units);
+            put(side->off_joins, side->joins);
+            // places without work: no sequence, no parts
+            AttnUnit *u = reinterpret_cast<AttnUnit *>(img + side->off_units);
+            for (int64_t i = int64_t(side->units.size()); i < side->cap_units; ++i)
+                u[i] = AttnUnit{-1, 0, 0, 0, 0, 0, 0, 0, -1};
+            AttnJoin *j = reinterpret_cast<AttnJoin *>(img + side->off_joins);
+            for (int64_t i = int64_t(side->joins.size()); i < side->cap_joins; ++i) j[i] = AttnJoin{};
+        }
         hipStream_t s = static_cast<hipStream_t>(stream);
         e = hipMemcpyAsync(ws, img, p->image_bytes, hipMemcpyHostToDevice, s);
         if (e == hipSuccess) e = hipEventRecord(p->staged[k], s);
@@ -491,17 +519,25 @@ lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
     a.head_dim = p->d.head_dim;
     a.causal = p->d.causal;
     a.window = p->d.window;
-    a.scale2 = scale * 1.44269504088896340736f;
-    const Side &side = p->rows;
-    a.units = reinterpret_cast<const AttnUnit *>(ws + side.off_units);
-    a.joins = reinterpret_cast<const AttnJoin *>(ws + side.off_joins);
-    a.partial = reinterpret_cast<float *>(ws + side.off_partial);
-    a.lse = reinterpret_cast<float *>(ws + side.off_lse);
-    a.num_units = int32_t(side.cap_units);
-    a.num_joins = int32_t(side.cap_joins);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e = lora::launch_attn_rows(p->d.dtype, side.tile_rows / 16, a, s);
-    if (e == hipSuccess) e = lora::launch_attn_join(p->d.dtype, side.tile_rows, a, s);
+    hipError_t e = hipSuccess;
+    for (const Side *side : {&p->rows, &p->prompt}) {
+        const bool prompt = side == &p->prompt;
+        a.units = reinterpret_cast<const AttnUnit *>(ws + side->off_units);
+        a.joins = reinterpret_cast<const AttnJoin *>(ws + side->off_joins);
+        a.partial = reinterpret_cast<float *>(ws + side->off_partial);
+        a.lse = reinterpret_cast<float *>(ws + side->off_lse);
+        a.num_units = int32_t(side->cap_units);
+        a.num_joins = int32_t(side->cap_joins);
+        a.scale2 = scale * 1.44269504088896340736f;
+        a.negate = prompt && a.scale2 < 0;
+        // (the least scale leaves masked scores of -inf what they are)
+        if (prompt) a.scale2 = std::max(std::fabs(a.scale2), 1e-30f);
+        if (e == hipSuccess)
+            e = prompt ? lora::launch_attn_prompt(a, s)
+                       : lora::launch_attn_rows(p->d.dtype, side->tile_rows, a, s);
+        if (e == hipSuccess) e = lora::launch_attn_join(p->d.dtype, side->tile_rows, a, s);
+    }
     if (e != hipSuccess)
         return set_errorf(LORA_EHIP, "attention launch: %s", hipGetErrorString(e));
     return LORA_OK;

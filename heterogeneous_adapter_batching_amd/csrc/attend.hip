@@ -342,19 +342,19 @@ template <typename T, int DP, int NQ> hipError_t rows_launch(const AttnArgs &a, 
     hipLaunchKernelGGL((k_attend_rows<T, DP, NQ>), dim3(a.num_units), dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
-template <typename T, int DP> hipError_t rows_dim(int nq, const AttnArgs &a, hipStream_t s) {
-    if (nq == 1) return rows_launch<T, DP, 1>(a, s);
-    if (nq == 2) return rows_launch<T, DP, 2>(a, s);
+template <typename T, int DP> hipError_t rows_dim(int tile_rows, const AttnArgs &a, hipStream_t s) {
+    if (tile_rows == 16) return rows_launch<T, DP, 1>(a, s);
+    if (tile_rows == 32) return rows_launch<T, DP, 2>(a, s);
     if constexpr (DP <= 128) {
-        if (nq == 4) return rows_launch<T, DP, 4>(a, s);
+        if (tile_rows == 64) return rows_launch<T, DP, 4>(a, s);
     }
     return hipErrorInvalidValue;
 }
-template <typename T> hipError_t rows_types(int nq, const AttnArgs &a, hipStream_t s) {
+template <typename T> hipError_t rows_types(int tile_rows, const AttnArgs &a, hipStream_t s) {
     switch (attn_dim(a.head_dim)) {
-        case 64: return rows_dim<T, 64>(nq, a, s);
-        case 128: return rows_dim<T, 128>(nq, a, s);
-        default: return rows_dim<T, 256>(nq, a, s);
+        case 64: return rows_dim<T, 64>(tile_rows, a, s);
+        case 128: return rows_dim<T, 128>(tile_rows, a, s);
+        default: return rows_dim<T, 256>(tile_rows, a, s);
     }
 }
 template <typename T> hipError_t join_types(int tile_rows, const AttnArgs &a, hipStream_t s) {
@@ -369,9 +369,9 @@ template <typename T> hipError_t join_types(int tile_rows, const AttnArgs &a, hi
 
 }  // namespace
 
-hipError_t launch_attn_rows(int dtype, int nq, const AttnArgs &a, hipStream_t s) {
+hipError_t launch_attn_rows(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s) {
     if (a.num_units <= 0) return hipSuccess;
-    return dtype == LORA_F32 ? rows_types<float>(nq, a, s) : rows_types<uint16_t>(nq, a, s);
+    return dtype == LORA_F32 ? rows_types<float>(tile_rows, a, s) : rows_types<uint16_t>(tile_rows, a, s);
 }
 
 hipError_t launch_attn_join(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s) {

@@ -60,13 +60,17 @@ struct AttnArgs {
     int32_t group, head_dim;
     int32_t causal, window;      // window 0: all keys
     float scale2;                // scale log2 e
+    bool negate;                 // prompts: of -q, so that scale2 is positive
 };
 
-// Tiles of rows: of the kernel for few rows (single tokens, short chunks and
-// every float32 batch) up to 16 * kRowsMost(...), and of the one for prompts.
+// What a head is padded to, and the most rows of a tile of the kernel for few
+// rows (single tokens, short chunks, every float32 batch); prompts' have
+// their own kernel.
 constexpr int attn_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
-constexpr int attn_rows_tiles(int head_dim) { return head_dim <= 128 ? 4 : 2; }
-hipError_t launch_attn_rows(int dtype, int nq, const AttnArgs &a, hipStream_t s);
+constexpr int attn_rows_most(int head_dim) { return head_dim <= 128 ? 64 : 32; }
+hipError_t launch_attn_rows(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s);
+constexpr int kPromptRows = 128; // of a tile of prompts
+hipError_t launch_attn_prompt(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_join(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s);
 
 struct RotaryArgs {

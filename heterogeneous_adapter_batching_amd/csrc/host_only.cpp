@@ -35,6 +35,7 @@ hipError_t launch_linear(int, const LinearPlan &, bool, LinearArgs, hipStream_t)
     return hipErrorInvalidValue;
 }
 hipError_t launch_attn_rows(int, int, const AttnArgs &, hipStream_t) { return hipErrorInvalidValue; }
+hipError_t launch_attn_prompt(const AttnArgs &, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_attn_join(int, int, const AttnArgs &, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_rotary(int, const RotaryArgs &, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t static_scratch(void **, uint64_t *) { return hipErrorInvalidValue; }
