@@ -41,6 +41,11 @@ __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
+// (a maximum with NaN is NaN: three operands to an instruction, and the row's
+// result is NaN either way)
+__device__ __forceinline__ float largest(float a, float b) {
+    return __builtin_elementwise_maximum(a, b);
+}
 // fn over lanes l and l ^ 32
 template <typename Fn> __device__ __forceinline__ float over_halves(float v, Fn fn) {
     const auto h =
@@ -55,16 +60,23 @@ template <int N, typename Fn, int I = 0> __device__ __forceinline__ void each(Fn
     }
 }
 
+// Has a vector unit's result formed here, between the matrix instructions,
+// where the compiler would form it where it is used.
+__device__ __forceinline__ void here(float &v) { asm volatile("" : "+v"(v)); }
+
 // A row of a stage is DP elements in vectors of 16 bytes, exchanged by
-// (exclusive or) swizzle(row): the 16 rows that a read of K touches at one
-// vector, and the 8 rows at 4 vectors of a transposing read of V, then spread
-// over all banks.
-template <int DP> __device__ __forceinline__ constexpr int swizzle(int row) {
-    return DP == 64 ? ((row >> 1 & 3) << 1) | (row >> 3 & 1) : ((row & 7) << 1) | (row >> 3 & 1);
+// (exclusive or) a swizzle of the row, so that the 16 rows that a part of a
+// read of K touches at one vector, and the 4 rows at 4 vectors that a part of a
+// transposing read of V does, spread over all banks.
+template <int DP> __device__ __forceinline__ constexpr int k_swizzle(int row) {
+    return DP == 64 ? row >> 1 & 7 : (row & 3) << 2 | (row >> 2 & 3);
+}
+template <int DP> __device__ __forceinline__ constexpr int v_swizzle(int row) {
+    return DP == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2;
 }
 
-template <int DP, int QT>
-__global__ __launch_bounds__(kPromptThreads, DP == 256 || QT == 2 ? 1 : 2) void
+template <int DP>
+__global__ __launch_bounds__(kPromptThreads, DP == 256 ? 1 : 2) void
 k_attend_prompt(const AttnArgs a) {
     constexpr int RB = DP * 2;                        // bytes of a row in LDS
     constexpr int KK = DP / 16, DT = DP / 32;         // steps of a score, tiles of the output
@@ -79,29 +91,26 @@ k_attend_prompt(const AttnArgs a) {
     const int D = a.head_dim;
     const int tiles = (u.key1 - u.key0 + kKeys - 1) / kKeys;
 
-    // the rows' queries, and the last and first key that each sees
-    const int wave_row = u.row0 + w * QT * 32;
-    const uint32_t flip = a.negate ? 0x80008000u : 0u;
-    u32x4 q[QT][KK];
-    int last[QT], first[QT];
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        const int r = wave_row + t * 32 + n;
-        const bool row = r < u.rows;
-        const int tok = r / a.group, head = u.kv_head * a.group + r % a.group;
+    // the lane's row: its query, and the last and first key that it sees
+    const int wave_row = u.row0 + w * 32, r = wave_row + n;
+    const bool row = r < u.rows;
+    const int tok = r / a.group, head = u.kv_head * a.group + r % a.group;
+    u32x4 q[KK];
+    {
         const uint16_t *p = reinterpret_cast<const uint16_t *>(a.q) +
                             int64_t(u.tok0 + tok) * a.ldq + int64_t(head) * D;
+        const uint32_t flip = a.negate ? 0x80008000u : 0u;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             const int e = kk * 16 + h * 8;
-            q[t][kk] = u32x4{0u, 0u, 0u, 0u};
-            if (row && e < D) q[t][kk] = *reinterpret_cast<const u32x4 *>(p + e) ^ flip;
+            q[kk] = u32x4{0u, 0u, 0u, 0u};
+            if (row && e < D) q[kk] = *reinterpret_cast<const u32x4 *>(p + e) ^ flip;
         }
-        last[t] = !row ? -1 : a.causal ? min(u.pos0 + tok, u.key1 - 1) : u.key1 - 1;
-        first[t] = row && a.window ? u.pos0 + tok - a.window + 1 : 0;
     }
+    const int last = !row ? -1 : a.causal ? min(u.pos0 + tok, u.key1 - 1) : u.key1 - 1;
+    const int first = row && a.window ? u.pos0 + tok - a.window + 1 : 0;
     // keys that all of the wave's rows see: from all_from to all_to
-    const int tail = min(wave_row + QT * 32, u.rows) - 1;
+    const int tail = min(wave_row + 32, u.rows) - 1;
     int all_to = a.causal ? min(u.pos0 + wave_row / a.group, u.key1 - 1) : u.key1 - 1;
     const int all_from = a.window ? u.pos0 + tail / a.group - a.window + 1 : 0;
 
@@ -114,66 +123,77 @@ k_attend_prompt(const AttnArgs a) {
     bad = __syncthreads_or(bad);
     if (bad) all_to = -1;                             // every key is looked up
 
-    // a lane's vector in a copy, its vector of K's rows, its parts of V's
-    uint32_t k_off[COPIES], v_off[COPIES];
+    // a lane's vector in a copy (of 1024 bytes: whole rows), its vector of K's
+    // rows, its parts of V's
+    constexpr int PER = 1024 / RB, V_KINDS = PER < 4 ? 4 / PER : 1;
+    uint32_t k_off[COPIES], v_off[V_KINDS];
     const uint32_t k_row = uint32_t(a.cache.k_tok) * 2u, v_row = uint32_t(a.cache.v_tok) * 2u;
+    const int copy_row = lane * 16 / RB, copy_vec = lane * 16 % RB / 16;
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
-        const int at = i * 1024 + lane * 16, row = at / RB, vec = at % RB / 16 ^ swizzle<DP>(row);
-        k_off[i] = off_or_oob(vec * 8 < D, uint32_t(row) * k_row + uint32_t(vec) * 16u);
-        v_off[i] = off_or_oob(vec * 8 < D, uint32_t(row) * v_row + uint32_t(vec) * 16u);
+        const int vec = copy_vec ^ k_swizzle<DP>(i * PER + copy_row);
+        k_off[i] = off_or_oob(vec * 8 < D, uint32_t(copy_row) * k_row + uint32_t(vec) * 16u);
+        asm volatile("" : "+v"(k_off[i]));   // (kept, not formed again for every tile)
+    }
+#pragma unroll
+    for (int i = 0; i < V_KINDS; ++i) {
+        const int vec = copy_vec ^ v_swizzle<DP>(i * PER + copy_row);
+        v_off[i] = off_or_oob(vec * 8 < D, uint32_t(copy_row) * v_row + uint32_t(vec) * 16u);
+        asm volatile("" : "+v"(v_off[i]));
     }
     const uint32_t base = uint32_t(reinterpret_cast<uintptr_t>((lds_byte *)lds));
-    uint32_t k_at[KK], v_at[2][DT];
+    uint32_t k_at[KK], v_at[DT];
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk)
-        k_at[kk] = base + uint32_t(n * RB + ((2 * kk + h) ^ swizzle<DP>(n)) * 16);
+        k_at[kk] = base + uint32_t(n * RB + ((2 * kk + h) ^ k_swizzle<DP>(n)) * 16);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-            const int j = lane & 15, row = 8 * i + 4 * h + j / 4;
-            const int vec = 4 * dt + 2 * (lane >> 4 & 1) + (j & 3) / 2;
-            v_at[i][dt] = base + uint32_t(2 * STAGE + row * RB + (vec ^ swizzle<DP>(row)) * 16 +
-                                          (j & 1) * 8);
-        }
+    for (int dt = 0; dt < DT; ++dt) {
+        const int j = lane & 15, row = 4 * h + j / 4;
+        const int vec = 4 * dt + 2 * (lane >> 4 & 1) + (j & 3) / 2;
+        v_at[dt] = base + uint32_t(2 * STAGE + row * RB + (vec ^ v_swizzle<DP>(row)) * 16 +
+                                   (j & 1) * 8);
+    }
 
-    // the copies of tile i: the wave's 16 keys of K and of V
-    int page = (u.key0 + 16 * w) / ps, slot = (u.key0 + 16 * w) % ps;   // of K's next tile
-    int page_v = page, slot_v = slot;
-    auto resource = [&](int i, int pg, int sl, bool values) {
-        const int key = u.key0 + i * kKeys + 16 * w;
-        const int id = key < u.key1 ? load_invariant(table + pg) : -1;
+    // The copies of a tile: the wave's 16 keys of K and of V.  What they need
+    // (all of it uniform) is formed a tile ahead, from a page number read two
+    // ahead, between the matrix instructions.
+    const uint8_t *k_head = a.cache.k + int64_t(u.kv_head) * a.cache.k_head * 2;
+    const uint8_t *v_head = a.cache.v + int64_t(u.kv_head) * a.cache.v_head * 2;
+    const int64_t k_page = a.cache.k_page * 2, v_page = a.cache.v_page * 2;
+    const int pages_end = (u.key1 + ps - 1) / ps;     // of the unit's keys
+    int key = 0, slot = 0, next_page = 0, id = 0;     // the tile to be formed, the page read
+    u32x4 kr, vr, vr_last;                            // V is copied a tile behind K
+    auto read_page = [&] { id = load_invariant(table + min(next_page, pages_end - 1)); };
+    auto form = [&] {
         const bool there = id >= 0 && id < a.cache.num_pages;
         const int rows = there ? min(16, u.key1 - key) : 0;
-        const uint8_t *p = values
-            ? a.cache.v + (int64_t(there ? id : 0) * a.cache.v_page +
-                           int64_t(u.kv_head) * a.cache.v_head + int64_t(sl) * a.cache.v_tok) * 2
-            : a.cache.k + (int64_t(there ? id : 0) * a.cache.k_page +
-                           int64_t(u.kv_head) * a.cache.k_head + int64_t(sl) * a.cache.k_tok) * 2;
-        const uint32_t row = values ? v_row : k_row;
-        return raw_rsrc(p, rows ? uint32_t(rows - 1) * row + uint32_t(D * 2) : 0u);
-    };
-    auto step = [&](int &pg, int &sl) {
-        sl += kKeys;
-        while (sl >= ps) {
-            sl -= ps;
-            ++pg;
+        const int64_t pg = there ? id : 0;
+        vr_last = vr;
+        kr = raw_rsrc(k_head + pg * k_page + int64_t(slot) * k_row,
+                      rows > 0 ? uint32_t(rows - 1) * k_row + uint32_t(D * 2) : 0u);
+        vr = raw_rsrc(v_head + pg * v_page + int64_t(slot) * v_row,
+                      rows > 0 ? uint32_t(rows - 1) * v_row + uint32_t(D * 2) : 0u);
+        key += kKeys;
+        slot += kKeys;
+#pragma unroll
+        for (int i = 0; i < kKeys / kAttnPage; ++i) {
+            const bool over = slot >= ps;
+            slot -= over ? ps : 0;
+            next_page += over ? 1 : 0;
         }
+        read_page();
     };
-    auto copy_k = [&](int i) {
-        const u32x4 r = resource(i, page, slot, false);
-        const uint32_t at = base + uint32_t((i & 1) * STAGE + w * 16 * RB);
+    auto copy_k = [&](int stage) {
+        const uint32_t at = base + uint32_t(stage * STAGE + w * 16 * RB);
 #pragma unroll
-        for (int c = 0; c < COPIES; ++c) copy_to_lds(r, k_off[c], 0, at + uint32_t(c * 1024));
-        step(page, slot);
+        for (int c = 0; c < COPIES; ++c)
+            copy_to_lds(kr, k_off[c], uint32_t(c * PER) * k_row, at + uint32_t(c * 1024));
     };
-    auto copy_v = [&](int i) {
-        const u32x4 r = resource(i, page_v, slot_v, true);
-        const uint32_t at = base + uint32_t((2 + (i & 1)) * STAGE + w * 16 * RB);
+    auto copy_v = [&](int stage) {
+        const uint32_t at = base + uint32_t((2 + stage) * STAGE + w * 16 * RB);
 #pragma unroll
-        for (int c = 0; c < COPIES; ++c) copy_to_lds(r, v_off[c], 0, at + uint32_t(c * 1024));
-        step(page_v, slot_v);
+        for (int c = 0; c < COPIES; ++c)
+            copy_to_lds(vr_last, v_off[c % V_KINDS], uint32_t(c * PER) * v_row, at + uint32_t(c * 1024));
     };
 
     auto k_frag = [&](int stage, int kt, int kk) {
@@ -182,194 +202,262 @@ k_attend_prompt(const AttnArgs a) {
     auto v_frag = [&](int stage, int s, int dt) {
         const uint32_t off = uint32_t(stage * STAGE + s * 16 * RB);
         const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                      (lds_s16x4 *)(uintptr_t)(v_at[0][dt] + off)));
+                                                      (lds_s16x4 *)(uintptr_t)(v_at[dt] + off)));
         const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                      (lds_s16x4 *)(uintptr_t)(v_at[1][dt] + off)));
+                                                      (lds_s16x4 *)(uintptr_t)(v_at[dt] + off + 8 * RB)));
         return u32x4{x[0], x[1], y[0], y[1]};
     };
 
     const float c2 = a.scale2;
-    f32x16 o[QT][DT];
-    float m[QT], l[QT];
+    f32x16 o[DT];
+    float m, l;
 
-    // the key of a lane's score r of key tile kt of tile i
-    auto key_of = [&](int i, int kt, int r) {
-        return u.key0 + i * kKeys + kt * 32 + 8 * (r / 4) + 4 * h + r % 4;
+    // the key of a lane's score i of key tile kt of tile `at`
+    auto key_of = [&](int at, int kt, int i) {
+        return u.key0 + at * kKeys + kt * 32 + 8 * (i / 4) + 4 * h + i % 4;
     };
-    auto partly = [&](int i) {
-        const int k0 = u.key0 + i * kKeys;
+    auto partly = [&](int at) {
+        const int k0 = u.key0 + at * kKeys;
         return k0 + kKeys - 1 > all_to || k0 < all_from;
     };
-    auto mask = [&](int i, f32x16 (&s)[QT][2]) {
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int key = key_of(i, kt, r);
-                bool there = true;
-                if (bad && key < u.key1) {
-                    const int id = table[key / ps];
-                    there = id >= 0 && id < a.cache.num_pages;
-                }
-#pragma unroll
-                for (int t = 0; t < QT; ++t)
-                    s[t][kt][r] = there && key <= last[t] && key >= first[t] ? s[t][kt][r] : kNone;
+    auto mask = [&](int at, f32x16 (&s)[2]) {
+        each<4>([&](auto sub) {          // 16 keys, which lie in one page
+            const int k0 = u.key0 + at * kKeys + 16 * sub;
+            bool there = true;
+            if (bad && k0 < u.key1) {
+                const int page = load_invariant(table + k0 / ps);
+                there = page >= 0 && page < a.cache.num_pages;
             }
-    };
-    // weights e, e + 1 of the lane's 32 of a row: bf16 pairs in the order of
-    // the second product's right operand
-    auto weigh = [&](const f32x16 (&s)[2], int e, float base_m, float &sum) {
-        const float x = exp2_of(fmaf(s[e / 16][e % 16], c2, -base_m));
-        const float y = exp2_of(fmaf(s[e / 16][e % 16 + 1], c2, -base_m));
-        sum += x + y;
-        return bf16x2_rne(x, y);
-    };
-    auto top_of = [&](const f32x16 (&s)[2]) {
-        float v = kNone;
+            const int to = there ? last : -1;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) v = fmaxf(v, fmaxf(s[0][r], s[1][r]));
-        return over_halves(v, max_of) * c2;
+            for (int i = 8 * (sub % 2); i < 8 * (sub % 2) + 8; ++i) {
+                const int k = key_of(at, sub / 2, i);
+                s[sub / 2][i] = k <= to && k >= first ? s[sub / 2][i] : kNone;
+            }
+        });
     };
-    // M raised to the tile's maximum, the sums brought to it
-    auto raise = [&](int t, float top) {
-        const float now = fmaxf(m[t], ceilf(top));
-        const float f = exp2_of(m[t] - finite_max(now));
-        m[t] = now;
-        l[t] *= f;
+    // weights 2 i, 2 i + 1 of the lane's 32, bf16 in the order of the second
+    // product's right operand; the row's sum is that of the rounded weights
+    auto weigh = [&](const f32x16 (&s)[2], int i, float low) {
+        const float x = exp2_of(fmaf(s[i / 8][i % 8 * 2], c2, -low));
+        const float y = exp2_of(fmaf(s[i / 8][i % 8 * 2 + 1], c2, -low));
+        const uint32_t p = bf16x2_rne(x, y);
+        l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p),
+                                            __builtin_bit_cast(bf16x2, 0x3f803f80u), l, false);
+        return p;
+    };
+    // the largest of a quarter of the lane's scores
+    auto top_of = [&](const f32x16 (&s)[2], int i) {
+        const f32x16 &x = s[i / 2];
+        const int j = i % 2 * 8;
+        float v = largest(x[j], largest(x[j + 1], x[j + 2]));
+        v = largest(v, largest(x[j + 3], x[j + 4]));
+        return largest(largest(v, x[j + 5]), largest(x[j + 6], x[j + 7]));
+    };
+    // M raised to a tile's maximum, the sums brought to it
+    auto raise = [&](float top) {
+        const float now = fmaxf(m, ceilf(top));
+        const float f = exp2_of(m - finite_max(now));
+        m = now;
+        l *= f;
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) o[t][dt] *= f;
+        for (int dt = 0; dt < DT; ++dt) o[dt] *= f;
     };
 
-    auto attend = [&](auto careful_tag) {
-        constexpr bool CAREFUL = decltype(careful_tag)::value;
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            m[t] = kNone;
-            l[t] = 0.f;
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) o[t][dt] = f32x16{};
-        }
-        page = page_v = (u.key0 + 16 * w) / ps;
-        slot = slot_v = (u.key0 + 16 * w) % ps;
-        if (tiles <= 0) return;
-        for (int i = 0; i < tiles; ++i) {
-            copy_k(i);
-            copy_v(i);
-            wait_copies<0>();
-            __syncthreads();
-            f32x16 s[QT][2];
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    const u32x4 f = k_frag(i & 1, kt, kk);
-#pragma unroll
-                    for (int t = 0; t < QT; ++t)
-                        s[t][kt] = mma32(f, q[t][kk], kk ? s[t][kt] : f32x16{});
-                }
-            const bool part = partly(i);
-            if (part) mask(i, s);
-            u32x4 p[QT][4];
-#pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                const float top = top_of(s[t]);
-                if (__any(top > m[t] + kSlack)) raise(t, top);
-                const float b = finite_max(m[t]);
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) p[t][e / 8][e % 8 / 2] = weigh(s[t], e, b, l[t]);
-            }
-#pragma unroll
-            for (int st = 0; st < 4; ++st)
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) {
-                    u32x4 f = v_frag(i & 1, st, dt);
-                    if (CAREFUL && part) {
-#pragma unroll
-                        for (int d = 0; d < 4; ++d) f[d] &= ~odd_mask<uint16_t>(f[d]);
-                    }
-#pragma unroll
-                    for (int t = 0; t < QT; ++t) o[t][dt] = mma32(f, p[t][st], o[t][dt]);
-                }
-            if (CAREFUL && part) {
-                // the values that are not finite, key by key, for the rows that see it
-                for (int at = 0; at < kKeys; ++at) {
-                    const int key = u.key0 + i * kKeys + at;
-                    each<4>([&](auto st) {
-                        if (at / 16 != st) return;
-#pragma unroll
-                        for (int dt = 0; dt < DT; ++dt) {
-                            u32x4 f = v_frag(i & 1, st, dt);
-#pragma unroll
-                            for (int d = 0; d < 4; ++d) {
-                                const int e = 16 * st + 8 * (d / 2) + 4 * h + 2 * (d % 2);
-                                f[d] &= odd_mask<uint16_t>(f[d]) &
-                                        (e == at ? 0xffffu : e + 1 == at ? 0xffff0000u : 0u);
-                            }
-#pragma unroll
-                            for (int t = 0; t < QT; ++t) {
-                                const bool sees = key <= last[t] && key >= first[t];
-                                const f32x16 more = mma32(f, p[t][st], f32x16{});
-#pragma unroll
-                                for (int r = 0; r < 16; ++r) o[t][dt][r] += sees ? more[r] : 0.f;
-                            }
-                        }
-                    });
-                }
-            }
-            __syncthreads();
-        }
+    constexpr int AHEAD = 4, EARLY = 3;              // reads of K and V in flight
+    // Scores of a tile, 12 of the 16 pairs of the last one's weights beside them.
+    auto scores = [&](auto stage, f32x16 (&s)[2], auto &&beside) {
+        u32x4 f[AHEAD];
+        each<AHEAD>([&](auto at) { f[at] = k_frag(stage, at % 2, at / 2); });
+        each<2 * KK>([&](auto at) {
+            constexpr int kt = at % 2, kk = at / 2, next = at + AHEAD;
+            const u32x4 k = f[at % AHEAD];
+            if constexpr (next < 2 * KK) f[at % AHEAD] = k_frag(stage, next % 2, next / 2);
+            s[kt] = mma32(k, q[kk], kk ? s[kt] : f32x16{});
+            beside(at);
+            __builtin_amdgcn_sched_barrier(0);
+        });
     };
-    attend(std::integral_constant<bool, false>{});
+
+    auto begin = [&] {
+        m = kNone;
+        l = 0.f;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) o[dt] = f32x16{};
+        key = u.key0 + 16 * w;
+        slot = key % ps;
+        next_page = key / ps;
+        read_page();
+        form();
+    };
+    constexpr std::integral_constant<int, 0> zero{};
+    constexpr std::integral_constant<int, 1> one{};
+
+    // Tile i: its weights and their products with its values, beside the scores
+    // of tile i + 1 (but for the last).
+    float top = kNone;
+    auto tile = [&](int i, auto stage, auto has_next, f32x16 (&s)[2], f32x16 (&next)[2]) {
+        constexpr std::integral_constant<int, 1 - stage> other;
+        wait_copies<0>();
+        __syncthreads();                 // the copies are there, and tile i - 1 is done with
+        if constexpr (has_next) {
+            copy_v(other);
+            if (i + 2 < tiles) copy_k(stage);
+            form();
+        }
+        top = over_halves(top, max_of) * c2;
+        if (__any(top > m + kSlack)) raise(top);
+        const float low = finite_max(m);
+        u32x4 p[4];
+        auto weights = [&](auto j) {
+            p[j / 4][j % 4] = weigh(s, j, low);
+            here(l);
+        };
+        if constexpr (has_next) {
+            scores(other, next, [&](auto at) {
+                each<12>([&](auto j) {
+                    if constexpr (j * 2 * KK / 12 == at) weights(j);
+                });
+            });
+            if (partly(i + 1)) mask(i + 1, next);
+        } else {
+            each<12>(weights);
+        }
+        constexpr int STEPS = 4 * DT;
+        u32x4 f[EARLY];
+        float tops[4] = {kNone, kNone, kNone, kNone};
+        each<EARLY>([&](auto at) { f[at] = v_frag(stage, at / DT, at % DT); });
+        each<STEPS>([&](auto at) {
+            constexpr int st = at / DT, dt = at % DT, ahead = at + EARLY;
+            const u32x4 v = f[at % EARLY];
+            if constexpr (ahead < STEPS) f[at % EARLY] = v_frag(stage, ahead / DT, ahead % DT);
+            o[dt] = mma32(v, p[st], o[dt]);
+            if constexpr (at < 4) weights(std::integral_constant<int, 12 + at>{});
+            if constexpr (has_next && at % DT == DT - 1) {
+                tops[st] = top_of(next, st);
+                here(tops[st]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        top = largest(largest(tops[0], tops[1]), largest(tops[2], tops[3]));
+    };
+
+    begin();
+    if (tiles > 0) {
+        f32x16 sa[2], sb[2];
+        copy_k(0);
+        form();
+        copy_v(0);
+        wait_copies<0>();
+        __syncthreads();
+        if (tiles > 1) copy_k(1);
+        form();
+        scores(zero, sa, [](auto) {});
+        if (partly(0)) mask(0, sa);
+        top = largest(largest(top_of(sa, 0), top_of(sa, 1)), largest(top_of(sa, 2), top_of(sa, 3)));
+        int i = 0;
+        for (; i + 2 < tiles; i += 2) {
+            tile(i, zero, std::true_type{}, sa, sb);
+            tile(i + 1, one, std::true_type{}, sb, sa);
+        }
+        if (i + 1 < tiles) {
+            tile(i, zero, std::true_type{}, sa, sb);
+            tile(i + 1, one, std::false_type{}, sb, sa);
+        } else {
+            tile(i, zero, std::false_type{}, sa, sb);
+        }
+    }
+
     // Rows that do not see all keys of a tile have a weight of zero for the
-    // others, which is not enough where a value is not finite: then again, with
-    // such values left to the rows that see them.
+    // others, which is not enough where a value is not finite: then all of it
+    // again, step by step, with such values left to the rows that see them.
     bool odd = false;
 #pragma unroll
-    for (int t = 0; t < QT; ++t)
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) odd |= odd_mask<float>(__float_as_uint(o[dt][i])) != 0;
+    if (__syncthreads_or(odd)) {
+        begin();
+        for (int i = 0; i < tiles; ++i) {
+            copy_k(0);
+            form();
+            copy_v(0);
+            wait_copies<0>();
+            __syncthreads();
+            f32x16 s[2];
+            scores(zero, s, [](auto) {});
+            const bool part = partly(i);
+            if (part) mask(i, s);
+            top = largest(largest(top_of(s, 0), top_of(s, 1)), largest(top_of(s, 2), top_of(s, 3)));
+            top = over_halves(top, max_of) * c2;
+            if (__any(top > m + kSlack)) raise(top);
+            const float low = finite_max(m);
+            u32x4 p[4];
+            each<16>([&](auto j) { p[j / 4][j % 4] = weigh(s, j, low); });
+            each<4 * DT>([&](auto at) {
+                u32x4 v = v_frag(0, at / DT, at % DT);
+                if (part) {
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) v[d] &= ~odd_mask<uint16_t>(v[d]);
+                }
+                o[at % DT] = mma32(v, p[at / DT], o[at % DT]);
+            });
+            // the values that are not finite, key by key, for the rows that see it
+            for (int at = part ? 0 : kKeys; at < kKeys; ++at) {
+                const int k = u.key0 + i * kKeys + at;
+                const bool sees = k <= last && k >= first;
+                each<4>([&](auto st) {
+                    if (at / 16 != st) return;
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt) {
+                        u32x4 v = v_frag(0, st, dt);
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            const int e = 16 * st + 8 * (d / 2) + 4 * h + 2 * (d % 2);
+                            v[d] &= odd_mask<uint16_t>(v[d]) &
+                                    (e == at ? 0xffffu : e + 1 == at ? 0xffff0000u : 0u);
+                        }
+                        const f32x16 x = mma32(v, p[st], f32x16{});
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[dt][j] += sees ? x[j] : 0.f;
+                    }
+                });
+            }
+            __syncthreads();
+        }
+    }
+
+    // outputs: a lane has 4 consecutive elements, 8 apart, of its row
+    const float total = over_halves(l, sum_of);
+    const float inv = total == 0.f ? 0.f : 1.0f / total;
+    if (!row) return;
+    if (u.slot >= 0) {
+        const int64_t at = int64_t(u.slot) * kPromptRows + (r - u.row0);
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) odd |= odd_mask<float>(__float_as_uint(o[t][dt][r])) != 0;
-    if (__syncthreads_or(odd)) attend(std::integral_constant<bool, true>{});
-
-    // outputs: a lane has 4 consecutive elements, 8 apart, of its rows
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<f32x4 *>(a.partial + at * DP + dt * 32 + 2 * i + 4 * h) =
+                    f32x4{o[dt][i] * inv, o[dt][i + 1] * inv, o[dt][i + 2] * inv, o[dt][i + 3] * inv};
+        if (h == 0) a.lse[at] = total == 0.f ? kNone : m + log2f(total);
+    } else {
+        uint16_t *out = reinterpret_cast<uint16_t *>(a.o) + int64_t(u.tok0 + tok) * a.ldo +
+                        int64_t(head) * D;
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        const float total = over_halves(l[t], sum_of);
-        const float inv = total == 0.f ? 0.f : 1.0f / total;
-        const int r = wave_row + t * 32 + n;
-        if (r >= u.rows) continue;
-        if (u.slot >= 0) {
-            const int64_t at = int64_t(u.slot) * (kPromptWaves * QT * 32) + (r - u.row0);
+        for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<f32x4 *>(a.partial + at * DP + dt * 32 + 8 * i + 4 * h) =
-                        f32x4{o[t][dt][4 * i] * inv, o[t][dt][4 * i + 1] * inv,
-                              o[t][dt][4 * i + 2] * inv, o[t][dt][4 * i + 3] * inv};
-            if (h == 0) a.lse[at] = total == 0.f ? kNone : m[t] + log2f(total);
-        } else {
-            uint16_t *out = reinterpret_cast<uint16_t *>(a.o) +
-                            int64_t(u.tok0 + r / a.group) * a.ldo +
-                            int64_t(u.kv_head * a.group + r % a.group) * D;
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int d = dt * 32 + 8 * i + 4 * h;
-                    if (d < D)
-                        *reinterpret_cast<u32x2 *>(out + d) =
-                            u32x2{bf16x2_rne(o[t][dt][4 * i] * inv, o[t][dt][4 * i + 1] * inv),
-                                  bf16x2_rne(o[t][dt][4 * i + 2] * inv, o[t][dt][4 * i + 3] * inv)};
-                }
-        }
+            for (int i = 0; i < 16; i += 4) {
+                const int d = dt * 32 + 2 * i + 4 * h;
+                if (d < D)
+                    *reinterpret_cast<u32x2 *>(out + d) =
+                        u32x2{bf16x2_rne(o[dt][i] * inv, o[dt][i + 1] * inv),
+                              bf16x2_rne(o[dt][i + 2] * inv, o[dt][i + 3] * inv)};
+            }
     }
 }
 
 template <int DP> hipError_t prompt_launch(const AttnArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((k_attend_prompt<DP, kPromptRows / (32 * kPromptWaves)>), dim3(a.num_units),
-                       dim3(kPromptThreads), 0, s, a);
+    hipLaunchKernelGGL((k_attend_prompt<DP>), dim3(a.num_units), dim3(kPromptThreads), 0, s, a);
     return hipGetLastError();
 }
 
