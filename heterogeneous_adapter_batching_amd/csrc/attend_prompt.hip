@@ -32,9 +32,10 @@ typedef __attribute__((address_space(3))) uint8_t lds_byte;
 typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kPromptWaves = 4;
+constexpr int kPromptWaves = kPromptRows / 32;
 constexpr int kPromptThreads = kPromptWaves * kWaveSize;
-constexpr int kKeys = 64;                    // keys of a stage: 16 a wave
+constexpr int kKeys = 64;                    // keys of a stage
+constexpr int kShare = kKeys / kPromptWaves; // of them a wave copies, all in one page
 constexpr float kSlack = 8.f;
 
 __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
@@ -81,7 +82,7 @@ k_attend_prompt(const AttnArgs a) {
     constexpr int RB = DP * 2;                        // bytes of a row in LDS
     constexpr int KK = DP / 16, DT = DP / 32;         // steps of a score, tiles of the output
     constexpr int STAGE = kKeys * RB;                 // of K or V
-    constexpr int COPIES = 16 * RB / 1024;            // of a wave's 16 rows
+    constexpr int COPIES = kShare * RB / 1024;        // of a wave's rows
     __shared__ __align__(1024) uint8_t lds[4 * STAGE];   // two of K, two of V
 
     const AttnUnit u = load_invariant(a.units + blockIdx.x);
@@ -131,13 +132,13 @@ k_attend_prompt(const AttnArgs a) {
     const int copy_row = lane * 16 / RB, copy_vec = lane * 16 % RB / 16;
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
-        const int vec = copy_vec ^ k_swizzle<DP>(i * PER + copy_row);
+        const int vec = copy_vec ^ k_swizzle<DP>(w * kShare + i * PER + copy_row);
         k_off[i] = off_or_oob(vec * 8 < D, uint32_t(copy_row) * k_row + uint32_t(vec) * 16u);
         asm volatile("" : "+v"(k_off[i]));   // (kept, not formed again for every tile)
     }
 #pragma unroll
     for (int i = 0; i < V_KINDS; ++i) {
-        const int vec = copy_vec ^ v_swizzle<DP>(i * PER + copy_row);
+        const int vec = copy_vec ^ v_swizzle<DP>(w * kShare + i * PER + copy_row);
         v_off[i] = off_or_oob(vec * 8 < D, uint32_t(copy_row) * v_row + uint32_t(vec) * 16u);
         asm volatile("" : "+v"(v_off[i]));
     }
@@ -154,47 +155,49 @@ k_attend_prompt(const AttnArgs a) {
                                    (j & 1) * 8);
     }
 
-    // The copies of a tile: the wave's 16 keys of K and of V.  What they need
-    // (all of it uniform) is formed a tile ahead, from a page number read two
-    // ahead, between the matrix instructions.
+    // The copies of a tile: the wave's keys of K and of V.  Where they lie is
+    // looked up for 64 tiles at a time, a tile a lane.
     const uint8_t *k_head = a.cache.k + int64_t(u.kv_head) * a.cache.k_head * 2;
     const uint8_t *v_head = a.cache.v + int64_t(u.kv_head) * a.cache.v_head * 2;
-    const int64_t k_page = a.cache.k_page * 2, v_page = a.cache.v_page * 2;
-    const int pages_end = (u.key1 + ps - 1) / ps;     // of the unit's keys
-    int key = 0, slot = 0, next_page = 0, id = 0;     // the tile to be formed, the page read
-    u32x4 kr, vr, vr_last;                            // V is copied a tile behind K
-    auto read_page = [&] { id = load_invariant(table + min(next_page, pages_end - 1)); };
-    auto form = [&] {
-        const bool there = id >= 0 && id < a.cache.num_pages;
-        const int rows = there ? min(16, u.key1 - key) : 0;
-        const int64_t pg = there ? id : 0;
-        vr_last = vr;
-        kr = raw_rsrc(k_head + pg * k_page + int64_t(slot) * k_row,
-                      rows > 0 ? uint32_t(rows - 1) * k_row + uint32_t(D * 2) : 0u);
-        vr = raw_rsrc(v_head + pg * v_page + int64_t(slot) * v_row,
-                      rows > 0 ? uint32_t(rows - 1) * v_row + uint32_t(D * 2) : 0u);
-        key += kKeys;
-        slot += kKeys;
-#pragma unroll
-        for (int i = 0; i < kKeys / kAttnPage; ++i) {
-            const bool over = slot >= ps;
-            slot -= over ? ps : 0;
-            next_page += over ? 1 : 0;
+    uint64_t k_place = 0, v_place = 0;                // 0: no page
+    auto look_up = [&](int i) {
+        const int at = i + lane, key = u.key0 + at * kKeys + w * kShare;
+        k_place = v_place = 0;
+        if (key < u.key1) {
+            const int id = table[key / ps], slot = key % ps;
+            if (id >= 0 && id < a.cache.num_pages) {
+                k_place = reinterpret_cast<uint64_t>(k_head) +
+                          uint64_t(id * a.cache.k_page + slot * a.cache.k_tok) * 2;
+                v_place = reinterpret_cast<uint64_t>(v_head) +
+                          uint64_t(id * a.cache.v_page + slot * a.cache.v_tok) * 2;
+            }
         }
-        read_page();
     };
-    auto copy_k = [&](int stage) {
-        const uint32_t at = base + uint32_t(stage * STAGE + w * 16 * RB);
+    const uint32_t k_bytes = uint32_t(kShare - 1) * k_row + uint32_t(D * 2);
+    const uint32_t v_bytes = uint32_t(kShare - 1) * v_row + uint32_t(D * 2);
+    // tile i's rows of the cache as a buffer; no bytes past the unit's keys
+    auto rows_of = [&](int i, uint64_t place, uint32_t row, uint32_t bytes) {
+        const uint32_t lo = __builtin_amdgcn_readlane(int(uint32_t(place)), i & 63);
+        const uint32_t hi = __builtin_amdgcn_readlane(int(uint32_t(place >> 32)), i & 63);
+        const int over = u.key0 + i * kKeys + (w + 1) * kShare - u.key1;
+        if (over > 0) bytes -= uint32_t(over) * row;
+        return u32x4{lo, hi & 0xffffu, (lo | hi) != 0 && over < kShare ? bytes : 0u,
+                     uint32_t(kRsrcWord3)};
+    };
+    auto copy_k = [&](const u32x4 &r, int stage, int c) {
+        copy_to_lds(r, k_off[c], uint32_t(c * PER) * k_row,
+                    base + uint32_t(stage * STAGE + w * kShare * RB + c * 1024));
+    };
+    auto copy_v = [&](const u32x4 &r, int stage, int c) {
+        copy_to_lds(r, v_off[c % V_KINDS], uint32_t(c * PER) * v_row,
+                    base + uint32_t((2 + stage) * STAGE + w * kShare * RB + c * 1024));
+    };
+    auto copy_all = [&](auto &&copy, const u32x4 &r, int stage) {
 #pragma unroll
-        for (int c = 0; c < COPIES; ++c)
-            copy_to_lds(kr, k_off[c], uint32_t(c * PER) * k_row, at + uint32_t(c * 1024));
+        for (int c = 0; c < COPIES; ++c) copy(r, stage, c);
     };
-    auto copy_v = [&](int stage) {
-        const uint32_t at = base + uint32_t((2 + stage) * STAGE + w * 16 * RB);
-#pragma unroll
-        for (int c = 0; c < COPIES; ++c)
-            copy_to_lds(vr_last, v_off[c % V_KINDS], uint32_t(c * PER) * v_row, at + uint32_t(c * 1024));
-    };
+    auto k_rows = [&](int i) { return rows_of(i, k_place, k_row, k_bytes); };
+    auto v_rows = [&](int i) { return rows_of(i, v_place, v_row, v_bytes); };
 
     auto k_frag = [&](int stage, int kt, int kk) {
         return *(lds_u32x4 *)(uintptr_t)(k_at[kk] + uint32_t(stage * STAGE + kt * 32 * RB));
@@ -284,11 +287,7 @@ k_attend_prompt(const AttnArgs a) {
         l = 0.f;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[dt] = f32x16{};
-        key = u.key0 + 16 * w;
-        slot = key % ps;
-        next_page = key / ps;
-        read_page();
-        form();
+        look_up(0);
     };
     constexpr std::integral_constant<int, 0> zero{};
     constexpr std::integral_constant<int, 1> one{};
@@ -300,10 +299,13 @@ k_attend_prompt(const AttnArgs a) {
         constexpr std::integral_constant<int, 1 - stage> other;
         wait_copies<0>();
         __syncthreads();                 // the copies are there, and tile i - 1 is done with
+        // tile i + 2's keys go where tile i's were, tile i + 1's values where tile
+        // i - 1's were: one copy at a time, between the scores
+        u32x4 kr, vr;
         if constexpr (has_next) {
-            copy_v(other);
-            if (i + 2 < tiles) copy_k(stage);
-            form();
+            vr = v_rows(i + 1);
+            if ((i + 2) % 64 == 0) look_up(i + 2);
+            kr = k_rows(i + 2);
         }
         top = over_halves(top, max_of) * c2;
         if (__any(top > m + kSlack)) raise(top);
@@ -318,6 +320,12 @@ k_attend_prompt(const AttnArgs a) {
                 each<12>([&](auto j) {
                     if constexpr (j * 2 * KK / 12 == at) weights(j);
                 });
+                constexpr int gap = KK / COPIES;
+                if constexpr (at % gap == gap - 1) {
+                    constexpr int c = at / gap;
+                    if constexpr (c < COPIES) copy_v(vr, other, c);
+                    else copy_k(kr, stage, c - COPIES);
+                }
             });
             if (partly(i + 1)) mask(i + 1, next);
         } else {
@@ -345,13 +353,11 @@ k_attend_prompt(const AttnArgs a) {
     begin();
     if (tiles > 0) {
         f32x16 sa[2], sb[2];
-        copy_k(0);
-        form();
-        copy_v(0);
+        copy_all(copy_k, k_rows(0), 0);
+        copy_all(copy_v, v_rows(0), 0);
+        copy_all(copy_k, k_rows(1), 1);
         wait_copies<0>();
         __syncthreads();
-        if (tiles > 1) copy_k(1);
-        form();
         scores(zero, sa, [](auto) {});
         if (partly(0)) mask(0, sa);
         top = largest(largest(top_of(sa, 0), top_of(sa, 1)), largest(top_of(sa, 2), top_of(sa, 3)));
@@ -379,9 +385,9 @@ k_attend_prompt(const AttnArgs a) {
     if (__syncthreads_or(odd)) {
         begin();
         for (int i = 0; i < tiles; ++i) {
-            copy_k(0);
-            form();
-            copy_v(0);
+            if (i && i % 64 == 0) look_up(i);
+            copy_all(copy_k, k_rows(i), 0);
+            copy_all(copy_v, v_rows(i), 0);
             wait_copies<0>();
             __syncthreads();
             f32x16 s[2];
