@@ -149,7 +149,7 @@ int64_t blocks_of(int32_t lo, int32_t hi) {
 
 // Whether a sequence of so many rows is a prompt's.
 bool is_prompt(const attn_plan &p, int64_t rows) {
-    return p.d.dtype == LORA_BF16 && rows > lora::attn_rows_most(p.d.head_dim);
+    return p.d.dtype == LORA_BF16 && rows > lora::attn_rows_most(p.d.dtype, p.d.head_dim);
 }
 
 // fn(sequence, its first token, its rows) for the sequences of one side.
@@ -235,7 +235,7 @@ void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, i
     int64_t few = 0;
     each_seq(*p, false, [&](int32_t, int32_t, int64_t rows) { few = std::max(few, rows); });
     p->rows = Side{};
-    p->rows.tile_rows = few <= 16 ? 16 : few <= 32 ? 32 : lora::attn_rows_most(p->d.head_dim);
+    p->rows.tile_rows = few <= 16 ? 16 : few <= 32 ? 32 : lora::attn_rows_most(p->d.dtype, p->d.head_dim);
     cut(*p, &p->rows, false, kRowsUnits, kRowsKeys);
     p->prompt = Side{};
     p->prompt.tile_rows = lora::kPromptRows;

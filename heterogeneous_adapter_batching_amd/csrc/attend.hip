@@ -344,8 +344,10 @@ template <typename T, int DP, int NQ> hipError_t rows_launch(const AttnArgs &a, 
 }
 template <typename T, int DP> hipError_t rows_dim(int tile_rows, const AttnArgs &a, hipStream_t s) {
     if (tile_rows == 16) return rows_launch<T, DP, 1>(a, s);
-    if (tile_rows == 32) return rows_launch<T, DP, 2>(a, s);
-    if constexpr (DP <= 128) {
+    if constexpr (sizeof(T) == 4) {
+        if (tile_rows == 32) return rows_launch<T, DP, 2>(a, s);
+    }
+    if constexpr (sizeof(T) == 4 && DP <= 128) {
         if (tile_rows == 64) return rows_launch<T, DP, 4>(a, s);
     }
     return hipErrorInvalidValue;

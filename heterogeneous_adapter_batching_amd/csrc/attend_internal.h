@@ -64,10 +64,15 @@ struct AttnArgs {
 };
 
 // What a head is padded to, and the most rows of a tile of the kernel for few
-// rows (single tokens, short chunks, every float32 batch); prompts' have
-// their own kernel.
+// rows: single tokens, and float32 chunks of any length.  bfloat16 chunks have
+// a kernel of their own from 17 rows on (64 sequences of 5 to 8 tokens, 8 key
+// heads of 4 query heads, 2000 keys each: 109 us, the kernel for few rows with
+// tiles of 32 rows 152; of 16 tokens 117 and 231 with tiles of 64; single
+// tokens, 4 rows, of the batch of 128: 163 and 151).
 constexpr int attn_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
-constexpr int attn_rows_most(int head_dim) { return head_dim <= 128 ? 64 : 32; }
+constexpr int attn_rows_most(int dtype, int head_dim) {
+    return dtype == LORA_BF16 ? 16 : head_dim <= 128 ? 64 : 32;
+}
 hipError_t launch_attn_rows(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s);
 constexpr int kPromptRows = 128; // of a tile of prompts
 hipError_t launch_attn_prompt(const AttnArgs &a, hipStream_t s);

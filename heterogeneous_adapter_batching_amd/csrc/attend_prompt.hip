@@ -143,12 +143,14 @@ k_attend_prompt(const AttnArgs a) {
         asm volatile("" : "+v"(v_off[i]));
     }
     const uint32_t base = uint32_t(reinterpret_cast<uintptr_t>((lds_byte *)lds));
-    uint32_t k_at[KK], v_at[DT];
+    // (256 bytes of a row, which is what swizzles reach, in registers)
+    constexpr int K_AT = KK < 8 ? KK : 8, V_AT = DT < 4 ? DT : 4;
+    uint32_t k_at[K_AT], v_at[V_AT];
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk)
+    for (int kk = 0; kk < K_AT; ++kk)
         k_at[kk] = base + uint32_t(n * RB + ((2 * kk + h) ^ k_swizzle<DP>(n)) * 16);
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
+    for (int dt = 0; dt < V_AT; ++dt) {
         const int j = lane & 15, row = 4 * h + j / 4;
         const int vec = 4 * dt + 2 * (lane >> 4 & 1) + (j & 3) / 2;
         v_at[dt] = base + uint32_t(2 * STAGE + row * RB + (vec ^ v_swizzle<DP>(row)) * 16 +
@@ -200,14 +202,15 @@ k_attend_prompt(const AttnArgs a) {
     auto v_rows = [&](int i) { return rows_of(i, v_place, v_row, v_bytes); };
 
     auto k_frag = [&](int stage, int kt, int kk) {
-        return *(lds_u32x4 *)(uintptr_t)(k_at[kk] + uint32_t(stage * STAGE + kt * 32 * RB));
+        return *(lds_u32x4 *)(uintptr_t)(k_at[kk % K_AT] +
+                                         uint32_t(stage * STAGE + kt * 32 * RB + kk / K_AT * 256));
     };
     auto v_frag = [&](int stage, int s, int dt) {
-        const uint32_t off = uint32_t(stage * STAGE + s * 16 * RB);
+        const uint32_t off = v_at[dt % V_AT] + uint32_t(stage * STAGE + s * 16 * RB + dt / V_AT * 256);
         const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                      (lds_s16x4 *)(uintptr_t)(v_at[dt] + off)));
+                                                      (lds_s16x4 *)(uintptr_t)off));
         const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                      (lds_s16x4 *)(uintptr_t)(v_at[dt] + off + 8 * RB)));
+                                                      (lds_s16x4 *)(uintptr_t)(off + 8 * RB)));
         return u32x4{x[0], x[1], y[0], y[1]};
     };
 
@@ -240,14 +243,13 @@ k_attend_prompt(const AttnArgs a) {
         });
     };
     // weights 2 i, 2 i + 1 of the lane's 32, bf16 in the order of the second
-    // product's right operand; the row's sum is that of the rounded weights
+    // product's right operand (the dot product that would sum the pair shares
+    // the matrix cores' way: two additions cost less beside them)
     auto weigh = [&](const f32x16 (&s)[2], int i, float low) {
         const float x = exp2_of(fmaf(s[i / 8][i % 8 * 2], c2, -low));
         const float y = exp2_of(fmaf(s[i / 8][i % 8 * 2 + 1], c2, -low));
-        const uint32_t p = bf16x2_rne(x, y);
-        l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p),
-                                            __builtin_bit_cast(bf16x2, 0x3f803f80u), l, false);
-        return p;
+        l += x + y;
+        return bf16x2_rne(x, y);
     };
     // the largest of a quarter of the lane's scores
     auto top_of = [&](const f32x16 (&s)[2], int i) {
@@ -267,7 +269,9 @@ k_attend_prompt(const AttnArgs a) {
         for (int dt = 0; dt < DT; ++dt) o[dt] *= f;
     };
 
-    constexpr int AHEAD = 4, EARLY = 3;              // reads of K and V in flight
+    // reads of K and V in flight (heads of 256: one more spills registers into
+    // the loop, four prompts of 4096 1260 us against 1044)
+    constexpr int AHEAD = DP == 256 ? 3 : 4, EARLY = DP == 256 ? 2 : 3;
     // Scores of a tile, 12 of the 16 pairs of the last one's weights beside them.
     auto scores = [&](auto stage, f32x16 (&s)[2], auto &&beside) {
         u32x4 f[AHEAD];
@@ -377,12 +381,12 @@ k_attend_prompt(const AttnArgs a) {
     // Rows that do not see all keys of a tile have a weight of zero for the
     // others, which is not enough where a value is not finite: then all of it
     // again, step by step, with such values left to the rows that see them.
-    bool odd = false;
+    float odd = 0.f;                     // (NaN where a sum is not finite)
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) odd |= odd_mask<float>(__float_as_uint(o[dt][i])) != 0;
-    if (__syncthreads_or(odd)) {
+        for (int i = 0; i < 16; ++i) odd = fmaf(o[dt][i], 0.f, odd);
+    if (__syncthreads_or(odd != 0.f)) {
         begin();
         for (int i = 0; i < tiles; ++i) {
             if (i && i % 64 == 0) look_up(i);
