@@ -47,8 +47,10 @@ class AttentionPlan:
         self.lib = load()
         self._h = ctypes.c_void_p()
         self.ws = None
-        self.dtype_name = dtype
         self.heads, self.kv_heads, self.head_dim, self.page_size = heads, kv_heads, head_dim, page_size
+        self.page_shape = (kv_heads, page_size, head_dim)
+        if torch:
+            self.dtype = _torch_dtype(dtype)
         self.desc = AttnDesc(_DTYPES[dtype], _i32(heads, "heads"), _i32(kv_heads, "kv_heads"),
                              _i32(head_dim, "head_dim"), _i32(page_size, "page_size"),
                              int(bool(causal)), _i32(window, "window"), _i32(max_kv, "max_kv"))
@@ -84,10 +86,6 @@ class AttentionPlan:
     def handle(self):
         return self._h
 
-    @property
-    def dtype(self):
-        return _torch_dtype(self.dtype_name)
-
     def workspace_bytes(self) -> int:
         return int(self.lib.attn_plan_workspace_bytes(self._h))
 
@@ -107,7 +105,7 @@ class AttentionPlan:
         elif not ws.is_cuda or not ws.is_contiguous():
             raise ValueError("ws must be a contiguous CUDA tensor")
         _enqueue(self.lib.attn_plan_upload, (self._h, ws.data_ptr(), ws.nbytes), ws.device, stream)
-        self.ws = ws
+        self.ws, self.device = ws, ws.device
         return self
 
 
@@ -131,55 +129,97 @@ def rotary_frequencies(rotary_dim, *, base=10000.0, scaling="none", factor=1.0, 
     return torch.from_numpy(f).to(device) if device is not None else torch.from_numpy(f)
 
 
-def _plan_device(plan):
-    if plan.ws is None:
-        return None                          # the library refuses the plan
-    return plan.ws.device
+def _plan_device(plan, t):
+    """The device of a call: the plan's (one that was not uploaded is refused
+    by the library)."""
+    if plan.ws is not None:
+        return plan.device
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("q, k and v must be CUDA tensors")
+    return t.device
 
 
 def _heads(t, name, plan, heads, device):
-    """A matrix of the plan's tokens (and rows past them)."""
-    p, ld = _matrix(t, name, None, plan.dtype, device)
-    rows, cols = t.shape
-    if cols != heads * plan.head_dim or rows < plan.num_tokens:
-        raise ValueError(f"{name} must be [{plan.num_tokens} or more][{heads * plan.head_dim}], "
-                         f"got {list(t.shape)}")
-    return p, ld
+    """A matrix of the plan's tokens (and rows past them): pointer, stride."""
+    if t.__class__ is not torch.Tensor and not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device != device or t.dtype != plan.dtype:
+        _matrix(t, name, None, plan.dtype, device)
+        raise TypeError(f"{name} must be a CUDA tensor")
+    width = heads * plan.head_dim
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width or shape[0] < plan.num_tokens:
+        raise ValueError(f"{name} must be [{plan.num_tokens} or more][{width}], got {list(shape)}")
+    ld, step = t.stride()
+    if step != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    return t.data_ptr(), (ld if shape[0] > 1 else width)
 
 
 def _pages_of(t, name, plan, device):
-    """A cache's pointer and its page, head and token strides."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    """A cache's shape and its page, head and token strides."""
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != plan.dtype:
-        raise TypeError(f"{name} must be {plan.dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dim() != 4 or t.shape[1:] != (plan.kv_heads, plan.page_size, plan.head_dim):
-        raise ValueError(f"{name} must be [pages][{plan.kv_heads}][{plan.page_size}]"
-                         f"[{plan.head_dim}], got {list(t.shape)}")
+    if t.dtype != plan.dtype:
+        raise TypeError(f"{name} must be {plan.dtype}, got {t.dtype}")
+    shape = t.shape
+    if shape[1:] != plan.page_shape:
+        raise ValueError(f"{name} must be [pages]{list(plan.page_shape)}, got {list(shape)}")
     page, head, tok, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: a token's elements must be contiguous")
-    return (t.data_ptr(), 0 if t.shape[0] == 1 else page, 0 if plan.kv_heads == 1 else head, tok)
+    # (a dimension of one has any stride)
+    return shape[0], 0 if shape[0] == 1 else page, 0 if shape[1] == 1 else head, tok
+
+
+# (one descriptor per distinct set of values, as the library only reads them)
+@functools.lru_cache(maxsize=1024)
+def _kv_desc(k, v, num_pages, *strides):
+    return ctypes.byref(KvCache(k, v, *strides, _i32(num_pages, "pages")))
 
 
 def _cache(plan, k_cache, v_cache, pages, device):
     """The library's arguments of a cache and its page table."""
-    k, v = _pages_of(k_cache, "k_cache", plan, device), _pages_of(v_cache, "v_cache", plan, device)
-    if k_cache.shape[0] != v_cache.shape[0]:
+    n, *ks = _pages_of(k_cache, "k_cache", plan, device)
+    nv, *vs = _pages_of(v_cache, "v_cache", plan, device)
+    if n != nv:
         raise ValueError("k_cache and v_cache must have the same pages")
-    if not isinstance(pages, torch.Tensor) or not pages.is_cuda or pages.dtype != torch.int32:
+    if not isinstance(pages, torch.Tensor) or pages.dtype != torch.int32:
         raise TypeError("pages must be an int32 CUDA tensor")
     if pages.device != device:
         raise ValueError(f"pages is on {pages.device}, not on {device}")
-    if pages.dim() != 2 or pages.shape[0] < plan.num_seqs or \
-            (pages.shape[1] > 1 and pages.stride(1) != 1):
-        raise ValueError(f"pages must be [{plan.num_seqs} or more][pages of a sequence] with "
-                         f"contiguous rows, got {list(pages.shape)}")
-    ld = pages.stride(0) if pages.shape[0] > 1 else pages.shape[1]
-    desc = KvCache(k[0], v[0], *k[1:], *v[1:], _i32(k_cache.shape[0], "pages"))
-    return (ctypes.byref(desc), pages.data_ptr(), ld, _i32(pages.shape[1], "pages of a sequence"))
+    shape = pages.shape
+    if len(shape) != 2 or shape[0] < plan.num_seqs:
+        raise ValueError(f"pages must be [{plan.num_seqs} or more][pages of a sequence], got "
+                         f"{list(shape)}")
+    ld, step = pages.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError("pages must have contiguous rows")
+    return (_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), n, *ks, *vs), pages.data_ptr(),
+            ld if shape[0] > 1 else shape[1], _i32(shape[1], "pages of a sequence"))
+
+
+def _vector(t, name, dtype, least, device):
+    """A contiguous vector's pointer."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != 1 or t.shape[0] < least or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {least} or more")
+    return t.data_ptr()
+
+
+def _padded(q, plan, device, stream):
+    """A tensor like q for a call's results; rows past the plan's tokens are
+    zeros."""
+    t = _new(q.shape, q.dtype, device, stream)
+    if q.shape[0] > plan.num_tokens:
+        with torch.cuda.stream(stream):
+            t[plan.num_tokens:].zero_()
+    return t
 
 
 def paged_attention(plan, q, k_cache, v_cache, pages, *, scale=None, o=None, stream=None):
@@ -196,14 +236,11 @@ def paged_attention(plan, q, k_cache, v_cache, pages, *, scale=None, o=None, str
     head_dim^-0.5.  What a token does not see does not reach it, also where it
     is infinite or NaN; a page outside the cache counts as absent.  Calls that
     share a plan's workspace must not overlap.  Inference only.  Returns o."""
-    device = _plan_device(plan) or q.device
+    device = _plan_device(plan, q)
     qp, ldq = _heads(q, "q", plan, plan.heads, device)
     scale = plan.head_dim ** -0.5 if scale is None else float(scale)
     if o is None:
-        o = _new(q.shape, q.dtype, device, stream)
-        if q.shape[0] > plan.num_tokens:
-            with torch.cuda.stream(stream):
-                o[plan.num_tokens:].zero_()
+        o = _padded(q, plan, device, stream)
     op, ldo = _heads(o, "o", plan, plan.heads, device)
     _enqueue(plan.lib.paged_attention,
              (plan.handle, qp, ldq, *_cache(plan, k_cache, v_cache, pages, device), scale, op, ldo),
@@ -227,42 +264,30 @@ def rotary_append(plan, q, k, v, k_cache, v_cache, pages, freqs, *, layout="half
     among their keys.  q may be None (an encoder's keys and values), or k, v,
     both caches and pages together (queries alone).  Other arguments as
     paged_attention."""
-    device = _plan_device(plan) or (k if q is None else q).device
-    qp = ldq = op = ldo = kp = ldk = vp = ldv = pp = fp = 0
+    if q is None and k is None:
+        raise ValueError("neither q nor k")
+    device = _plan_device(plan, k if q is None else q)
+    qp = ldq = op = ldo = kp = ldk = vp = ldv = pp = fp = n = 0
     if q is not None:
         qp, ldq = _heads(q, "q", plan, plan.heads, device)
         if q_out is None:
-            q_out = _new(q.shape, q.dtype, device, stream)
-            if q.shape[0] > plan.num_tokens:
-                with torch.cuda.stream(stream):
-                    q_out[plan.num_tokens:].zero_()
+            q_out = _padded(q, plan, device, stream)
         op, ldo = _heads(q_out, "q_out", plan, plan.heads, device)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    absent = [t is None for t in (k, v, k_cache, v_cache, pages)]
-    if all(absent):
-        cache = (None, 0, 0, 0)
-    elif any(absent):
-        raise ValueError("k, v, k_cache, v_cache and pages are given together or not at all")
-    else:
+    absent = (k is None) + (v is None) + (k_cache is None) + (v_cache is None) + (pages is None)
+    if absent == 0:
         kp, ldk = _heads(k, "k", plan, plan.kv_heads, device)
         vp, ldv = _heads(v, "v", plan, plan.kv_heads, device)
         cache = _cache(plan, k_cache, v_cache, pages, device)
-    for t, name, dtype, rows in ((positions, "positions", torch.int32, plan.num_tokens),
-                                 (freqs, "freqs", torch.float64, 1)):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
-            raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-        if t.dim() != 1 or t.shape[0] < rows or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous vector of {rows} or more")
+    elif absent == 5:
+        cache = (None, 0, 0, 0)
+    else:
+        raise ValueError("k, v, k_cache, v_cache and pages are given together or not at all")
     if positions is not None:
-        pp = positions.data_ptr()
-    n = 0
+        pp = _vector(positions, "positions", torch.int32, plan.num_tokens, device)
     if freqs is not None:
-        fp, n = freqs.data_ptr(), freqs.shape[0]
+        fp, n = _vector(freqs, "freqs", torch.float64, 1, device), freqs.shape[0]
     desc = _rotary_desc(2 * n, layout, ctypes.c_float(magnitude).value)
     _enqueue(plan.lib.rotary_append,
              (plan.handle, desc, qp, ldq, op, ldo, kp, ldk, vp, ldv, *cache, pp, fp), device, stream)

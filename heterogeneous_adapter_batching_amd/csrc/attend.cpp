@@ -36,6 +36,7 @@ constexpr int32_t kMostTokens = 1 << 23, kMostKeys = 1 << 30;
 // fewest keys of a part.
 constexpr int kRowsUnits = 1024, kRowsKeys = 256;
 constexpr int kPromptUnits = 512, kPromptKeys = 512;
+constexpr int kCus = 256;
 
 // One kernel's share of a plan: its tiles of rows, and their keys in parts.
 struct Side {
@@ -204,11 +205,15 @@ void cut(const attn_plan &p, Side *side, bool prompt, int64_t target, int64_t le
             if (parts > 1) slot += int32_t(parts * p.d.kv_heads);
         }
     });
-    // the longest parts first: the short ones fill the end
-    if (prompt)
-        std::stable_sort(side->units.begin(), side->units.end(), [](const AttnUnit &a, const AttnUnit &b) {
-            return a.key1 - a.key0 > b.key1 - b.key0;
-        });
+    // the longest parts first, for the short ones to fill the end (sorted by
+    // counting: no part has more than `part` blocks)
+    std::vector<int64_t> at(size_t(part) + 2, 0);
+    const auto rank = [&](const AttnUnit &u) { return size_t(part - blocks_of(u.key0, u.key1)); };
+    for (const AttnUnit &u : side->units) ++at[rank(u) + 1];
+    for (size_t i = 1; i < at.size(); ++i) at[i] += at[i - 1];
+    std::vector<AttnUnit> sorted(side->units.size());
+    for (const AttnUnit &u : side->units) sorted[size_t(at[rank(u)]++)] = u;
+    side->units.swap(sorted);
     side->cap_units = int64_t(side->units.size());
     side->cap_joins = int64_t(side->joins.size());
     side->cap_slots = slot;
@@ -235,7 +240,15 @@ void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, i
     int64_t few = 0;
     each_seq(*p, false, [&](int32_t, int32_t, int64_t rows) { few = std::max(few, rows); });
     p->rows = Side{};
+    // (float32 chunks: large tiles read keys less often, small ones use more of
+    // the chip)
     p->rows.tile_rows = few <= 16 ? 16 : few <= 32 ? 32 : lora::attn_rows_most(p->d.dtype, p->d.head_dim);
+    auto tiles = [&](int32_t rows_a_tile) {
+        int64_t n = 0;
+        each_seq(*p, false, [&](int32_t, int32_t, int64_t rows) { n += (rows + rows_a_tile - 1) / rows_a_tile; });
+        return n * p->d.kv_heads;
+    };
+    while (p->rows.tile_rows > 16 && tiles(p->rows.tile_rows) < kCus) p->rows.tile_rows /= 2;
     cut(*p, &p->rows, false, kRowsUnits, kRowsKeys);
     p->prompt = Side{};
     p->prompt.tile_rows = lora::kPromptRows;

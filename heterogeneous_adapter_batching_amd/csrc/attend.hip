@@ -24,8 +24,10 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWaveSize;
 
+template <typename T> constexpr int dtype_of = sizeof(T) == 2 ? LORA_BF16 : LORA_F32;
+
 template <typename T, int DP, int NQ>
-__global__ __launch_bounds__(kThreads) void k_attend_rows(const AttnArgs a) {
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void k_attend_rows(const AttnArgs a) {
     constexpr int E = Elem<T>::E;                     // elements of 16 bytes
     constexpr int KS = DP / (4 * E);                  // matrix steps of a score
     constexpr int KT = E / 4;                         // 16-key tiles of a matrix step over keys
@@ -34,6 +36,10 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttnArgs a) {
     constexpr int VC = DP / (16 * VW);                // and its vectors of a key
     constexpr int VD = VW * int(sizeof(T)) / 4;       // words of such a vector
     constexpr int LD = DP + 4;
+    // Tiles that hold all of a sequence's rows read its keys once: past the L2.
+    // (128 sequences of 19 to 7824 keys, 730 MB: 123 us against 139; four of
+    // 68157 to 127138, 1.7 GB: 260 against 298, 6.6 TB/s.)
+    constexpr int POLICY = NQ * 16 < attn_rows_most(dtype_of<T>, DP) || NQ == 1 ? kNT : 0;
     __shared__ float so[kWaves][16][LD];
     __shared__ float sm[kWaves][16], sl[kWaves][16];
 
@@ -80,53 +86,66 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttnArgs a) {
             for (int j = 0; j < VW; ++j) o[t][c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    PageWalk walk(a, u.seq, u.key0 + w * BK);
-    const uint32_t k_row = uint32_t(a.cache.k_tok) * es, v_row = uint32_t(a.cache.v_tok) * es;
-    for (int b = u.key0 + w * BK; b < u.key1; b += kWaves * BK) {
-        // this wave's keys b .. b + BK - 1
+    // A wave takes every kWaves-th run of BK keys.
+    struct Keys {
         u32x4 k[KT][KS];
         uint32_t v[4 * KT][VC][VD];
         bool there[KT];
-        rsrc_t vr[KT];
+    };
+    PageWalk walk(a, u.seq, u.key0 + w * BK);
+    const uint32_t k_row = uint32_t(a.cache.k_tok) * es, v_row = uint32_t(a.cache.v_tok) * es;
+    uint32_t k_off[KS], v_off[VC];
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk)
+        k_off[kk] = off_or_oob((kk * 4 + g) * E < D, uint32_t(n) * k_row + uint32_t(kk * 4 + g) * 16u);
+#pragma unroll
+    for (int c = 0; c < VC; ++c)
+        v_off[c] = off_or_oob((c * 16 + n) * VW < D,
+                              uint32_t(4 * g) * v_row + uint32_t((c * 16 + n) * VW * es));
+    auto load16 = [](rsrc_t r, uint32_t off, uint32_t at) {
+        return __builtin_amdgcn_raw_buffer_load_b128(r, int(off), int(at), POLICY);
+    };
+    auto load = [&](int b, Keys &x) {
 #pragma unroll
         for (int tt = 0; tt < KT; ++tt) {
             const int key = b + 16 * tt;
             const int page = key < u.key1 ? load_invariant(walk.row + walk.page) : -1;
-            there[tt] = page >= 0 && page < a.cache.num_pages;
-            const int64_t at = there[tt] ? page : 0;
+            x.there[tt] = page >= 0 && page < a.cache.num_pages;
+            const int64_t at = x.there[tt] ? page : 0;
             const uint8_t *kp = a.cache.k + (at * a.cache.k_page + int64_t(u.kv_head) * a.cache.k_head +
                                              int64_t(walk.slot) * a.cache.k_tok) * es;
             const uint8_t *vp = a.cache.v + (at * a.cache.v_page + int64_t(u.kv_head) * a.cache.v_head +
                                              int64_t(walk.slot) * a.cache.v_tok) * es;
             // the tile's rows that are keys of the unit
-            const int rows = there[tt] ? min(16, u.key1 - key) : 0;
+            const int rows = x.there[tt] ? min(16, u.key1 - key) : 0;
             const rsrc_t kr = make_rsrc(kp, rows ? uint32_t(rows - 1) * k_row + uint32_t(D * es) : 0u);
-            vr[tt] = make_rsrc(vp, rows ? uint32_t(rows - 1) * v_row + uint32_t(D * es) : 0u);
+            const rsrc_t vr = make_rsrc(vp, rows ? uint32_t(rows - 1) * v_row + uint32_t(D * es) : 0u);
+            // (rows past the last are past the buffer's end)
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
-                k[tt][kk] = bload16(kr, off_or_oob(n < rows && (kk * 4 + g) * E < D,
-                                                   uint32_t(n) * k_row + uint32_t(kk * 4 + g) * 16u));
+            for (int kk = 0; kk < KS; ++kk) x.k[tt][kk] = load16(kr, k_off[kk], 0);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int c = 0; c < VC; ++c) {
-                    const uint32_t off = off_or_oob(
-                        4 * g + i < rows && (c * 16 + n) * VW < D,
-                        uint32_t(4 * g + i) * v_row + uint32_t((c * 16 + n) * VW * es));
+                    const uint32_t off = v_off[c], at_row = uint32_t(i) * v_row;
                     if constexpr (VD == 4) {
-                        const u32x4 x = bload16(vr[tt], off);
+                        const u32x4 y = load16(vr, off, at_row);
 #pragma unroll
-                        for (int d = 0; d < 4; ++d) v[tt * 4 + i][c][d] = x[d];
+                        for (int d = 0; d < 4; ++d) x.v[tt * 4 + i][c][d] = y[d];
                     } else {
-                        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(vr[tt], int(off), 0, 0);
-                        v[tt * 4 + i][c][0] = x[0];
-                        v[tt * 4 + i][c][1] = x[1];
+                        const u32x2 y = __builtin_amdgcn_raw_buffer_load_b64(vr, int(off), int(at_row), POLICY);
+                        x.v[tt * 4 + i][c][0] = y[0];
+                        x.v[tt * 4 + i][c][1] = y[1];
                     }
                 }
             walk.skip(16);
         }
         walk.skip((kWaves - 1) * BK);
-
+    };
+    auto attend = [&](int b, const Keys &x) {
+        const auto &k = x.k;
+        const auto &v = x.v;
+        const auto &there = x.there;
         // V^T: element j of vector c of the lane's keys
         auto vt = [&](int c, int j) {
             u32x4 r;
@@ -234,6 +253,11 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttnArgs a) {
                 }
             }
         }
+    };
+    for (int b = u.key0 + w * BK; b < u.key1; b += kWaves * BK) {
+        Keys x;
+        load(b, x);
+        attend(b, x);
     }
 
     // The waves' parts meet in LDS, 16 rows at a time.
@@ -295,32 +319,62 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttnArgs a) {
 }
 
 // The parts of a tile's keys joined: o = sum_i 2^(lse_i - M) o_i / sum_i
-// 2^(lse_i - M), 16 rows a workgroup.
-template <typename T, int DP>
+// 2^(lse_i - M).  16 / WAYS rows a workgroup, a row's parts dealt to WAYS groups
+// of 16 threads: a few rows in many parts (single tokens behind long contexts:
+// 32 parts of 4 rows took 18 us with one way, 6 with 16) or many in a few.
+template <typename T, int DP, int WAYS>
 __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a, int tile_rows) {
-    constexpr int OW = DP / 16;
+    constexpr int OW = DP / 16, ROWS = 16 / WAYS;
+    __shared__ float tops[16], totals[WAYS > 1 ? 16 : 1], sums[WAYS > 1 ? 16 : 1][DP + 4];
     const AttnJoin j = load_invariant(a.joins + blockIdx.x);
-    const int row = int(blockIdx.y) * 16 + (threadIdx.x >> 4), col = (threadIdx.x & 15) * OW;
-    const int rr = j.row0 + row;
-    if (row >= tile_rows || rr >= j.rows || j.slots <= 0 || col >= a.head_dim) return;
+    if (j.slots <= 0 || j.row0 + int(blockIdx.y) * ROWS >= j.rows) return;
+    const int group = threadIdx.x >> 4, way = group % WAYS, col = (threadIdx.x & 15) * OW;
+    const int row = int(blockIdx.y) * ROWS + group / WAYS, rr = j.row0 + row;
+    const bool ok = row < tile_rows && rr < j.rows;
     const float *lse = a.lse + int64_t(j.slot0) * tile_rows + row;
     const float *part = a.partial + (int64_t(j.slot0) * tile_rows + row) * DP + col;
     float top = kNone;
-    for (int i = 0; i < j.slots; ++i) top = fmaxf(top, lse[int64_t(i) * tile_rows]);
+    if (ok)
+        for (int i = way; i < j.slots; i += WAYS) top = fmaxf(top, lse[int64_t(i) * tile_rows]);
+    if constexpr (WAYS > 1) {
+        tops[group] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WAYS; ++i) top = fmaxf(top, tops[group / WAYS * WAYS + i]);
+    }
     top = finite_max(top);
     float total = 0.f, r[OW] = {};
+    if (ok && col < a.head_dim) {
 #pragma unroll 4
-    for (int i = 0; i < j.slots; ++i) {
-        const float f = exp2_of(lse[int64_t(i) * tile_rows] - top);
-        const float *p = part + int64_t(i) * tile_rows * DP;
-        total += f;
+        for (int i = way; i < j.slots; i += WAYS) {
+            const float f = exp2_of(lse[int64_t(i) * tile_rows] - top);
+            const float *p = part + int64_t(i) * tile_rows * DP;
+            total += f;
 #pragma unroll
-        for (int e = 0; e < OW; e += 4) {
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(p + e);
+            for (int e = 0; e < OW; e += 4) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(p + e);
 #pragma unroll
-            for (int d = 0; d < 4; ++d) r[e + d] += f * x[d];
+                for (int d = 0; d < 4; ++d) r[e + d] += f * x[d];
+            }
         }
     }
+    if constexpr (WAYS > 1) {
+        if (col == 0) totals[group] = total;
+#pragma unroll
+        for (int e = 0; e < OW; ++e) sums[group][col + e] = r[e];
+        __syncthreads();
+        if (way) return;
+        total = 0.f;
+#pragma unroll
+        for (int e = 0; e < OW; ++e) r[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < WAYS; ++i) {
+            total += totals[group + i];
+#pragma unroll
+            for (int e = 0; e < OW; ++e) r[e] += sums[group + i][col + e];
+        }
+    }
+    if (!ok || col >= a.head_dim) return;
     const float inv = total == 0.f ? 0.f : 1.0f / total;
 #pragma unroll
     for (int e = 0; e < OW; ++e) r[e] *= inv;
@@ -359,14 +413,22 @@ template <typename T> hipError_t rows_types(int tile_rows, const AttnArgs &a, hi
         default: return rows_dim<T, 256>(tile_rows, a, s);
     }
 }
-template <typename T> hipError_t join_types(int tile_rows, const AttnArgs &a, hipStream_t s) {
-    const dim3 grid(a.num_joins, (tile_rows + 15) / 16), block(256);
-    switch (attn_dim(a.head_dim)) {
-        case 64: hipLaunchKernelGGL((k_attend_join<T, 64>), grid, block, 0, s, a, tile_rows); break;
-        case 128: hipLaunchKernelGGL((k_attend_join<T, 128>), grid, block, 0, s, a, tile_rows); break;
-        default: hipLaunchKernelGGL((k_attend_join<T, 256>), grid, block, 0, s, a, tile_rows);
-    }
+template <typename T, int DP> hipError_t join_launch(int tile_rows, const AttnArgs &a, hipStream_t s) {
+    const dim3 block(256);
+    if (tile_rows <= 16)
+        hipLaunchKernelGGL((k_attend_join<T, DP, 16>), dim3(a.num_joins, tile_rows), block, 0, s, a,
+                           tile_rows);
+    else
+        hipLaunchKernelGGL((k_attend_join<T, DP, 1>), dim3(a.num_joins, (tile_rows + 15) / 16), block,
+                           0, s, a, tile_rows);
     return hipGetLastError();
+}
+template <typename T> hipError_t join_types(int tile_rows, const AttnArgs &a, hipStream_t s) {
+    switch (attn_dim(a.head_dim)) {
+        case 64: return join_launch<T, 64>(tile_rows, a, s);
+        case 128: return join_launch<T, 128>(tile_rows, a, s);
+        default: return join_launch<T, 256>(tile_rows, a, s);
+    }
 }
 
 }  // namespace
