@@ -122,7 +122,7 @@ def rotary_frequencies(rotary_dim, *, base=10000.0, scaling="none", factor=1.0, 
     scaling "linear" divides them by factor; "by_parts" leaves pairs that make
     at least `high` turns in original_length positions, divides those of at
     most `low`, and blends between them."""
-    f = np.empty(max(_i32(rotary_dim, "rotary_dim"), 2) // 2, np.float64)
+    f = np.empty(min(max(_i32(rotary_dim, "rotary_dim"), 2), 256) // 2, np.float64)
     check(load().rotary_frequencies(
         f.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), rotary_dim, base,
         _code(ROTARY_SCALINGS, scaling, "scaling"), factor, original_length, low, high))

@@ -33,7 +33,10 @@ uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 constexpr int32_t kMostTokens = 1 << 23, kMostKeys = 1 << 30;
 
 // Units a launch aims for when it cuts the tiles' keys into parts, and the
-// fewest keys of a part.
+// fewest keys of a part.  The kernel for few rows has two workgroups a CU, the
+// prompts' too: a round, or two of them (four sequences behind 68157 to 127138
+// keys, us: 512 parts 383, 768 324, 1024 299, 1536 324, 2048 302; 128 sequences
+// of 19 to 7824 keys 144, 137, 141, 140, 141).
 constexpr int kRowsUnits = 1024, kRowsKeys = 256;
 constexpr int kPromptUnits = 512, kPromptKeys = 512;
 constexpr int kCus = 256;
@@ -170,16 +173,18 @@ void cut(const attn_plan &p, Side *side, bool prompt, int64_t target, int64_t le
     side->units.clear();
     side->joins.clear();
     side->tiles = 0;
-    int64_t total = 0;
+    int64_t total = 0, longest = 0;
     each_seq(p, prompt, [&](int32_t s, int32_t, int64_t rows) {
         for (int64_t r = 0; r < rows; r += side->tile_rows) {
             int32_t lo, hi;
             tile_keys(p, s, r, std::min<int64_t>(rows, r + side->tile_rows), &lo, &hi);
             total += blocks_of(lo, hi) * p.d.kv_heads;
+            longest = std::max(longest, blocks_of(lo, hi));
             side->tiles += p.d.kv_heads;
         }
     });
-    const int64_t part = std::max(least / lora::kAttnBlock, (total + target - 1) / target);
+    const int64_t low = least / lora::kAttnBlock;
+    const int64_t part = std::min(std::max(low, (total + target - 1) / target), std::max(longest, low));
     int32_t slot = 0;
     each_seq(p, prompt, [&](int32_t s, int32_t tok0, int64_t rows) {
         for (int64_t r = 0; r < rows; r += side->tile_rows) {
@@ -218,12 +223,14 @@ void cut(const attn_plan &p, Side *side, bool prompt, int64_t target, int64_t le
     side->cap_joins = int64_t(side->joins.size());
     side->cap_slots = slot;
     if (p.d.max_kv) {
-        // room for any lengths up to max_kv, so that the launches stay the same
+        // Room for any lengths up to max_kv, so that the launches stay the same.
+        // Parts are at least total / target blocks long, so that fewer than
+        // `target` tiles are cut, into at most twice as many parts.
         const int64_t most = (int64_t(p.d.max_kv) + lora::kAttnBlock - 1) / lora::kAttnBlock;
-        const int64_t low = least / lora::kAttnBlock, each = std::max<int64_t>(1, (most + low - 1) / low);
+        const int64_t each = std::max<int64_t>(1, (most + low - 1) / low);
         side->cap_units = std::min(side->tiles * each, side->tiles + target);
-        side->cap_joins = each > 1 ? side->tiles : 0;
-        side->cap_slots = each > 1 ? side->cap_units : 0;
+        side->cap_joins = each > 1 ? std::min(side->tiles, target) : 0;
+        side->cap_slots = each > 1 ? std::min(side->tiles * each, 2 * target) : 0;
     }
 }
 
@@ -409,9 +416,9 @@ lora_status attn_plan_rebuild(attn_plan *p, const int32_t *new_lens, const int32
     if (!p) return set_errorf(LORA_EINVAL, "null plan");
     const lora_status st = check_lens(p->d, new_lens, kv_lens, num_seqs);
     if (st != LORA_OK) return st;
+    p->ws = nullptr;                       // its tables are the last batch's
     return guarded([&] {
         plan_build(p, new_lens, kv_lens, num_seqs);
-        p->ws = nullptr;                   // its tables are the last batch's
         return LORA_OK;
     });
 }
