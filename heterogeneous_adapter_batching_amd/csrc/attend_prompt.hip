@@ -3,19 +3,32 @@
 //
 // The mathematics and the orientation of the products are attend.hip's; here
 // the matrix cores bound them, so keys and values go through LDS, 64 of each a
-// stage by direct copies, and a wave keeps QT x 32 rows' queries and sums in
-// registers.  One pass runs three steps of three tiles side by side, which do
-// not depend on each other: the scores of tile i + 1, the weights of tile i,
-// the products of tile i - 1 with its values.  So the vector units' work (an
-// exponential for every 4 head_dim operations of the matrix cores) goes on
-// under the matrix instructions of one and the same wave.
+// stage by direct copies, two stages of each, and a wave keeps 32 rows' queries
+// and sums in registers.  The scores of tile i + 1 do not depend on tile i's
+// weights, so they are formed beside one another: every matrix instruction has
+// a few of the vector units' behind it (an exponential, the scaling, the sum
+// and half a conversion for each 4 head_dim operations of the matrix cores),
+// the reads of a later one's operand, and now and then a copy for the tile after
+// next.  Four waves are a workgroup and two workgroups a CU.
 //
-// Weights are 2^(c s - M) with an integer M per row at least as large as the
-// largest c s when it was set.  They are formed with the M of before, while
-// their own tile's maximum is still being formed beside them; only where that
-// exceeds M by more than kSlack (seldom, after the first tile) M is raised and
-// the tile's weights are formed again.  2^kSlack of headroom costs nothing: the
-// sums are float32 and the weights bfloat16, whose exponents have room.
+// Weights are 2^(c s - M) with an integer M per row, raised (and the row's sums
+// scaled by a power of two, exactly) only where a tile's largest c s exceeds it
+// by more than kSlack: seldom, after the first tile.  Up to 2^kSlack, weights
+// lose nothing: the sums are float32 and the weights bfloat16, whose exponents
+// have room (for values up to 2^119).  The weights are rounded to bfloat16, as
+// the matrix cores take them: 2^-9 of each weight, where their sum keeps float32.
+// (attend.hip, where it costs nothing, adds the remainders.)
+//
+// What bounds it: the matrix cores, busy half of the cycles at the 1.85 GHz that
+// the chip's power leaves them.  Four prompts of 4096 tokens, 32 heads over 8
+// of 128: 548 to 570 us (965 to 1003 TFLOP/s of what is seen; 16384 tokens 1130;
+// the large product of linear.hip 1320 to 1350).  An eighth of it is the copies
+// (the same without them: 486 us), a tenth the weights; LDS has no conflicts.
+// Tried and left: two tiles of 32 rows a wave, which halve the reads of LDS, at
+// one wave a SIMD (heads of 64, where they fit the registers, 868 us against
+// 673); 8 waves sharing a stage (the same for prompts, chunks 156 against 123);
+// the sum of a pair of weights as a dot product, which goes the matrix cores'
+// way (2% slower); more or fewer reads in flight (the same).
 #include <type_traits>
 
 #include <hip/hip_runtime.h>

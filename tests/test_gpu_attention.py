@@ -169,6 +169,55 @@ def test_one_sequence_much_longer_than_the_others():
     check(b := Batch([1, 300], [20000, 300], seed=9, page=64, dim=128, heads=8), run(b))
 
 
+@pytest.mark.parametrize("bad", [None, math.nan])
+def test_units_of_more_than_64_tiles(bad):
+    """Chunks whose workgroups look their pages up more than once: more work
+    than the launch cuts (unless for a value that sends them again)."""
+    b = Batch([40, 17, 33, 64], [18000, 17999, 9000, 90], heads=64, kv_heads=64, dim=16, page=48, seed=20)
+    clean = run(b)
+    check(b, clean)
+    if bad is not None:
+        at = b.kv[0] - 3                         # seen by the last three tokens alone
+        b.v[int(b.pages[0, at // b.page]), :, at % b.page, 7] = bad
+        o = run(b)
+        keep = torch.ones(b.tokens, dtype=torch.bool, device="cuda")
+        keep[37:40] = False
+        assert torch.equal(o[keep], clean[keep])
+        assert o[37:40].view(3, 64, 16)[..., 7].isnan().all()
+
+
+@pytest.mark.parametrize("dim", [24, 128, 200])
+@pytest.mark.parametrize("seqs", [11, 16])
+def test_many_float32_chunks(dim, seqs):
+    """Batches that fill the chip with tiles of 32 and 64 rows."""
+    check(b := Batch([70] * seqs, [70 + 13 * s for s in range(seqs)], heads=8, kv_heads=8, dim=dim,
+                     dtype="f32", seed=dim), run(b))
+
+
+@pytest.mark.parametrize("new", [[3, 1], [120, 2]])
+def test_padded_queries(new):
+    """Rows past the plan's tokens: not read, and zeros in a new output."""
+    b = Batch(new, [200, 50], seed=21)
+    q = torch.full((b.tokens + 6, b.q.shape[1]), math.nan, dtype=torch.bfloat16, device="cuda")
+    q[:b.tokens] = b.q
+    o = hab.paged_attention(plan_of(b).upload(), q, b.k, b.v, b.pages)
+    check(b, o[:b.tokens])
+    assert (o[b.tokens:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_query_that_is_not_finite(dtype):
+    for new, kv in (([4], [40]), ([200], [300])):
+        b = Batch(new, kv, dtype=dtype, seed=22)
+        clean = run(b)
+        b.q[1, 70], b.q[2, 3] = math.nan, math.inf
+        o = run(b).view(b.tokens, b.heads, b.dim)
+        assert o[1, 1].isnan().all() and not torch.isfinite(o[2, 0]).any()
+        keep = torch.ones(b.tokens, b.heads, dtype=torch.bool, device="cuda")
+        keep[1, 1] = keep[2, 0] = False
+        assert torch.equal(o[keep], clean.view(o.shape)[keep])
+
+
 def test_deterministic():
     b = Batch([1, 200, 1], [5000, 700, 90], seed=10)
     a = run(b)
