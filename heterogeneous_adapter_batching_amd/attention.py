@@ -15,7 +15,7 @@ except ImportError:                    # batches can be planned without it
 
 from ._lib import (ROTARY_LAYOUTS, ROTARY_SCALINGS, AttnDesc, KvCache, RotaryDesc, check, load)
 from .api import _DTYPES, _i32, _torch_dtype
-from .layer import _code, _enqueue, _matrix, _new
+from .layer import _code, _enqueue, _new, _Tensor
 
 _i32p = ctypes.POINTER(ctypes.c_int32)
 
@@ -49,6 +49,7 @@ class AttentionPlan:
         self.ws = None
         self.heads, self.kv_heads, self.head_dim, self.page_size = heads, kv_heads, head_dim, page_size
         self.page_shape = (kv_heads, page_size, head_dim)
+        self.q_width, self.k_width = heads * head_dim, kv_heads * head_dim
         if torch:
             self.dtype = _torch_dtype(dtype)
         self.desc = AttnDesc(_DTYPES[dtype], _i32(heads, "heads"), _i32(kv_heads, "kv_heads"),
@@ -129,7 +130,18 @@ def rotary_frequencies(rotary_dim, *, base=10000.0, scaling="none", factor=1.0, 
     return torch.from_numpy(f).to(device) if device is not None else torch.from_numpy(f)
 
 
-def _plan_device(plan, t):
+# A layer makes these calls with tensors of a dozen properties each, so the
+# properties are asked for once, in the cheapest form, and what is wrong is told
+# apart only when something is.
+def _refuse(t, name, plan, device):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != plan.dtype:
+        raise TypeError(f"{name} must be {plan.dtype}, got {t.dtype}")
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _device(plan, t):
     """The device of a call: the plan's (one that was not uploaded is refused
     by the library)."""
     if plan.ws is not None:
@@ -139,14 +151,10 @@ def _plan_device(plan, t):
     return t.device
 
 
-def _heads(t, name, plan, heads, device):
+def _heads(t, name, plan, width, device):
     """A matrix of the plan's tokens (and rows past them): pointer, stride."""
-    if t.__class__ is not torch.Tensor and not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device != device or t.dtype != plan.dtype:
-        _matrix(t, name, None, plan.dtype, device)
-        raise TypeError(f"{name} must be a CUDA tensor")
-    width = heads * plan.head_dim
+    if not isinstance(t, _Tensor) or t.get_device() != device.index or t.dtype != plan.dtype:
+        _refuse(t, name, plan, device)
     shape = t.shape
     if len(shape) != 2 or shape[1] != width or shape[0] < plan.num_tokens:
         raise ValueError(f"{name} must be [{plan.num_tokens} or more][{width}], got {list(shape)}")
@@ -158,12 +166,8 @@ def _heads(t, name, plan, heads, device):
 
 def _pages_of(t, name, plan, device):
     """A cache's shape and its page, head and token strides."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dtype != plan.dtype:
-        raise TypeError(f"{name} must be {plan.dtype}, got {t.dtype}")
+    if not isinstance(t, _Tensor) or t.get_device() != device.index or t.dtype != plan.dtype:
+        _refuse(t, name, plan, device)
     shape = t.shape
     if shape[1:] != plan.page_shape:
         raise ValueError(f"{name} must be [pages]{list(plan.page_shape)}, got {list(shape)}")
@@ -171,45 +175,48 @@ def _pages_of(t, name, plan, device):
     if one != 1:
         raise ValueError(f"{name}: a token's elements must be contiguous")
     # (a dimension of one has any stride)
-    return shape[0], 0 if shape[0] == 1 else page, 0 if shape[1] == 1 else head, tok
+    return shape[0], 0 if shape[0] == 1 else page, 0 if plan.kv_heads == 1 else head, tok
 
 
 # (one descriptor per distinct set of values, as the library only reads them)
 @functools.lru_cache(maxsize=1024)
-def _kv_desc(k, v, num_pages, *strides):
-    return ctypes.byref(KvCache(k, v, *strides, _i32(num_pages, "pages")))
+def _kv_desc(k, v, k_pages, v_pages):
+    if k_pages[0] != v_pages[0]:
+        raise ValueError("k_cache and v_cache must have the same pages")
+    return ctypes.byref(KvCache(k, v, *k_pages[1:], *v_pages[1:], _i32(k_pages[0], "pages")))
 
 
 def _cache(plan, k_cache, v_cache, pages, device):
     """The library's arguments of a cache and its page table."""
-    n, *ks = _pages_of(k_cache, "k_cache", plan, device)
-    nv, *vs = _pages_of(v_cache, "v_cache", plan, device)
-    if n != nv:
-        raise ValueError("k_cache and v_cache must have the same pages")
-    if not isinstance(pages, torch.Tensor) or pages.dtype != torch.int32:
+    desc = _kv_desc(k_cache.data_ptr() if isinstance(k_cache, _Tensor) else 0,
+                    v_cache.data_ptr() if isinstance(v_cache, _Tensor) else 0,
+                    _pages_of(k_cache, "k_cache", plan, device),
+                    _pages_of(v_cache, "v_cache", plan, device))
+    if not isinstance(pages, _Tensor) or pages.dtype != torch.int32:
         raise TypeError("pages must be an int32 CUDA tensor")
-    if pages.device != device:
+    if pages.get_device() != device.index:
         raise ValueError(f"pages is on {pages.device}, not on {device}")
     shape = pages.shape
     if len(shape) != 2 or shape[0] < plan.num_seqs:
         raise ValueError(f"pages must be [{plan.num_seqs} or more][pages of a sequence], got "
                          f"{list(shape)}")
+    rows, count = shape
     ld, step = pages.stride()
-    if step != 1 and shape[1] > 1:
+    if step != 1 and count > 1:
         raise ValueError("pages must have contiguous rows")
-    return (_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), n, *ks, *vs), pages.data_ptr(),
-            ld if shape[0] > 1 else shape[1], _i32(shape[1], "pages of a sequence"))
+    return desc, pages.data_ptr(), (ld if rows > 1 else count), _i32(count, "pages of a sequence")
 
 
 def _vector(t, name, dtype, least, device):
-    """A contiguous vector's pointer."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    """A contiguous vector's pointer and length."""
+    if not isinstance(t, _Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dim() != 1 or t.shape[0] < least or not t.is_contiguous():
+    shape = t.shape
+    if len(shape) != 1 or shape[0] < least or (shape[0] > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {least} or more")
-    return t.data_ptr()
+    return t.data_ptr(), shape[0]
 
 
 def _padded(q, plan, device, stream):
@@ -236,12 +243,12 @@ def paged_attention(plan, q, k_cache, v_cache, pages, *, scale=None, o=None, str
     head_dim^-0.5.  What a token does not see does not reach it, also where it
     is infinite or NaN; a page outside the cache counts as absent.  Calls that
     share a plan's workspace must not overlap.  Inference only.  Returns o."""
-    device = _plan_device(plan, q)
-    qp, ldq = _heads(q, "q", plan, plan.heads, device)
+    device = _device(plan, q)
+    qp, ldq = _heads(q, "q", plan, plan.q_width, device)
     scale = plan.head_dim ** -0.5 if scale is None else float(scale)
     if o is None:
         o = _padded(q, plan, device, stream)
-    op, ldo = _heads(o, "o", plan, plan.heads, device)
+    op, ldo = _heads(o, "o", plan, plan.q_width, device)
     _enqueue(plan.lib.paged_attention,
              (plan.handle, qp, ldq, *_cache(plan, k_cache, v_cache, pages, device), scale, op, ldo),
              device, stream)
@@ -266,29 +273,29 @@ def rotary_append(plan, q, k, v, k_cache, v_cache, pages, freqs, *, layout="half
     paged_attention."""
     if q is None and k is None:
         raise ValueError("neither q nor k")
-    device = _plan_device(plan, k if q is None else q)
+    device = _device(plan, k if q is None else q)
     qp = ldq = op = ldo = kp = ldk = vp = ldv = pp = fp = n = 0
     if q is not None:
-        qp, ldq = _heads(q, "q", plan, plan.heads, device)
+        qp, ldq = _heads(q, "q", plan, plan.q_width, device)
         if q_out is None:
             q_out = _padded(q, plan, device, stream)
-        op, ldo = _heads(q_out, "q_out", plan, plan.heads, device)
+        op, ldo = _heads(q_out, "q_out", plan, plan.q_width, device)
     elif q_out is not None:
         raise ValueError("q_out without q")
     absent = (k is None) + (v is None) + (k_cache is None) + (v_cache is None) + (pages is None)
     if absent == 0:
-        kp, ldk = _heads(k, "k", plan, plan.kv_heads, device)
-        vp, ldv = _heads(v, "v", plan, plan.kv_heads, device)
+        kp, ldk = _heads(k, "k", plan, plan.k_width, device)
+        vp, ldv = _heads(v, "v", plan, plan.k_width, device)
         cache = _cache(plan, k_cache, v_cache, pages, device)
     elif absent == 5:
         cache = (None, 0, 0, 0)
     else:
         raise ValueError("k, v, k_cache, v_cache and pages are given together or not at all")
     if positions is not None:
-        pp = _vector(positions, "positions", torch.int32, plan.num_tokens, device)
+        pp, _ = _vector(positions, "positions", torch.int32, plan.num_tokens, device)
     if freqs is not None:
-        fp, n = _vector(freqs, "freqs", torch.float64, 1, device), freqs.shape[0]
-    desc = _rotary_desc(2 * n, layout, ctypes.c_float(magnitude).value)
+        fp, n = _vector(freqs, "freqs", torch.float64, 1, device)
+    desc = _rotary_desc(2 * n, layout, float(magnitude))
     _enqueue(plan.lib.rotary_append,
              (plan.handle, desc, qp, ldq, op, ldo, kp, ldk, vp, ldv, *cache, pp, fp), device, stream)
     return q_out

@@ -39,11 +39,11 @@ constexpr int32_t kMostTokens = 1 << 23, kMostKeys = 1 << 30;
 // of 19 to 7824 keys 144, 137, 141, 140, 141).
 constexpr int kRowsUnits = 1024, kRowsKeys = 256;
 constexpr int kPromptUnits = 512, kPromptKeys = 512;
-constexpr int kCus = 256;
+constexpr int kCus = 256, kShortKeys = 1024;
 
 // One kernel's share of a plan: its tiles of rows, and their keys in parts.
 struct Side {
-    int32_t tile_rows = 0;                 // 0: no sequence is on this side
+    int32_t tile_rows = 0, waves = 4;      // rows of a tile; waves of a workgroup (few rows)
     int64_t tiles = 0;                     // tiles of rows, over all key heads
     std::vector<AttnUnit> units;
     std::vector<AttnJoin> joins;
@@ -256,7 +256,20 @@ void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, i
         return n * p->d.kv_heads;
     };
     while (p->rows.tile_rows > 16 && tiles(p->rows.tile_rows) < kCus) p->rows.tile_rows /= 2;
-    cut(*p, &p->rows, false, kRowsUnits, kRowsKeys);
+    // A few tiles over short contexts: 8 waves a workgroup and all of a tile's
+    // keys, without a launch to join parts.
+    int64_t longest = p->d.max_kv;
+    if (!longest)
+        each_seq(*p, false, [&](int32_t s, int32_t, int64_t rows) {
+            int32_t lo, hi;
+            tile_keys(*p, s, 0, rows, &lo, &hi);
+            longest = std::max<int64_t>(longest, hi - lo);
+        });
+    p->rows.waves = p->rows.tile_rows == 16 && lora::attn_dim(p->d.head_dim) <= 128 &&
+                            tiles(16) <= kCus && longest <= kShortKeys
+                        ? lora::kManyWaves
+                        : 4;
+    cut(*p, &p->rows, false, kRowsUnits, p->rows.waves == 4 ? kRowsKeys : kShortKeys);
     p->prompt = Side{};
     p->prompt.tile_rows = lora::kPromptRows;
     cut(*p, &p->prompt, true, kPromptUnits, kPromptKeys);
@@ -555,7 +568,7 @@ lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
         if (prompt) a.scale2 = std::max(std::fabs(a.scale2), 1e-30f);
         if (e == hipSuccess)
             e = prompt ? lora::launch_attn_prompt(a, s)
-                       : lora::launch_attn_rows(p->d.dtype, side->tile_rows, a, s);
+                       : lora::launch_attn_rows(p->d.dtype, side->tile_rows, side->waves, a, s);
         if (e == hipSuccess) e = lora::launch_attn_join(p->d.dtype, side->tile_rows, a, s);
     }
     if (e != hipSuccess)

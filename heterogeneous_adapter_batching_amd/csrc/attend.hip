@@ -27,13 +27,12 @@
 namespace lora {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * kWaveSize;
-
 template <typename T> constexpr int dtype_of = sizeof(T) == 2 ? LORA_BF16 : LORA_F32;
 
-template <typename T, int DP, int NQ>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void k_attend_rows(const AttnArgs a) {
+// NQ tiles of 16 rows, NW waves that take the unit's keys in turn.
+template <typename T, int DP, int NQ, int NW>
+__global__ __launch_bounds__(NW * kWaveSize, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void k_attend_rows(const AttnArgs a) {
+    static_assert(NW == 4 || NQ == 1, "the join of 16 rows takes 256 threads");
     constexpr int E = Elem<T>::E;                     // elements of 16 bytes
     constexpr int KS = DP / (4 * E);                  // matrix steps of a score
     constexpr int KT = E / 4;                         // 16-key tiles of a matrix step over keys
@@ -46,8 +45,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void
     // (128 sequences of 19 to 7824 keys, 730 MB: 123 us against 139; four of
     // 68157 to 127138, 1.7 GB: 260 against 298, 6.6 TB/s.)
     constexpr int POLICY = NQ * 16 < attn_rows_most(dtype_of<T>, DP) || NQ == 1 ? kNT : 0;
-    __shared__ float so[kWaves][16][LD];
-    __shared__ float sm[kWaves][16], sl[kWaves][16];
+    __shared__ float so[NW][16][LD];
+    __shared__ float sm[NW][16], sl[NW][16];
 
     const AttnUnit u = load_invariant(a.units + blockIdx.x);
     if (u.seq < 0) return;
@@ -92,7 +91,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void
             for (int j = 0; j < VW; ++j) o[t][c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // A wave takes every kWaves-th run of BK keys.
+    // A wave takes every NW-th run of BK keys.
     struct Keys {
         u32x4 k[KT][KS];
         uint32_t v[4 * KT][VC][VD];
@@ -146,7 +145,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void
                 }
             walk.skip(16);
         }
-        walk.skip((kWaves - 1) * BK);
+        walk.skip((NW - 1) * BK);
     };
     auto attend = [&](int b, const Keys &x) {
         const auto &k = x.k;
@@ -260,7 +259,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void
             }
         }
     };
-    for (int b = u.key0 + w * BK; b < u.key1; b += kWaves * BK) {
+    for (int b = u.key0 + w * BK; b < u.key1; b += NW * BK) {
         Keys x;
         load(b, x);
         attend(b, x);
@@ -286,12 +285,13 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void
             sl[w][n] = sum;
         }
         __syncthreads();
+        if (NW > 4 && tid >= 256) return;
         float top = sm[0][row];
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) top = fmaxf(top, sm[i][row]);
+        for (int i = 1; i < NW; ++i) top = fmaxf(top, sm[i][row]);
         float total = 0.f, r[OW] = {};
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
+        for (int i = 0; i < NW; ++i) {
             const float f = exp2_of(sm[i][row] - finite_max(top));
             total += f * sl[i][row];
 #pragma unroll
@@ -398,11 +398,15 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a, int tile_
     }
 }
 
-template <typename T, int DP, int NQ> hipError_t rows_launch(const AttnArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((k_attend_rows<T, DP, NQ>), dim3(a.num_units), dim3(kThreads), 0, s, a);
+template <typename T, int DP, int NQ, int NW = 4>
+hipError_t rows_launch(const AttnArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((k_attend_rows<T, DP, NQ, NW>), dim3(a.num_units), dim3(NW * kWaveSize), 0, s, a);
     return hipGetLastError();
 }
-template <typename T, int DP> hipError_t rows_dim(int tile_rows, const AttnArgs &a, hipStream_t s) {
+template <typename T, int DP> hipError_t rows_dim(int tile_rows, int waves, const AttnArgs &a, hipStream_t s) {
+    if constexpr (DP <= 128) {
+        if (tile_rows == 16 && waves == kManyWaves) return rows_launch<T, DP, 1, kManyWaves>(a, s);
+    }
     if (tile_rows == 16) return rows_launch<T, DP, 1>(a, s);
     if constexpr (sizeof(T) == 4) {
         if (tile_rows == 32) return rows_launch<T, DP, 2>(a, s);
@@ -412,11 +416,11 @@ template <typename T, int DP> hipError_t rows_dim(int tile_rows, const AttnArgs 
     }
     return hipErrorInvalidValue;
 }
-template <typename T> hipError_t rows_types(int tile_rows, const AttnArgs &a, hipStream_t s) {
+template <typename T> hipError_t rows_types(int tile_rows, int waves, const AttnArgs &a, hipStream_t s) {
     switch (attn_dim(a.head_dim)) {
-        case 64: return rows_dim<T, 64>(tile_rows, a, s);
-        case 128: return rows_dim<T, 128>(tile_rows, a, s);
-        default: return rows_dim<T, 256>(tile_rows, a, s);
+        case 64: return rows_dim<T, 64>(tile_rows, waves, a, s);
+        case 128: return rows_dim<T, 128>(tile_rows, waves, a, s);
+        default: return rows_dim<T, 256>(tile_rows, waves, a, s);
     }
 }
 template <typename T, int DP> hipError_t join_launch(int tile_rows, const AttnArgs &a, hipStream_t s) {
@@ -439,9 +443,10 @@ template <typename T> hipError_t join_types(int tile_rows, const AttnArgs &a, hi
 
 }  // namespace
 
-hipError_t launch_attn_rows(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s) {
+hipError_t launch_attn_rows(int dtype, int tile_rows, int waves, const AttnArgs &a, hipStream_t s) {
     if (a.num_units <= 0) return hipSuccess;
-    return dtype == LORA_F32 ? rows_types<float>(tile_rows, a, s) : rows_types<uint16_t>(tile_rows, a, s);
+    return dtype == LORA_F32 ? rows_types<float>(tile_rows, waves, a, s)
+                             : rows_types<uint16_t>(tile_rows, waves, a, s);
 }
 
 hipError_t launch_attn_join(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s) {

@@ -73,7 +73,9 @@ constexpr int attn_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 
 constexpr int attn_rows_most(int dtype, int head_dim) {
     return dtype == LORA_BF16 ? 16 : head_dim <= 128 ? 64 : 32;
 }
-hipError_t launch_attn_rows(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s);
+// Waves of a workgroup of tiles of 16 rows: 4, or (heads of up to 128) 8.
+constexpr int kManyWaves = 8;
+hipError_t launch_attn_rows(int dtype, int tile_rows, int waves, const AttnArgs &a, hipStream_t s);
 constexpr int kPromptRows = 128; // of a tile of prompts
 hipError_t launch_attn_prompt(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_join(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s);
