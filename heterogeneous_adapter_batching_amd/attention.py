@@ -237,7 +237,7 @@ def paged_attention(plan, q, k_cache, v_cache, pages, *, scale=None, o=None, str
     for every query head, over the keys that the plan lets the token see; zeros
     where there are none.  q and o are [tokens][heads * head_dim] (q may be a
     slice of the q/k/v product; rows past the plan's tokens are not looked at
-    and stay as they are), k_cache and v_cache [pages][kv_heads][page_size]
+    and stay as they are, or are zeros in a new o), k_cache and v_cache [pages][kv_heads][page_size]
     [head_dim] with contiguous elements and any strides of multiples of 8,
     pages int32 [sequences][pages of a sequence].  scale defaults to
     head_dim^-0.5.  What a token does not see does not reach it, also where it

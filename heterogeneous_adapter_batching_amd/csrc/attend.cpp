@@ -5,11 +5,11 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <exception>
 #include <initializer_list>
 #include <iterator>
 #include <memory>
 #include <mutex>
-#include <new>
 #include <unordered_map>
 #include <vector>
 
@@ -401,8 +401,8 @@ lora::CacheArgs cache_args(const attn_plan &p, const lora_kv_cache &c) {
 template <typename Fn> lora_status guarded(Fn fn) {
     try {
         return fn();
-    } catch (const std::bad_alloc &) {
-        return set_errorf(LORA_ENOSPC, "out of host memory");
+    } catch (const std::exception &e) {
+        return set_errorf(LORA_ENOSPC, "host memory: %s", e.what());
     }
 }
 

@@ -54,18 +54,18 @@ template <> struct Vec8<float> {
 };
 __device__ __forceinline__ float value(uint16_t v) { return __uint_as_float(uint32_t(v) << 16); }
 __device__ __forceinline__ float value(float v) { return v; }
-__device__ __forceinline__ void put(uint16_t *p, float v) { *p = uint16_t(bf16x2_rne(v, v)); }
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
 
 enum RotaryItems : int {
-    kHalves,     // 8 pairs: two vectors, half the rotated part apart
-    kPairs,      // 4 pairs: one vector
-    kOnes,       // one pair: rotated parts that are not made of whole vectors
+    kHalves,     // pairs half the rotated part apart, whole vectors of each: 8 pairs
+    kPairs,      // neighbours: a vector
+    kOffset,     // halves that are not whole vectors: a vector, its elements'
+                 // partners through LDS
 };
 
-// What one thread does at a time in a head that is rotated: `turned` items of
-// the rotated part, then `plain` of the rest.  The same thread reads and writes
-// all of an item, so that q may be rotated in place.
+// A thread reads and writes all of what it takes at a time, so that q may be
+// rotated in place; kOffset has whole heads in LDS before it writes them.
+// (16384 tokens of 40 heads, 90 elements of 128 rotated, us: halves 83, by 8
+// unaligned pairs a thread 226, by single pairs 182; neighbours 74.)
 template <typename T, int ITEMS>
 __global__ __launch_bounds__(kThreads) void k_rotary(const RotaryArgs a) {
     __shared__ float2 turn[LORA_ATTN_MAX_HEAD_DIM / 2];   // (m cos, m sin) of every pair
@@ -97,64 +97,89 @@ __global__ __launch_bounds__(kThreads) void k_rotary(const RotaryArgs a) {
     const T *v = reinterpret_cast<const T *>(a.v) + int64_t(t) * a.ldv;
     T *qo = reinterpret_cast<T *>(a.q_out) + int64_t(t) * a.ldqo;
 
-    constexpr int PER = ITEMS == kHalves ? 16 : ITEMS == kPairs ? 8 : 2;   // elements of an item
-    constexpr int REST = ITEMS == kOnes ? 1 : 8;
-    const int turned = 2 * pairs / PER, plain = (a.head_dim - 2 * pairs) / REST;
-    const int heads = (a.q ? a.heads : 0) + (kc ? a.kv_heads : 0), first_k = a.q ? a.heads : 0;
+    const int vecs = a.head_dim / 8, first_k = a.q ? a.heads : 0;
+    const int heads = first_k + (kc ? a.kv_heads : 0);
+    const auto source = [&](int h) {
+        return h < first_k ? q + int64_t(h) * a.head_dim : k + int64_t(h - first_k) * a.head_dim;
+    };
+    const auto target = [&](int h) {
+        return h < first_k ? qo + int64_t(h) * a.head_dim
+                           : kc + int64_t(h - first_k) * a.cache.k_head;
+    };
     __syncthreads();
-    for (int i = tid; i < heads * (turned + plain); i += kThreads) {
-        const int h = i / (turned + plain), e = i % (turned + plain);
-        const T *src = h < first_k ? q + int64_t(h) * a.head_dim
-                                   : k + int64_t(h - first_k) * a.head_dim;
-        T *dst = h < first_k ? qo + int64_t(h) * a.head_dim
-                             : kc + int64_t(h - first_k) * a.cache.k_head;
-        if (e >= turned) {
-            const int at = 2 * pairs + (e - turned) * REST;
-            if constexpr (ITEMS == kOnes) {
-                dst[at] = src[at];
-            } else {
-                Vec8<T> x;
-                x.load(src + at);
-                x.store(dst + at);
-            }
-        } else if constexpr (ITEMS == kHalves) {
-            Vec8<T> x, y;
-            x.load(src + e * 8);
-            y.load(src + pairs + e * 8);
-            float f[8], g[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 cs = turn[e * 8 + j];
-                f[j] = x.get(j) * cs.x - y.get(j) * cs.y;
-                g[j] = y.get(j) * cs.x + x.get(j) * cs.y;
-            }
-            x.set(f);
-            y.set(g);
-            x.store(dst + e * 8);
-            y.store(dst + pairs + e * 8);
-        } else if constexpr (ITEMS == kPairs) {
+    if constexpr (ITEMS == kOffset) {
+        __shared__ __align__(16) T staged[kThreads * 8];
+        const int at_once = kThreads / vecs, mine = tid / vecs, e = tid % vecs * 8;
+        for (int h0 = 0; h0 < heads; h0 += at_once) {
+            const int h = h0 + mine;
+            const bool ok = mine < at_once && h < heads;
             Vec8<T> x;
-            x.load(src + e * 8);
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 cs = turn[e * 4 + j];
-                f[2 * j] = x.get(2 * j) * cs.x - x.get(2 * j + 1) * cs.y;
-                f[2 * j + 1] = x.get(2 * j + 1) * cs.x + x.get(2 * j) * cs.y;
+            if (ok) {
+                x.load(source(h) + e);
+                x.store(staged + tid * 8);
             }
-            x.set(f);
-            x.store(dst + e * 8);
-        } else {
-            const int at = a.layout == LORA_ROTARY_HALF ? e : 2 * e;
-            const int to = a.layout == LORA_ROTARY_HALF ? e + pairs : 2 * e + 1;
-            const float x = value(src[at]), y = value(src[to]);
-            const float2 cs = turn[e];
-            put(dst + at, x * cs.x - y * cs.y);
-            put(dst + to, y * cs.x + x * cs.y);
+            __syncthreads();
+            if (ok && e < 2 * pairs) {
+                const T *head = staged + tid * 8 - e;
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = e + j;
+                    f[j] = x.get(j);
+                    if (i >= 2 * pairs) continue;
+                    const bool low = i < pairs;
+                    const float2 cs = turn[low ? i : i - pairs];
+                    const float z = value(head[low ? i + pairs : i - pairs]);
+                    f[j] = low ? f[j] * cs.x - z * cs.y : f[j] * cs.x + z * cs.y;
+                }
+                x.set(f);
+            }
+            if (ok) x.store(target(h) + e);
+            __syncthreads();
+        }
+    } else {
+        const int turned = ITEMS == kHalves ? pairs / 8 : 0, items = vecs - turned;
+        for (int i = tid; i < heads * items; i += kThreads) {
+            const int h = i / items, e = i % items;
+            const T *src = source(h);
+            T *dst = target(h);
+            Vec8<T> x;
+            float f[8];
+            if (ITEMS == kHalves && e < turned) {
+                Vec8<T> y;
+                x.load(src + e * 8);
+                y.load(src + pairs + e * 8);
+                float g[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 cs = turn[e * 8 + j];
+                    f[j] = x.get(j) * cs.x - y.get(j) * cs.y;
+                    g[j] = y.get(j) * cs.x + x.get(j) * cs.y;
+                }
+                x.set(f);
+                y.set(g);
+                x.store(dst + e * 8);
+                y.store(dst + pairs + e * 8);
+                continue;
+            }
+            const int at = (e + turned) * 8;             // (past both halves)
+            x.load(src + at);
+            if (ITEMS == kPairs && at < 2 * pairs) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    f[j] = x.get(j);
+                    f[j + 1] = x.get(j + 1);
+                    if (at + j >= 2 * pairs) continue;
+                    const float2 cs = turn[at / 2 + j / 2];
+                    f[j] = x.get(j) * cs.x - x.get(j + 1) * cs.y;
+                    f[j + 1] = x.get(j + 1) * cs.x + x.get(j) * cs.y;
+                }
+                x.set(f);
+            }
+            x.store(dst + at);
         }
     }
     if (!vc) return;
-    const int vecs = a.head_dim / 8;
     for (int i = tid; i < a.kv_heads * vecs; i += kThreads) {
         const int h = i / vecs, e = i % vecs;
         Vec8<T> x;
@@ -166,12 +191,12 @@ __global__ __launch_bounds__(kThreads) void k_rotary(const RotaryArgs a) {
 template <typename T> hipError_t rotary_types(const RotaryArgs &a, hipStream_t s) {
     const dim3 grid(a.T), block(kThreads);
     const int r = a.freqs ? a.rotary_dim : 0;
-    if (a.layout == LORA_ROTARY_HALF && r % 16 == 0)
-        hipLaunchKernelGGL((k_rotary<T, kHalves>), grid, block, 0, s, a);
-    else if (a.layout == LORA_ROTARY_INTERLEAVED && r % 8 == 0)
+    if (a.layout == LORA_ROTARY_INTERLEAVED)
         hipLaunchKernelGGL((k_rotary<T, kPairs>), grid, block, 0, s, a);
+    else if (r % 16 == 0)
+        hipLaunchKernelGGL((k_rotary<T, kHalves>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((k_rotary<T, kOnes>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_rotary<T, kOffset>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
