@@ -237,12 +237,13 @@ def paged_attention(plan, q, k_cache, v_cache, pages, *, scale=None, o=None, str
     for every query head, over the keys that the plan lets the token see; zeros
     where there are none.  q and o are [tokens][heads * head_dim] (q may be a
     slice of the q/k/v product; rows past the plan's tokens are not looked at
-    and stay as they are, or are zeros in a new o), k_cache and v_cache [pages][kv_heads][page_size]
-    [head_dim] with contiguous elements and any strides of multiples of 8,
-    pages int32 [sequences][pages of a sequence].  scale defaults to
-    head_dim^-0.5.  What a token does not see does not reach it, also where it
-    is infinite or NaN; a page outside the cache counts as absent.  Calls that
-    share a plan's workspace must not overlap.  Inference only.  Returns o."""
+    and stay as they are, or are zeros in a new o), k_cache and v_cache
+    [pages][kv_heads][page_size][head_dim] with contiguous elements and any
+    strides of multiples of 8, pages int32 [sequences][pages of a sequence].
+    scale defaults to head_dim^-0.5.  What a token does not see does not reach
+    it, also where it is infinite or NaN; a page outside the cache counts as
+    absent.  Calls that share a plan's workspace must not overlap.  Inference
+    only.  Returns o."""
     device = _device(plan, q)
     qp, ldq = _heads(q, "q", plan, plan.q_width, device)
     scale = plan.head_dim ** -0.5 if scale is None else float(scale)
