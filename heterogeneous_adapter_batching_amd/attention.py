@@ -40,7 +40,8 @@ class AttentionPlan:
     `window` of them unless that is 0; else all of its sequence's keys (an
     encoder's states; new_lens and kv_lens are then independent).  max_kv: the
     most keys of any later rebuild, so that a captured graph may be replayed
-    after rebuild(the same new_lens, other kv_lens).upload(the same ws)."""
+    after rebuild(the same new_lens, other kv_lens).upload(the same ws); the
+    page table then has room for max_kv keys."""
 
     def __init__(self, heads, kv_heads, head_dim, page_size, new_lens, kv_lens, *, dtype="bf16",
                  causal=True, window=0, max_kv=0):

@@ -368,9 +368,11 @@ lora_status check_cache(const attn_plan &p, const lora_kv_cache *c, const int32_
     if (ld_pages < pages_per_seq || ld_pages > (int64_t(1) << 40))
         return set_errorf(LORA_EINVAL, "ld of the page table (%lld) is less than its %d pages",
                           (long long)ld_pages, pages_per_seq);
-    if (int64_t(pages_per_seq) * p.d.page_size < p.most_kv)
+    // (a captured call may be replayed for up to max_kv)
+    const int32_t keys = std::max(p.most_kv, p.d.max_kv);
+    if (int64_t(pages_per_seq) * p.d.page_size < keys)
         return set_errorf(LORA_EINVAL, "%d pages of %d a sequence do not hold %d keys",
-                          pages_per_seq, p.d.page_size, p.most_kv);
+                          pages_per_seq, p.d.page_size, keys);
     return LORA_OK;
 }
 

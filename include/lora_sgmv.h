@@ -766,8 +766,9 @@ typedef struct {
  * than 0 or num_pages and more counts as absent.  q, o: [T][ldq / ldo], head h
  * at column h * head_dim, 16-byte aligned, leading dimensions multiples of 8;
  * rows from the plan's last token on are not touched.  pages: [S][ld_pages]
- * on the device, pages_per_seq of them for each sequence, enough for its keys.
- * o may not overlap q or the cache.
+ * on the device, pages_per_seq of them for each sequence, enough for its keys
+ * (with max_kv: for max_kv of them, since a graph keeps the table it was
+ * captured with).  o may not overlap q or the cache.
  * Errors: LORA_EINVAL, LORA_ESTATE (the plan), LORA_EHIP. */
 lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
                             const lora_kv_cache *cache, const int32_t *pages, int64_t ld_pages,

@@ -229,3 +229,11 @@ def test_tensors_on_the_host_are_refused():
         hab.paged_attention(plan, q, kc, kc, pages)
     with pytest.raises(TypeError):
         hab.rotary_append(plan, q, q[:, :128], q[:, :128], kc, kc, pages, None)
+
+
+@pytest.mark.parametrize("call", [attend, rotary])
+@pytest.mark.parametrize("most, status", [(0, ESTATE), (48, ESTATE), (49, EINVAL)])
+def test_page_tables_hold_max_kv(call, most, status):
+    """A graph is replayed with the table that it was captured with, for up to
+    max_kv keys."""
+    assert call(max_kv=most) == status
