@@ -31,6 +31,9 @@ bool is_dtype(int32_t d) { return d == LORA_F32 || d == LORA_BF16; }
 uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
 constexpr int32_t kMostTokens = 1 << 23, kMostKeys = 1 << 30;
+// The largest stride, in elements, and the most elements from a cache's first
+// page to its last: what follows from them stays within 64 bits.
+constexpr int64_t kMostStride = int64_t(1) << 36, kMostCache = int64_t(1) << 40;
 
 // Units a launch aims for when it cuts the tiles' keys into parts, and the
 // fewest keys of a part.  The kernel for few rows has two workgroups a CU, the
@@ -309,9 +312,9 @@ struct Rows {
 lora_status check_rows(const Rows &r, int32_t es) {
     if (!r.ptr || !aligned(r.ptr, 16))
         return set_errorf(LORA_EINVAL, "%s must be non-null and 16-byte aligned", r.name);
-    if (r.ld < r.width || r.ld % 8 || r.ld > (int64_t(1) << 40))
-        return set_errorf(LORA_EINVAL, "ld of %s (%lld) is not a multiple of 8 from its width %lld",
-                          r.name, (long long)r.ld, (long long)r.width);
+    if (r.ld < r.width || r.ld % 8 || r.ld > kMostStride)
+        return set_errorf(LORA_EINVAL, "ld of %s (%lld) is not a multiple of 8 from its width %lld "
+                          "to 2^36", r.name, (long long)r.ld, (long long)r.width);
     return LORA_OK;
 }
 // Whether two matrices of T rows reach into each other: column slices of the
@@ -331,9 +334,11 @@ bool overlap(const Rows &a, const Rows &b, int64_t T, int32_t es) {
 }
 
 // The cache and its page table; and whether the tensors beside them (T rows
-// each) lie apart from it.
+// each) lie apart from it.  A cache that is written has a place for each key and
+// each value.
 lora_status check_cache(const attn_plan &p, const lora_kv_cache *c, const int32_t *pages,
-                        int64_t ld_pages, int32_t pages_per_seq, std::initializer_list<Rows> beside) {
+                        int64_t ld_pages, int32_t pages_per_seq, bool written,
+                        std::initializer_list<Rows> beside) {
     if (!c) return set_errorf(LORA_EINVAL, "null cache");
     const int32_t es = esize(p.d.dtype);
     if (c->num_pages < 1) return set_errorf(LORA_EINVAL, "a cache of %d pages", c->num_pages);
@@ -347,9 +352,16 @@ lora_status check_cache(const attn_plan &p, const lora_kv_cache *c, const int32_
         if (!t.ptr || !aligned(t.ptr, 16))
             return set_errorf(LORA_EINVAL, "%s must be non-null and 16-byte aligned", t.name);
         for (int64_t st : {t.page, t.head, t.tok})
-            if (st < 0 || st % 8 || st > (int64_t(1) << 40))
-                return set_errorf(LORA_EINVAL, "a stride of %s (%lld) is no multiple of 8 in 0..2^40",
+            if (st < 0 || st % 8 || st > kMostStride)
+                return set_errorf(LORA_EINVAL, "a stride of %s (%lld) is no multiple of 8 in 0..2^36",
                                   t.name, (long long)st);
+        if (t.page > kMostCache / c->num_pages)
+            return set_errorf(LORA_EINVAL, "%s: %d pages, %lld elements apart", t.name, c->num_pages,
+                              (long long)t.page);
+        if (written && ((c->num_pages > 1 && t.page < p.d.head_dim) ||
+                        (p.d.kv_heads > 1 && t.head < p.d.head_dim)))
+            return set_errorf(LORA_EINVAL, "places of %s coincide: pages %lld and heads %lld elements "
+                              "apart", t.name, (long long)t.page, (long long)t.head);
         if (t.tok < p.d.head_dim || t.tok * es * 16 >= (int64_t(1) << 31))
             return set_errorf(LORA_EINVAL, "%s: tokens %lld elements apart, heads of %d", t.name,
                               (long long)t.tok, p.d.head_dim);
@@ -365,8 +377,9 @@ lora_status check_cache(const attn_plan &p, const lora_kv_cache *c, const int32_
     }
     if (!pages || !aligned(pages, 4))
         return set_errorf(LORA_EINVAL, "the page table must be non-null and 4-byte aligned");
-    if (ld_pages < pages_per_seq || ld_pages > (int64_t(1) << 40))
-        return set_errorf(LORA_EINVAL, "ld of the page table (%lld) is less than its %d pages",
+    if (written && c->k == c->v) return set_errorf(LORA_EINVAL, "k_cache is v_cache");
+    if (ld_pages < pages_per_seq || ld_pages > kMostStride)
+        return set_errorf(LORA_EINVAL, "ld of the page table (%lld) is not from its %d pages to 2^36",
                           (long long)ld_pages, pages_per_seq);
     // (a captured call may be replayed for up to max_kv)
     const int32_t keys = std::max(p.most_kv, p.d.max_kv);
@@ -539,7 +552,7 @@ lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
     for (const Rows *r : {&rq, &ro})
         if ((st = check_rows(*r, es)) != LORA_OK) return st;
     if (overlap(rq, ro, T, es)) return set_errorf(LORA_EINVAL, "o overlaps q");
-    if ((st = check_cache(*p, cache, pages, ld_pages, pages_per_seq, {ro})) != LORA_OK)
+    if ((st = check_cache(*p, cache, pages, ld_pages, pages_per_seq, false, {ro})) != LORA_OK)
         return st;
     if ((st = check_uploaded(p)) != LORA_OK) return st;
 
@@ -649,7 +662,8 @@ lora_status rotary_append(const attn_plan *p, const lora_rotary_desc *r, const v
             if ((st = check_rows(*x, es)) != LORA_OK) return st;
             if (q && overlap(ro, *x, T, es)) return set_errorf(LORA_EINVAL, "q_out overlaps %s", x->name);
         }
-        if ((st = check_cache(*p, cache, pages, ld_pages, pages_per_seq, {ro, rk, rv})) != LORA_OK)
+        if ((st = check_cache(*p, cache, pages, ld_pages, pages_per_seq, true, {rq, ro, rk, rv})) !=
+            LORA_OK)
             return st;
     } else if (k || v) {
         return set_errorf(LORA_EINVAL, "keys or values without a cache");

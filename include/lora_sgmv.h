@@ -747,7 +747,9 @@ lora_status attn_plan_stats(const attn_plan *p, int32_t *num_tokens, int32_t *nu
 
 /* Keys and values of num_pages pages: element e of token t of page p, head h,
  * at k + p k_page_stride + h k_head_stride + t k_token_stride + e.  16-byte
- * aligned; strides are multiples of 8 elements. */
+ * aligned; strides are multiples of 8 elements, at most 2^36, and pages lie
+ * within 2^40.  Pages and heads may coincide (strides of 0) where the cache is
+ * only read. */
 typedef struct {
     void *k, *v;
     int64_t k_page_stride, k_head_stride, k_token_stride;
@@ -807,7 +809,8 @@ typedef struct {
  * (rotary_dim 0).  q and q_out may be NULL (keys and values only: an
  * encoder's states), and so may k, v, cache and pages together (queries only).
  * A token whose page the table gives as less than 0 or num_pages and more is
- * not stored.  Two tokens of one batch must not share a place in the cache.
+ * not stored.  Two tokens of one batch must not share a place in the cache;
+ * one whose heads or pages coincide, or whose k is v, is refused.
  * Rows from the plan's last token on are not touched.  Sequences as the plan
  * says, their last new_lens[s] keys being the new ones (a plan that is not
  * causal too).  Alignment as paged_attention.

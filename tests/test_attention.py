@@ -237,3 +237,28 @@ def test_page_tables_hold_max_kv(call, most, status):
     """A graph is replayed with the table that it was captured with, for up to
     max_kv keys."""
     assert call(max_kv=most) == status
+
+
+@pytest.mark.parametrize("call", [attend, rotary])
+@pytest.mark.parametrize("bad", [
+    dict(ldq=1 << 37), dict(ld_pages=1 << 37), dict(c=cache(page=1 << 36, pages=(1 << 31) - 1)),
+    dict(c=cache(head=1 << 37))])
+def test_extents_stay_within_64_bits(call, bad):
+    assert call(**bad) == EINVAL
+
+
+@pytest.mark.parametrize("places", [dict(page=0), dict(page=56), dict(head=0), dict(head=32),
+                                    dict(v=P + 2 * M)])
+def test_places_that_coincide_are_read_and_not_written(places):
+    assert attend(c=cache(**places)) == ESTATE
+    assert rotary(c=cache(**places)) == EINVAL
+
+
+def test_places_of_one_page_and_one_head():
+    """A dimension of one has any stride."""
+    assert rotary(c=cache(page=0, pages=1)) == ESTATE
+    assert rotary(c=cache(head=0), heads=4, kv_heads=1) == ESTATE
+
+
+def test_queries_in_the_cache():
+    assert rotary(q=P + 2 * M + 64) == EINVAL and rotary(q=P + 3 * M) == EINVAL
