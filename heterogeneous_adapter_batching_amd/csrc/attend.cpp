@@ -299,6 +299,15 @@ void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, i
     p->ws_bytes = at;
 }
 
+void plan_clear(attn_plan *p) {
+    p->new_lens.clear();
+    p->kv_lens.clear();
+    p->tokens.clear();
+    p->most_kv = 0;
+    p->rows = p->prompt = Side{};
+    p->image_bytes = p->ws_bytes = 0;
+}
+
 bool aligned(const void *ptr, int64_t bytes) {
     return reinterpret_cast<uintptr_t>(ptr) % uint64_t(bytes) == 0;
 }
@@ -448,7 +457,12 @@ lora_status attn_plan_rebuild(attn_plan *p, const int32_t *new_lens, const int32
     if (st != LORA_OK) return st;
     p->ws = nullptr;                       // its tables are the last batch's
     return guarded([&] {
-        plan_build(p, new_lens, kv_lens, num_seqs);
+        try {
+            plan_build(p, new_lens, kv_lens, num_seqs);
+        } catch (...) {
+            plan_clear(p);                 // of no tokens, rather than of half a batch
+            throw;
+        }
         return LORA_OK;
     });
 }
