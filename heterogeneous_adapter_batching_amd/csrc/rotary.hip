@@ -80,9 +80,10 @@ __global__ __launch_bounds__(kThreads) void k_rotary(const RotaryArgs a) {
         turn[tid] = float2{a.magnitude * c, a.magnitude * s};
     }
 
-    // the place of the token's key and value; none in a page that is none
+    // the place of the token's key and value; none in a page that is none, or
+    // where a replayed graph's sequence has fewer keys than new tokens now
     T *kc = nullptr, *vc = nullptr;
-    if (a.cache.k) {
+    if (a.cache.k && tok.pos >= 0) {
         const int p = tok.pos / a.cache.page_size, slot = tok.pos % a.cache.page_size;
         const int page = load_invariant(a.pages + int64_t(tok.seq) * a.ld_pages + p);
         if (page >= 0 && page < a.cache.num_pages) {

@@ -809,8 +809,10 @@ typedef struct {
  * (rotary_dim 0).  q and q_out may be NULL (keys and values only: an
  * encoder's states), and so may k, v, cache and pages together (queries only).
  * A token whose page the table gives as less than 0 or num_pages and more is
- * not stored.  Two tokens of one batch must not share a place in the cache;
- * one whose heads or pages coincide, or whose k is v, is refused.
+ * not stored, nor one in front of its sequence's first key (a graph replayed
+ * after a plan that is not causal was rebuilt for fewer keys than new tokens).
+ * Two tokens of one batch must not share a place in the cache; a cache whose
+ * heads or pages coincide, or whose k is v, is refused.
  * Rows from the plan's last token on are not touched.  Sequences as the plan
  * says, their last new_lens[s] keys being the new ones (a plan that is not
  * causal too).  Alignment as paged_attention.

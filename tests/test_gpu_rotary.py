@@ -175,3 +175,33 @@ def test_captured_and_replayed():
         check(b, q, b.heads, out, pos, f, "half", 1.0)
         check(b, k, b.kv_heads, kc[page, :, slot], pos, f, "half", 1.0)
         assert torch.equal(vc[page, :, slot].flatten(1), v)
+
+
+def test_replayed_with_fewer_keys_than_new_tokens():
+    """A plan that is not causal may be rebuilt so, and a captured append
+    replayed: tokens in front of the first key are not stored."""
+    b, q, k, v = case([2, 3], [9, 30], seed=7, causal=False)
+    plan = hab.AttentionPlan(b.heads, b.kv_heads, b.dim, b.page, b.new, b.kv, dtype=b.dtype,
+                             causal=False, max_kv=30).upload()
+    k, v = k.clone(), v.clone()
+    page = b.page
+    kc = torch.zeros(8, b.kv_heads, page, b.dim, dtype=k.dtype, device="cuda")
+    vc = torch.zeros_like(kc)
+    pages = torch.tensor([[3, 5], [6, 2]], dtype=torch.int32, device="cuda")[:, :max(1, -(-30 // page))]
+    hab.rotary_append(plan, None, k, v, kc, vc, pages, None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hab.rotary_append(plan, None, k, v, kc, vc, pages, None)
+    plan.rebuild([2, 3], [1, 30]).upload(ws=plan.ws)
+    for _ in range(3):
+        kc.zero_()
+        vc.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for c, rows in ((kc, k), (vc, v)):
+            want = torch.zeros_like(c)
+            want[3, :, 0] = rows[1].view(b.kv_heads, b.dim)
+            for i, pos in enumerate((27, 28, 29)):
+                want[int(pages[1, pos // page]), :, pos % page] = rows[2 + i].view(b.kv_heads, b.dim)
+            assert torch.equal(c, want)
