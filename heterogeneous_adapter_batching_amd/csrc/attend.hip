@@ -297,15 +297,16 @@ __global__ __launch_bounds__(NW * kWaveSize, sizeof(T) == 2 && DP <= 128 ? 2 : 1
 #pragma unroll
             for (int e = 0; e < OW; ++e) r[e] += f * so[i][row][col + e];
         }
-        const float inv = total == 0.f ? 0.f : 1.0f / total;
-#pragma unroll
-        for (int e = 0; e < OW; ++e) r[e] *= inv;
         const int rr = u.row0 + t * 16 + row;
         if (rr >= u.rows) continue;
+        const bool lost = total == 0.f && sees_a_key(a, u, rr);
+        const float inv = inverse_of(total, lost, u.slot >= 0);
+#pragma unroll
+        for (int e = 0; e < OW; ++e) r[e] *= inv;
         if (u.slot >= 0) {
             const int64_t at = int64_t(u.slot) * (NQ * 16) + t * 16 + row;
             store_row<OW>(a.partial + at * DP + col, r);
-            if ((tid & 15) == 0) a.lse[at] = total == 0.f ? kNone : top + log2f(total);
+            if ((tid & 15) == 0) a.lse[at] = log_weight(top, total, lost);
         } else {
             T *out = reinterpret_cast<T *>(a.o) + int64_t(u.tok0 + rr / a.group) * a.ldo +
                      int64_t(u.kv_head * a.group + rr % a.group) * D;
@@ -348,6 +349,7 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a, int tile_
 #pragma unroll
         for (int i = 0; i < WAYS; ++i) top = fmaxf(top, tops[group / WAYS * WAYS + i]);
     }
+    const bool lost = top == kLost;      // no part has a score above -inf
     top = finite_max(top);
     float total = 0.f, r[OW] = {};
     if (ok && col < a.head_dim) {
@@ -381,7 +383,7 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a, int tile_
         }
     }
     if (!ok || col >= a.head_dim) return;
-    const float inv = total == 0.f ? 0.f : 1.0f / total;
+    const float inv = inverse_of(lost ? 0.f : total, lost, false);
 #pragma unroll
     for (int e = 0; e < OW; ++e) r[e] *= inv;
     T *out = reinterpret_cast<T *>(a.o) + int64_t(j.tok0 + rr / a.group) * a.ldo +

@@ -28,6 +28,34 @@ __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2
 // its scores, which are -inf.
 __device__ __forceinline__ float finite_max(float m) { return m == kNone ? 0.f : m; }
 
+// Whether row r of a unit sees a key at all.  Weights that sum to zero are those
+// of a row that sees none, whose result is zeros, or of one whose scores are all
+// -inf, whose weights exp(-inf + inf) are no numbers: this is asked of them alone.
+__device__ __forceinline__ bool sees_a_key(const AttnArgs &a, const AttnUnit &u, int r) {
+    const int pos = u.pos0 + r / a.group;
+    const int first = a.window ? max(u.key0, pos - a.window + 1) : u.key0;
+    const int last = a.causal ? min(pos, u.key1 - 1) : u.key1 - 1;
+    const int32_t *table = a.pages + int64_t(u.seq) * a.ld_pages;
+    if (first <= last)
+        for (int p = first / a.cache.page_size; p <= last / a.cache.page_size; ++p)
+            if (table[p] >= 0 && table[p] < a.cache.num_pages) return true;
+    return false;
+}
+
+// The logarithm of what a part of a row's keys weighs, by which parts are
+// joined: kNone for a part without keys, kLost for one whose scores are all
+// -inf, which any other key's exceeds.
+constexpr float kLost = -0x1.fffffep127f, kLeast = -0x1.fffffcp127f;
+__device__ __forceinline__ float log_weight(float top, float total, bool lost) {
+    if (total == 0.f) return lost ? kLost : kNone;
+    const float w = top + log2f(total);
+    return w == kLost ? kLeast : w;
+}
+// What a row's sums are multiplied by; split: the row has other parts.
+__device__ __forceinline__ float inverse_of(float total, bool lost, bool split) {
+    return total != 0.f ? 1.0f / total : lost && !split ? __builtin_nanf("") : 0.f;
+}
+
 // The parts of a word, two bf16 or a float32, that are not finite.
 template <typename T> __device__ __forceinline__ uint32_t odd_mask(uint32_t w);
 template <> __device__ __forceinline__ uint32_t odd_mask<uint16_t>(uint32_t w) {

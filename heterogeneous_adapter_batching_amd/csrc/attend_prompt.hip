@@ -452,8 +452,9 @@ k_attend_prompt(const AttnArgs a) {
 
     // outputs: a lane has 4 consecutive elements, 8 apart, of its row
     const float total = over_halves(l, sum_of);
-    const float inv = total == 0.f ? 0.f : 1.0f / total;
     if (!row) return;
+    const bool lost = total == 0.f && sees_a_key(a, u, r);
+    const float inv = inverse_of(total, lost, u.slot >= 0);
     if (u.slot >= 0) {
         const int64_t at = int64_t(u.slot) * kPromptRows + (r - u.row0);
 #pragma unroll
@@ -462,7 +463,7 @@ k_attend_prompt(const AttnArgs a) {
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<f32x4 *>(a.partial + at * DP + dt * 32 + 2 * i + 4 * h) =
                     f32x4{o[dt][i] * inv, o[dt][i + 1] * inv, o[dt][i + 2] * inv, o[dt][i + 3] * inv};
-        if (h == 0) a.lse[at] = total == 0.f ? kNone : m + log2f(total);
+        if (h == 0) a.lse[at] = log_weight(m, total, lost);
     } else {
         uint16_t *out = reinterpret_cast<uint16_t *>(a.o) + int64_t(u.tok0 + tok) * a.ldo +
                         int64_t(head) * D;

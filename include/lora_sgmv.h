@@ -763,9 +763,10 @@ typedef struct {
  * says the token sees.  Sums, maxima and (float32) products are float32;
  * bfloat16 weights enter the second product as bfloat16, for tiles of few rows
  * with the rounding's remainder in a second one; o is rounded once.  A token
- * without a key gets zeros.  Keys and values that a token does not see do not
- * reach it, whatever they hold; a key in a page that the table gives as less
- * than 0 or num_pages and more counts as absent.  q, o: [T][ldq / ldo], head h
+ * without a key gets zeros; one whose scores are all -inf, as the formula has
+ * it, NaN.  Keys and values that a token does not see do not reach it, whatever
+ * they hold; a key in a page that the table gives as less than 0 or num_pages
+ * and more counts as absent.  q, o: [T][ldq / ldo], head h
  * at column h * head_dim, 16-byte aligned, leading dimensions multiples of 8;
  * rows from the plan's last token on are not touched.  pages: [S][ld_pages]
  * on the device, pages_per_seq of them for each sequence, enough for its keys
