@@ -272,9 +272,11 @@ k_attend_prompt(const AttnArgs a) {
         v = largest(v, largest(x[j + 3], x[j + 4]));
         return largest(largest(v, x[j + 5]), largest(x[j + 6], x[j + 7]));
     };
-    // M raised to a tile's maximum, the sums brought to it
+    // M raised to a tile's maximum, the sums brought to it: the rows that exceed
+    // it by the slack alone, so that a row's bits do not follow keys that only
+    // other rows of the wave see
     auto raise = [&](float top) {
-        const float now = fmaxf(m, ceilf(top));
+        const float now = top > m + kSlack ? ceilf(top) : m;
         const float f = exp2_of(m - finite_max(now));
         m = now;
         l *= f;
