@@ -15,8 +15,9 @@
 // scaled by a power of two, exactly) only where a tile's largest c s exceeds it
 // by more than kSlack: seldom, after the first tile.  Up to 2^kSlack, weights
 // lose nothing: the sums are float32 and the weights bfloat16, whose exponents
-// have room (for values up to 2^119).  The weights are rounded to bfloat16, as
-// the matrix cores take them: 2^-9 of each weight, where their sum keeps float32.
+// have room.  (Values past 2^119 can bring a sum to infinity so; then the rows go
+// again, with weights of at most 1.)  The weights are rounded to bfloat16, as
+// the matrix cores take them: 2^-8 of each weight, where their sum keeps float32.
 // (attend.hip, where it costs nothing, adds the remainders.)
 //
 // What bounds it: the matrix cores, busy half of the cycles at the 1.85 GHz that
@@ -258,9 +259,9 @@ k_attend_prompt(const AttnArgs a) {
     // weights 2 i, 2 i + 1 of the lane's 32, bf16 in the order of the second
     // product's right operand (the dot product that would sum the pair shares
     // the matrix cores' way: two additions cost less beside them)
-    auto weigh = [&](const f32x16 (&s)[2], int i, float low) {
-        const float x = exp2_of(fmaf(s[i / 8][i % 8 * 2], c2, -low));
-        const float y = exp2_of(fmaf(s[i / 8][i % 8 * 2 + 1], c2, -low));
+    auto weigh = [&](const f32x16 (&s)[2], int i, float low, float times = 1.f) {
+        const float x = exp2_of(fmaf(s[i / 8][i % 8 * 2], c2, -low)) * times;
+        const float y = exp2_of(fmaf(s[i / 8][i % 8 * 2 + 1], c2, -low)) * times;
         l += x + y;
         return bf16x2_rne(x, y);
     };
@@ -395,7 +396,11 @@ k_attend_prompt(const AttnArgs a) {
 
     // Rows that do not see all keys of a tile have a weight of zero for the
     // others, which is not enough where a value is not finite: then all of it
-    // again, step by step, with such values left to the rows that see them.
+    // again, step by step, with such values left to the rows that see them and
+    // all weights 2^-kSlack of what they were, so that they are at most 1: the
+    // same bits in the end, and finite sums where only the slack was too much.
+    const float down = exp2_of(-kSlack);
+    float scaled = 1.f;
     float odd = 0.f;                     // (NaN where a sum is not finite)
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
@@ -403,6 +408,7 @@ k_attend_prompt(const AttnArgs a) {
         for (int i = 0; i < 16; ++i) odd = fmaf(o[dt][i], 0.f, odd);
     if (__syncthreads_or(odd != 0.f)) {
         begin();
+        scaled = down;
         for (int i = 0; i < tiles; ++i) {
             if (i && i % 64 == 0) look_up(i);
             copy_all(copy_k, k_rows(i), 0);
@@ -418,7 +424,7 @@ k_attend_prompt(const AttnArgs a) {
             if (__any(top > m + kSlack)) raise(top);
             const float low = finite_max(m);
             u32x4 p[4];
-            each<16>([&](auto j) { p[j / 4][j % 4] = weigh(s, j, low); });
+            each<16>([&](auto j) { p[j / 4][j % 4] = weigh(s, j, low, down); });
             each<4 * DT>([&](auto at) {
                 u32x4 v = v_frag(0, at / DT, at % DT);
                 if (part) {
@@ -465,7 +471,7 @@ k_attend_prompt(const AttnArgs a) {
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<f32x4 *>(a.partial + at * DP + dt * 32 + 2 * i + 4 * h) =
                     f32x4{o[dt][i] * inv, o[dt][i + 1] * inv, o[dt][i + 2] * inv, o[dt][i + 3] * inv};
-        if (h == 0) a.lse[at] = log_weight(m, total, lost);
+        if (h == 0) a.lse[at] = log_weight(m, total / scaled, lost);
     } else {
         uint16_t *out = reinterpret_cast<uint16_t *>(a.o) + int64_t(u.tok0 + tok) * a.ldo +
                         int64_t(head) * D;

@@ -1,12 +1,57 @@
 """Attention where float32's range ends, and rows whose bits follow their own
 keys alone."""
+import math
+
 import pytest
 import torch
 
 from attention_reference import Batch
-from test_gpu_attention import run
+from test_gpu_attention import check, run
 
 pytestmark = pytest.mark.gpu
+
+
+def place(b, s, j):
+    return int(b.pages[s, j // b.page]), j % b.page
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new, kv", [(32, 200), (130, 400), (40, 9000)])
+def test_values_near_the_largest(new, kv, dim):
+    """A key that scores 2^7.8 times the earlier ones' weights, whose value is
+    2^122: a running maximum left where it was would bring its product to
+    2^129.8, and the row to infinity."""
+    b = Batch([new], [kv], heads=4, kv_heads=2, dim=dim, seed=kv)
+    b.q.zero_()
+    b.q.view(b.tokens, 4, dim)[..., 0] = 8.0
+    b.k.copy_(torch.where(b.k.isnan(), b.k, torch.zeros_like(b.k)))
+    page, slot = place(b, 0, 150)
+    b.k[page, :, slot, 0] = 5.4375               # score 5.4375: 2^7.845
+    b.v[page, :, slot] = b.v[page, :, slot].sign() * 2.0 ** 122
+    check(b, run(b, scale=0.125), 0.125)
+
+
+def test_values_near_the_largest_beside_infinite_ones():
+    """The same where a later value, which the last tokens alone see, is
+    infinite: theirs is, the others' are right."""
+    b = Batch([64], [260], heads=2, kv_heads=2, seed=1)
+    b.q.zero_()
+    b.q.view(b.tokens, 2, b.dim)[..., 0] = 8.0
+    b.k.copy_(torch.where(b.k.isnan(), b.k, torch.zeros_like(b.k)))
+    page, slot = place(b, 0, 150)
+    b.k[page, :, slot, 0] = 5.4375
+    b.v[page, :, slot] = b.v[page, :, slot].sign() * 2.0 ** 122
+    clean = run(b, scale=0.125)
+    check(b, clean, 0.125)
+    page, slot = place(b, 0, 250)
+    b.v[page, :, slot, 3] = math.inf
+    o = run(b, scale=0.125)
+    sees = b.seen(0)[:, 250]
+    assert torch.equal(o[~sees], clean[~sees]) and sees.any() and (~sees).any()
+    o, clean = (t.view(b.tokens, 2, b.dim) for t in (o, clean))
+    assert (o[sees][..., 3] == math.inf).all()
+    o[..., 3], clean[..., 3] = 0, 0
+    assert torch.equal(o, clean)
 
 
 @pytest.mark.parametrize("dim", [64, 128])
