@@ -558,7 +558,9 @@ lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
                             void *stream) {
     if (!p) return set_errorf(LORA_EINVAL, "null plan");
     lora_status st;
-    if (!std::isfinite(scale)) return set_errorf(LORA_EINVAL, "scale must be finite");
+    const float scale2 = scale * 1.44269504088896340736f;
+    if (!std::isfinite(scale2))
+        return set_errorf(LORA_EINVAL, "scale must be finite, and its product with log2 e too");
     const int64_t T = int64_t(p->tokens.size()), width = int64_t(p->d.heads) * p->d.head_dim;
     if (T == 0) return LORA_OK;            // empty batch: no tensor is looked at
     const int32_t es = esize(p->d.dtype);
@@ -593,10 +595,12 @@ lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
         a.lse = reinterpret_cast<float *>(ws + side->off_lse);
         a.num_units = int32_t(side->cap_units);
         a.num_joins = int32_t(side->cap_joins);
-        a.scale2 = scale * 1.44269504088896340736f;
-        a.negate = prompt && a.scale2 < 0;
-        // (the least scale leaves masked scores of -inf what they are)
-        if (prompt) a.scale2 = std::max(std::fabs(a.scale2), 1e-30f);
+        a.scale2 = scale2;
+        if (prompt) {
+            a.negate = scale2 < 0;
+            a.zero = scale2 == 0;
+            a.scale2 = a.zero ? 1.0f : std::fabs(scale2);
+        }
         if (e == hipSuccess)
             e = prompt ? lora::launch_attn_prompt(a, s)
                        : lora::launch_attn_rows(p->d.dtype, side->tile_rows, side->waves, a, s);

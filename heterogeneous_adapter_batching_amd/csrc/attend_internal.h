@@ -60,7 +60,10 @@ struct AttnArgs {
     int32_t group, head_dim;
     int32_t causal, window;      // window 0: all keys
     float scale2;                // scale log2 e
-    bool negate;                 // prompts: of -q, so that scale2 is positive
+    // prompts, whose masked scores of -inf a scale has to leave what they are:
+    // of -q, so that scale2 is positive; and of zeros for every finite element of
+    // q where scale2 is zero (1 is passed)
+    bool negate, zero;
 };
 
 // What a head is padded to, and the most rows of a tile of the kernel for few

@@ -120,6 +120,9 @@ k_attend_prompt(const AttnArgs a) {
             const int e = kk * 16 + h * 8;
             q[kk] = u32x4{0u, 0u, 0u, 0u};
             if (row && e < D) q[kk] = *reinterpret_cast<const u32x4 *>(p + e) ^ flip;
+            if (a.zero)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) q[kk][d] &= odd_mask<uint16_t>(q[kk][d]);
         }
     }
     const int last = !row ? -1 : a.causal ? min(u.pos0 + tok, u.key1 - 1) : u.key1 - 1;

@@ -1,5 +1,5 @@
-"""Attention where float32's range ends, and rows whose bits follow their own
-keys alone."""
+"""Attention where float32's range ends: values near its largest, scales of
+zero and next to it; and rows whose bits follow their own keys alone."""
 import math
 
 import pytest
@@ -52,6 +52,27 @@ def test_values_near_the_largest_beside_infinite_ones():
     assert (o[sees][..., 3] == math.inf).all()
     o[..., 3], clean[..., 3] = 0, 0
     assert torch.equal(o, clean)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("scale", [0.0, 1e-36, -1e-36, 1e-38, 2e-40])
+def test_scales_next_to_zero(scale, new, dtype):
+    """Products of 10^36 and more, brought into range (or to nothing) by the
+    scale."""
+    b = Batch([new], [300], dtype=dtype, seed=3)
+    b.q.mul_(1e18)
+    b.k.mul_(1e18)
+    check(b, run(b, scale=scale), scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 60])
+def test_a_scale_of_zero_and_infinite_products(new, dtype):
+    """0 times an infinite product is no number."""
+    b = Batch([new], [300], dtype=dtype, seed=4)
+    b.k[place(b, 0, 7)[0], :, place(b, 0, 7)[1], 5] = math.inf
+    assert run(b, scale=0.0).isnan().all()
 
 
 @pytest.mark.parametrize("dim", [64, 128])
