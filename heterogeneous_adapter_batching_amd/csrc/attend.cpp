@@ -54,9 +54,9 @@ struct Side {
     uint64_t off_units = 0, off_joins = 0, off_partial = 0, off_lse = 0;
 };
 
-}  // namespace
-
-struct attn_plan {
+// What a plan holds of its batch: built as a whole, so that a rebuild that fails
+// leaves the last one.
+struct Batch {
     lora_attn_desc d{};
     int32_t group = 1;
     std::vector<int32_t> new_lens, kv_lens;
@@ -64,7 +64,11 @@ struct attn_plan {
     int32_t most_kv = 0;
     Side rows, prompt;
     uint64_t off_tokens = 0, image_bytes = 0, ws_bytes = 0;
+};
 
+}  // namespace
+
+struct attn_plan : Batch {
     void *ws = nullptr;
     // pinned staging, two buffers in turn: an upload waits only for the copy
     // before last
@@ -138,7 +142,7 @@ lora_status check_lens(const lora_attn_desc &d, const int32_t *new_lens, const i
 }
 
 // The keys that rows row0 .. row1 - 1 see between them, from a whole block on.
-void tile_keys(const attn_plan &p, int32_t s, int64_t row0, int64_t row1, int32_t *lo, int32_t *hi) {
+void tile_keys(const Batch &p, int32_t s, int64_t row0, int64_t row1, int32_t *lo, int32_t *hi) {
     const int32_t kv = p.kv_lens[s], pos0 = kv - p.new_lens[s];
     *lo = 0;
     *hi = kv;
@@ -155,12 +159,12 @@ int64_t blocks_of(int32_t lo, int32_t hi) {
 }
 
 // Whether a sequence of so many rows is a prompt's.
-bool is_prompt(const attn_plan &p, int64_t rows) {
+bool is_prompt(const Batch &p, int64_t rows) {
     return p.d.dtype == LORA_BF16 && rows > lora::attn_rows_most(p.d.dtype, p.d.head_dim);
 }
 
 // fn(sequence, its first token, its rows) for the sequences of one side.
-template <typename Fn> void each_seq(const attn_plan &p, bool prompt, Fn fn) {
+template <typename Fn> void each_seq(const Batch &p, bool prompt, Fn fn) {
     int32_t tok0 = 0;
     for (size_t s = 0; s < p.new_lens.size(); ++s) {
         const int64_t rows = int64_t(p.new_lens[s]) * p.group;
@@ -172,7 +176,7 @@ template <typename Fn> void each_seq(const attn_plan &p, bool prompt, Fn fn) {
 // Cuts every tile's keys into parts, so that the launch has about `target`
 // units, none shorter than `least` keys, and lays them out one after another.
 // The cut is even: no more parts than tiles + target in all.
-void cut(const attn_plan &p, Side *side, bool prompt, int64_t target, int64_t least) {
+void cut(const Batch &p, Side *side, bool prompt, int64_t target, int64_t least) {
     side->units.clear();
     side->joins.clear();
     side->tiles = 0;
@@ -237,11 +241,12 @@ void cut(const attn_plan &p, Side *side, bool prompt, int64_t target, int64_t le
     }
 }
 
-void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, int32_t S) {
+Batch plan_batch(const lora_attn_desc &d, const int32_t *new_lens, const int32_t *kv_lens, int32_t S) {
+    Batch batch, *const p = &batch;
+    p->d = d;
+    p->group = d.heads / d.kv_heads;
     p->new_lens.assign(new_lens, new_lens + S);
     p->kv_lens.assign(kv_lens, kv_lens + S);
-    p->tokens.clear();
-    p->most_kv = 0;
     for (int32_t s = 0; s < S; ++s) {
         p->most_kv = std::max(p->most_kv, kv_lens[s]);
         for (int32_t i = 0; i < new_lens[s]; ++i)
@@ -249,7 +254,6 @@ void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, i
     }
     int64_t few = 0;
     each_seq(*p, false, [&](int32_t, int32_t, int64_t rows) { few = std::max(few, rows); });
-    p->rows = Side{};
     // (float32 chunks: large tiles read keys less often, small ones use more of
     // the chip)
     p->rows.tile_rows = few <= 16 ? 16 : few <= 32 ? 32 : lora::attn_rows_most(p->d.dtype, p->d.head_dim);
@@ -275,7 +279,6 @@ void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, i
                         ? lora::kManyWaves
                         : 4;
     cut(*p, &p->rows, false, kRowsUnits, p->rows.waves == 4 ? kRowsKeys : kShortKeys);
-    p->prompt = Side{};
     p->prompt.tile_rows = lora::kPromptRows;
     cut(*p, &p->prompt, true, kPromptUnits, kPromptKeys);
 
@@ -297,15 +300,7 @@ void plan_build(attn_plan *p, const int32_t *new_lens, const int32_t *kv_lens, i
         side->off_lse = place(rows * 4);
     }
     p->ws_bytes = at;
-}
-
-void plan_clear(attn_plan *p) {
-    p->new_lens.clear();
-    p->kv_lens.clear();
-    p->tokens.clear();
-    p->most_kv = 0;
-    p->rows = p->prompt = Side{};
-    p->image_bytes = p->ws_bytes = 0;
+    return batch;
 }
 
 bool aligned(const void *ptr, int64_t bytes) {
@@ -345,7 +340,7 @@ bool overlap(const Rows &a, const Rows &b, int64_t T, int32_t es) {
 // The cache and its page table; and whether the tensors beside them (T rows
 // each) lie apart from it.  A cache that is written has a place for each key and
 // each value.
-lora_status check_cache(const attn_plan &p, const lora_kv_cache *c, const int32_t *pages,
+lora_status check_cache(const Batch &p, const lora_kv_cache *c, const int32_t *pages,
                         int64_t ld_pages, int32_t pages_per_seq, bool written,
                         std::initializer_list<Rows> beside) {
     if (!c) return set_errorf(LORA_EINVAL, "null cache");
@@ -406,7 +401,7 @@ lora_status check_uploaded(const attn_plan *p) {
     return LORA_OK;
 }
 
-lora::CacheArgs cache_args(const attn_plan &p, const lora_kv_cache &c) {
+lora::CacheArgs cache_args(const Batch &p, const lora_kv_cache &c) {
     lora::CacheArgs a{};
     a.k = static_cast<uint8_t *>(c.k);
     a.v = static_cast<uint8_t *>(c.v);
@@ -442,9 +437,7 @@ lora_status attn_plan_create(attn_plan **out, const lora_attn_desc *d, const int
     if ((st = check_lens(*d, new_lens, kv_lens, num_seqs)) != LORA_OK) return st;
     return guarded([&] {
         std::unique_ptr<attn_plan> p(new attn_plan());
-        p->d = *d;
-        p->group = d->heads / d->kv_heads;
-        plan_build(p.get(), new_lens, kv_lens, num_seqs);
+        static_cast<Batch &>(*p) = plan_batch(*d, new_lens, kv_lens, num_seqs);
         *out = p.release();
         return LORA_OK;
     });
@@ -455,14 +448,9 @@ lora_status attn_plan_rebuild(attn_plan *p, const int32_t *new_lens, const int32
     if (!p) return set_errorf(LORA_EINVAL, "null plan");
     const lora_status st = check_lens(p->d, new_lens, kv_lens, num_seqs);
     if (st != LORA_OK) return st;
-    p->ws = nullptr;                       // its tables are the last batch's
     return guarded([&] {
-        try {
-            plan_build(p, new_lens, kv_lens, num_seqs);
-        } catch (...) {
-            plan_clear(p);                 // of no tokens, rather than of half a batch
-            throw;
-        }
+        static_cast<Batch &>(*p) = plan_batch(p->d, new_lens, kv_lens, num_seqs);
+        p->ws = nullptr;                   // its tables are the last batch's
         return LORA_OK;
     });
 }

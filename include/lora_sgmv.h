@@ -722,7 +722,8 @@ typedef struct {
  * parts of about equal size, also when one sequence is much longer than the
  * others.  At most 2^23 tokens, and tiles of 16 rows (a token's query heads of
  * one key head) over all key heads; at most 2^30 keys a sequence.
- * attn_plan_rebuild re-plans in place; attn_plan_upload copies the tables into
+ * attn_plan_rebuild re-plans in place (an error leaves the plan as it was);
+ * attn_plan_upload copies the tables into
  * `ws` (256-byte aligned, attn_plan_workspace_bytes) on `stream`, from one of
  * two pinned buffers in turn.  A call with a plan that was rebuilt since, or
  * whose workspace another plan has been uploaded to, is refused (LORA_ESTATE).
