@@ -9,8 +9,6 @@
 #include <initializer_list>
 #include <iterator>
 #include <memory>
-#include <mutex>
-#include <unordered_map>
 #include <vector>
 
 #include <hip/hip_runtime.h>
@@ -79,16 +77,6 @@ struct attn_plan : Batch {
 };
 
 namespace {
-
-// Which plan's tables each workspace holds: the last one uploaded into it.
-std::mutex g_mutex;
-std::unordered_map<const void *, const attn_plan *> g_owner;
-
-bool owns_workspace(const attn_plan *pl) {
-    std::lock_guard<std::mutex> lock(g_mutex);
-    const auto it = g_owner.find(pl->ws);
-    return it != g_owner.end() && it->second == pl;
-}
 
 lora_status check_attn_desc(const lora_attn_desc *d) {
     if (!d) return set_errorf(LORA_EINVAL, "null attention descriptor");
@@ -321,13 +309,37 @@ lora_status check_rows(const Rows &r, int32_t es) {
                           "to 2^36", r.name, (long long)r.ld, (long long)r.width);
     return LORA_OK;
 }
+// The bytes that T rows span, T > 0.
+struct Bytes {
+    uintptr_t lo, hi;
+};
+Bytes bytes_of(const Rows &r, int64_t T, int32_t es) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(r.ptr);
+    return {lo, lo + uint64_t((T - 1) * r.ld + r.width) * es};
+}
+// Keys or values of a cache.
+struct CacheSide {
+    const char *name;
+    const void *ptr;
+    int64_t page, head, tok;
+};
+CacheSide k_side(const lora_kv_cache &c) {
+    return {"k_cache", c.k, c.k_page_stride, c.k_head_stride, c.k_token_stride};
+}
+CacheSide v_side(const lora_kv_cache &c) {
+    return {"v_cache", c.v, c.v_page_stride, c.v_head_stride, c.v_token_stride};
+}
+Bytes bytes_of(const Batch &p, const lora_kv_cache &c, const CacheSide &t) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(t.ptr);
+    return {lo, lo + uint64_t((c.num_pages - 1) * t.page + (p.d.kv_heads - 1) * t.head +
+                              (p.d.page_size - 1) * t.tok + p.d.head_dim) * esize(p.d.dtype)};
+}
 // Whether two matrices of T rows reach into each other: column slices of the
 // same rows do not.
 bool overlap(const Rows &a, const Rows &b, int64_t T, int32_t es) {
     if (!a.ptr || !b.ptr || T <= 0) return false;
-    const uint64_t alo = reinterpret_cast<uintptr_t>(a.ptr), blo = reinterpret_cast<uintptr_t>(b.ptr);
-    const uint64_t ahi = alo + uint64_t((T - 1) * a.ld + a.width) * es;
-    const uint64_t bhi = blo + uint64_t((T - 1) * b.ld + b.width) * es;
+    const auto [alo, ahi] = bytes_of(a, T, es);
+    const auto [blo, bhi] = bytes_of(b, T, es);
     if (ahi <= blo || bhi <= alo) return false;
     if (T > 1 && a.ld == b.ld) {
         const uint64_t l = uint64_t(a.ld) * es;
@@ -346,13 +358,7 @@ lora_status check_cache(const Batch &p, const lora_kv_cache *c, const int32_t *p
     if (!c) return set_errorf(LORA_EINVAL, "null cache");
     const int32_t es = esize(p.d.dtype);
     if (c->num_pages < 1) return set_errorf(LORA_EINVAL, "a cache of %d pages", c->num_pages);
-    const struct {
-        const char *name;
-        const void *ptr;
-        int64_t page, head, tok;
-    } side[2] = {{"k_cache", c->k, c->k_page_stride, c->k_head_stride, c->k_token_stride},
-                 {"v_cache", c->v, c->v_page_stride, c->v_head_stride, c->v_token_stride}};
-    for (const auto &t : side) {
+    for (const CacheSide &t : {k_side(*c), v_side(*c)}) {
         if (!t.ptr || !aligned(t.ptr, 16))
             return set_errorf(LORA_EINVAL, "%s must be non-null and 16-byte aligned", t.name);
         for (int64_t st : {t.page, t.head, t.tok})
@@ -369,13 +375,10 @@ lora_status check_cache(const Batch &p, const lora_kv_cache *c, const int32_t *p
         if (t.tok < p.d.head_dim || t.tok * es * 16 >= (int64_t(1) << 31))
             return set_errorf(LORA_EINVAL, "%s: tokens %lld elements apart, heads of %d", t.name,
                               (long long)t.tok, p.d.head_dim);
-        const uint64_t lo = reinterpret_cast<uintptr_t>(t.ptr);
-        const uint64_t hi = lo + uint64_t((c->num_pages - 1) * t.page + (p.d.kv_heads - 1) * t.head +
-                                          (p.d.page_size - 1) * t.tok + p.d.head_dim) * es;
+        const Bytes all = bytes_of(p, *c, t);
         for (const Rows &r : beside) {
-            const uint64_t at = reinterpret_cast<uintptr_t>(r.ptr);
-            const uint64_t end = at + uint64_t((int64_t(p.tokens.size()) - 1) * r.ld + r.width) * es;
-            if (r.ptr && at < hi && lo < end)
+            const Bytes rows = bytes_of(r, int64_t(p.tokens.size()), es);
+            if (r.ptr && rows.lo < all.hi && all.lo < rows.hi)
                 return set_errorf(LORA_EINVAL, "%s overlaps %s", r.name, t.name);
         }
     }
@@ -393,11 +396,26 @@ lora_status check_cache(const Batch &p, const lora_kv_cache *c, const int32_t *p
     return LORA_OK;
 }
 
-lora_status check_uploaded(const attn_plan *p) {
+// The plan's workspace holds its tables, and the call's tensors and cache (null:
+// none) lie apart from it.
+lora_status check_uploaded(const attn_plan *p, const lora_kv_cache *c, std::initializer_list<Rows> beside) {
     if (!p->ws) return set_errorf(LORA_ESTATE, "plan has not been uploaded");
-    if (!owns_workspace(p))
+    if (!lora::owns_workspace(p, p->ws))
         return set_errorf(LORA_ESTATE, "the plan's workspace holds another plan's tables since "
                           "(upload this plan again)");
+    const int32_t es = esize(p->d.dtype);
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p->ws), hi = lo + attn_plan_workspace_bytes(p);
+    const auto apart = [&](const char *name, const Bytes &b) {
+        return b.lo >= hi || lo >= b.hi
+                   ? LORA_OK
+                   : set_errorf(LORA_EINVAL, "%s overlaps the plan's workspace", name);
+    };
+    lora_status st = LORA_OK;
+    for (const Rows &r : beside)
+        if (r.ptr && (st = apart(r.name, bytes_of(r, int64_t(p->tokens.size()), es))) != LORA_OK) return st;
+    if (c && ((st = apart("k_cache", bytes_of(*p, *c, k_side(*c)))) != LORA_OK ||
+              (st = apart("v_cache", bytes_of(*p, *c, v_side(*c)))) != LORA_OK))
+        return st;
     return LORA_OK;
 }
 
@@ -457,11 +475,7 @@ lora_status attn_plan_rebuild(attn_plan *p, const int32_t *new_lens, const int32
 
 lora_status attn_plan_destroy(attn_plan *p) {
     if (!p) return LORA_OK;
-    {
-        std::lock_guard<std::mutex> lock(g_mutex);
-        for (auto it = g_owner.begin(); it != g_owner.end();)
-            it = it->second == p ? g_owner.erase(it) : std::next(it);
-    }
+    lora::release_workspaces(p);
     for (int i = 0; i < 2; ++i) {
         // (a copy out of the buffer may still be queued)
         if (p->staged[i]) {
@@ -534,8 +548,7 @@ lora_status attn_plan_upload(attn_plan *p, void *ws, uint64_t ws_bytes, void *st
         if (e != hipSuccess) return set_errorf(LORA_EHIP, "plan upload: %s", hipGetErrorString(e));
         p->next_staging = 1 - k;
         p->ws = ws;
-        std::lock_guard<std::mutex> lock(g_mutex);
-        g_owner[ws] = p;
+        lora::claim_workspace(p, ws, attn_plan_workspace_bytes(p));
         return LORA_OK;
     });
 }
@@ -558,7 +571,7 @@ lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
     if (overlap(rq, ro, T, es)) return set_errorf(LORA_EINVAL, "o overlaps q");
     if ((st = check_cache(*p, cache, pages, ld_pages, pages_per_seq, false, {ro})) != LORA_OK)
         return st;
-    if ((st = check_uploaded(p)) != LORA_OK) return st;
+    if ((st = check_uploaded(p, cache, {rq, ro})) != LORA_OK) return st;
 
     uint8_t *ws = static_cast<uint8_t *>(p->ws);
     lora::AttnArgs a{};
@@ -677,7 +690,7 @@ lora_status rotary_append(const attn_plan *p, const lora_rotary_desc *r, const v
     if (positions && !aligned(positions, 4))
         return set_errorf(LORA_EINVAL, "positions must be 4-byte aligned");
     if (freqs && !aligned(freqs, 8)) return set_errorf(LORA_EINVAL, "freqs must be 8-byte aligned");
-    if ((st = check_uploaded(p)) != LORA_OK) return st;
+    if ((st = check_uploaded(p, cache, {rq, ro, rk, rv})) != LORA_OK) return st;
 
     lora::RotaryArgs a{};
     if (cache) a.cache = cache_args(*p, *cache);

@@ -950,18 +950,40 @@ lora_status plan_create(lora_plan **out, const lora_pool *p, int32_t T, const in
     return LORA_OK;
 }
 
-// Which plan's tables each workspace holds: the last plan uploaded into it.
-// A call with a plan whose workspace has since received another plan's
-// tables is refused (it would read the other plan's descriptors).
-std::mutex g_ws_mutex;
-std::unordered_map<const void *, const lora_plan *> g_ws_owner;
-
-bool owns_workspace(const lora_plan *pl) {
-    std::lock_guard<std::mutex> lock(g_ws_mutex);
-    auto it = g_ws_owner.find(pl->ws);
-    return it != g_ws_owner.end() && it->second == pl;
-}
 }  // namespace
+
+namespace lora {
+namespace {
+// Claimed workspaces by their first byte: no two of them overlap.
+struct Claim {
+    uintptr_t end;
+    const void *plan;
+};
+std::mutex g_ws_mutex;
+std::map<uintptr_t, Claim> g_ws_claims;
+}  // namespace
+
+void claim_workspace(const void *plan, const void *ws, uint64_t bytes) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(ws), hi = lo + std::max<uint64_t>(bytes, 1);
+    std::lock_guard<std::mutex> lock(g_ws_mutex);
+    auto it = g_ws_claims.upper_bound(lo);
+    if (it != g_ws_claims.begin() && std::prev(it)->second.end > lo) --it;
+    while (it != g_ws_claims.end() && it->first < hi) it = g_ws_claims.erase(it);
+    g_ws_claims.emplace(lo, Claim{hi, plan});
+}
+
+bool owns_workspace(const void *plan, const void *ws) {
+    std::lock_guard<std::mutex> lock(g_ws_mutex);
+    const auto it = g_ws_claims.find(reinterpret_cast<uintptr_t>(ws));
+    return it != g_ws_claims.end() && it->second.plan == plan;
+}
+
+void release_workspaces(const void *plan) {
+    std::lock_guard<std::mutex> lock(g_ws_mutex);
+    for (auto it = g_ws_claims.begin(); it != g_ws_claims.end();)
+        it = it->second.plan == plan ? g_ws_claims.erase(it) : std::next(it);
+}
+}  // namespace lora
 
 extern "C" {
 
@@ -1040,11 +1062,7 @@ lora_status lora_plan_destroy(lora_plan *pl) {
         }
         if (pl->staging[i]) (void)hipHostFree(pl->staging[i]);
     }
-    {
-        std::lock_guard<std::mutex> lock(g_ws_mutex);
-        for (auto it = g_ws_owner.begin(); it != g_ws_owner.end();)
-            it = it->second == pl ? g_ws_owner.erase(it) : std::next(it);
-    }
+    lora::release_workspaces(pl);
     delete pl;
     return LORA_OK;
 }
@@ -1174,10 +1192,7 @@ lora_status lora_plan_upload(lora_plan *pl, void *ws, uint64_t ws_bytes, int32_t
     pl->max_proj = max_proj;
     pl->lay = lay;
     pl->part_layer = -1;               // a new workspace holds no partials
-    {
-        std::lock_guard<std::mutex> lock(g_ws_mutex);
-        g_ws_owner[ws] = pl;
-    }
+    lora::claim_workspace(pl, ws, lay.ws_bytes);
     return LORA_OK;
 }
 
@@ -1229,7 +1244,7 @@ lora_status check_call(const lora_pool *p, const lora_plan *pl, int32_t layer, i
     if (pl->pool_generation != p->generation)
         return fail(LORA_ESTATE, "an adapter was unregistered after the plan was built");
     if (!pl->ws) return fail(LORA_ESTATE, "plan has not been uploaded");
-    if (!owns_workspace(pl))
+    if (!lora::owns_workspace(pl, pl->ws))
         return fail(LORA_ESTATE, "the plan's workspace holds another plan's tables since "
                                  "(upload this plan again)");
     if (layer < 0 || layer >= p->d.num_layers)

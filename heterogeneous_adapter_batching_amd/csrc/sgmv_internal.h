@@ -438,6 +438,14 @@ hipError_t launch_expand_merge(int dtype, int nvm, int max_tok, const MergeArgs 
 constexpr uint64_t kStaticScratchBytes = uint64_t(LORA_STATIC_SCRATCH_MIB) << 20;
 hipError_t static_scratch(void **ptr, uint64_t *bytes);
 
+// Which plan's tables a device workspace holds, for plans of every kind: the
+// last one uploaded into it.  An upload claims the bytes that its plan uses,
+// and whoever held some of them no longer does: a call with such a plan would
+// read another's descriptors, and is refused.
+void claim_workspace(const void *plan, const void *ws, uint64_t bytes);
+bool owns_workspace(const void *plan, const void *ws);
+void release_workspaces(const void *plan);
+
 // Whether the kernels were built with LORA_SGMV_DEBUG, and the current
 // device's debug error bits (after waiting for the device), cleared on request.
 bool debug_build();

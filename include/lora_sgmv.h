@@ -397,8 +397,8 @@ uint64_t lora_workspace_bytes(const lora_pool *p, int32_t num_tokens, int32_t nu
  * scratch for the shrink's partial sums); calls must be ordered after this
  * upload, and calls that share `ws` must not run concurrently.  A workspace
  * holds the tables of the plan uploaded into it last: a call with another
- * plan that was uploaded into it before is refused with LORA_ESTATE (upload
- * that plan again).  Errors: LORA_EINVAL (bad max_proj, null or misaligned
+ * plan (an attention plan too) that was uploaded into any of the bytes before
+ * is refused with LORA_ESTATE (upload that plan again).  Errors: LORA_EINVAL (bad max_proj, null or misaligned
  * ws), LORA_ESTATE (ws_bytes too small), LORA_EHIP. */
 lora_status lora_plan_upload(lora_plan *pl, void *ws, uint64_t ws_bytes, int32_t max_proj,
                              void *stream);
@@ -723,10 +723,11 @@ typedef struct {
  * others.  At most 2^23 tokens, and tiles of 16 rows (a token's query heads of
  * one key head) over all key heads; at most 2^30 keys a sequence.
  * attn_plan_rebuild re-plans in place (an error leaves the plan as it was);
- * attn_plan_upload copies the tables into
- * `ws` (256-byte aligned, attn_plan_workspace_bytes) on `stream`, from one of
- * two pinned buffers in turn.  A call with a plan that was rebuilt since, or
- * whose workspace another plan has been uploaded to, is refused (LORA_ESTATE).
+ * attn_plan_upload copies the tables into `ws` (256-byte aligned,
+ * attn_plan_workspace_bytes) on `stream`, from one of two pinned buffers in
+ * turn.  A call with a plan that was rebuilt since, or that another plan, of
+ * either kind, has been uploaded over in part or whole, is refused
+ * (LORA_ESTATE); so is one whose tensors reach into the workspace (LORA_EINVAL).
  * A captured graph keeps the launches it was captured with.  With max_kv they
  * depend on new_lens (and max_kv) alone: such a graph may be replayed after a
  * rebuild with the same new_lens and an upload into the same workspace.

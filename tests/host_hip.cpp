@@ -1,0 +1,34 @@
+// The HIP runtime calls of the library's host sources, on host memory: the
+// host code's uploads and checks can then be run whole on a machine without a
+// GPU.  Kernels cannot (their launchers are host_only.cpp's, which fail), so a
+// call whose arguments hold ends with LORA_EHIP.
+#include <cstdlib>
+#include <cstring>
+
+#include <hip/hip_runtime.h>
+
+extern "C" {
+hipError_t hipHostMalloc(void **p, size_t n, unsigned) {
+    *p = std::malloc(n);
+    return *p ? hipSuccess : hipErrorOutOfMemory;
+}
+hipError_t hipHostFree(void *p) {
+    std::free(p);
+    return hipSuccess;
+}
+hipError_t hipMemcpyAsync(void *to, const void *from, size_t n, hipMemcpyKind, hipStream_t) {
+    std::memcpy(to, from, n);
+    return hipSuccess;
+}
+hipError_t hipEventCreateWithFlags(hipEvent_t *e, unsigned) {
+    *e = reinterpret_cast<hipEvent_t>(1);
+    return hipSuccess;
+}
+hipError_t hipEventDestroy(hipEvent_t) { return hipSuccess; }
+hipError_t hipEventQuery(hipEvent_t) { return hipSuccess; }
+hipError_t hipEventRecord(hipEvent_t, hipStream_t) { return hipSuccess; }
+hipError_t hipEventSynchronize(hipEvent_t) { return hipSuccess; }
+hipError_t hipStreamSynchronize(hipStream_t) { return hipSuccess; }
+hipError_t hipStreamWaitEvent(hipStream_t, hipEvent_t, unsigned) { return hipSuccess; }
+const char *hipGetErrorString(hipError_t) { return "no GPU"; }
+}
