@@ -349,6 +349,67 @@ bool overlap(const Rows &a, const Rows &b, int64_t T, int32_t es) {
     return true;
 }
 
+// Whether two different places of one side of the cache have elements in common:
+// |dp page + dh head + dt tok - shift| < head_dim for distances within its pages,
+// heads and tokens, not all zero.  With `same`, all zero counts too: whether
+// places of a side and of another, with the same strides and `shift` elements
+// on, do.  Strides of which each reaches past all that the smaller ones span
+// answer it at once; else every distance along the two shorter dimensions is
+// looked at, and the third solved for.
+bool meet(const Batch &p, const lora_kv_cache &c, const CacheSide &t, int64_t shift, bool same) {
+    struct Dim {
+        int64_t stride, count;
+    };
+    Dim d[4] = {{t.page, c.num_pages}, {t.head, p.d.kv_heads}, {t.tok, p.d.page_size},
+                {std::abs(shift), same ? 2 : 1}};
+    const int64_t D = p.d.head_dim;
+    std::sort(d, d + 4, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
+    int64_t span = D;
+    bool nested = true;
+    for (const Dim &x : d)
+        if (x.count > 1) {
+            nested &= x.stride >= span;
+            span += (x.count - 1) * x.stride;
+        }
+    if (nested) return false;
+    Dim e[3] = {{t.page, c.num_pages}, {t.head, p.d.kv_heads}, {t.tok, p.d.page_size}};
+    std::sort(e, e + 3, [](const Dim &a, const Dim &b) { return a.count < b.count; });
+    const Dim &x = e[0], &y = e[1], &z = e[2];
+    for (int64_t i = 1 - x.count; i < x.count; ++i)
+        for (int64_t j = 1 - y.count; j < y.count; ++j) {
+            // the distances k along z with |k z - rest| < D
+            const int64_t rest = shift - i * x.stride - j * y.stride;
+            if (z.stride == 0) {
+                if (std::abs(rest) < D && (same || i || j || z.count > 1)) return true;
+                continue;
+            }
+            int64_t k = (rest - D) / z.stride - 1;
+            for (k = std::max(k, 1 - z.count); k < z.count && k * z.stride < rest + D; ++k)
+                if (std::abs(k * z.stride - rest) < D && (same || i || j || k)) return true;
+        }
+    return false;
+}
+
+// Whether no place of the keys has an element in common with one of the values:
+// they lie apart as wholes, or have the same strides and do not meet, or the
+// same page stride and lie apart within it.
+bool sides_apart(const Batch &p, const lora_kv_cache &c) {
+    const CacheSide k = k_side(c), v = v_side(c);
+    const Bytes kb = bytes_of(p, c, k), vb = bytes_of(p, c, v);
+    if (kb.hi <= vb.lo || vb.hi <= kb.lo) return true;
+    const int64_t es = esize(p.d.dtype);
+    const int64_t bytes = vb.lo >= kb.lo ? int64_t(vb.lo - kb.lo) : -int64_t(kb.lo - vb.lo);
+    if (bytes % es == 0 && (c.num_pages == 1 || k.page == v.page) &&
+        (p.d.kv_heads == 1 || k.head == v.head) && k.tok == v.tok)
+        return !meet(p, c, k, bytes / es, true);
+    if (c.num_pages == 1 || k.page != v.page) return false;
+    const auto in_page = [&](const CacheSide &t) {
+        return ((p.d.kv_heads - 1) * t.head + (p.d.page_size - 1) * t.tok + p.d.head_dim) * es;
+    };
+    const int64_t page = k.page * es, at = (bytes % page + page) % page;
+    return at >= in_page(k) && at + in_page(v) <= page;
+}
+
 // The cache and its page table; and whether the tensors beside them (T rows
 // each) lie apart from it.  A cache that is written has a place for each key and
 // each value.
@@ -368,13 +429,13 @@ lora_status check_cache(const Batch &p, const lora_kv_cache *c, const int32_t *p
         if (t.page > kMostCache / c->num_pages)
             return set_errorf(LORA_EINVAL, "%s: %d pages, %lld elements apart", t.name, c->num_pages,
                               (long long)t.page);
-        if (written && ((c->num_pages > 1 && t.page < p.d.head_dim) ||
-                        (p.d.kv_heads > 1 && t.head < p.d.head_dim)))
-            return set_errorf(LORA_EINVAL, "places of %s coincide: pages %lld and heads %lld elements "
-                              "apart", t.name, (long long)t.page, (long long)t.head);
         if (t.tok < p.d.head_dim || t.tok * es * 16 >= (int64_t(1) << 31))
             return set_errorf(LORA_EINVAL, "%s: tokens %lld elements apart, heads of %d", t.name,
                               (long long)t.tok, p.d.head_dim);
+        if (written && meet(p, *c, t, 0, false))
+            return set_errorf(LORA_EINVAL, "places of %s coincide: pages %lld, heads %lld, tokens %lld "
+                              "elements apart", t.name, (long long)t.page, (long long)t.head,
+                              (long long)t.tok);
         const Bytes all = bytes_of(p, *c, t);
         for (const Rows &r : beside) {
             const Bytes rows = bytes_of(r, int64_t(p.tokens.size()), es);
@@ -384,7 +445,8 @@ lora_status check_cache(const Batch &p, const lora_kv_cache *c, const int32_t *p
     }
     if (!pages || !aligned(pages, 4))
         return set_errorf(LORA_EINVAL, "the page table must be non-null and 4-byte aligned");
-    if (written && c->k == c->v) return set_errorf(LORA_EINVAL, "k_cache is v_cache");
+    if (written && !sides_apart(p, *c))
+        return set_errorf(LORA_EINVAL, "places of k_cache and v_cache coincide");
     if (ld_pages < pages_per_seq || ld_pages > kMostStride)
         return set_errorf(LORA_EINVAL, "ld of the page table (%lld) is not from its %d pages to 2^36",
                           (long long)ld_pages, pages_per_seq);

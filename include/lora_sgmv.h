@@ -814,8 +814,10 @@ typedef struct {
  * A token whose page the table gives as less than 0 or num_pages and more is
  * not stored, nor one in front of its sequence's first key (a graph replayed
  * after a plan that is not causal was rebuilt for fewer keys than new tokens).
- * Two tokens of one batch must not share a place in the cache; a cache whose
- * heads or pages coincide, or whose k is v, is refused.
+ * Two tokens of one batch must not share a place in the cache; a cache in which
+ * two places have elements in common, of keys, of values, or of one and the
+ * other, is refused.  (Keys and values with different strides that reach into
+ * each other have to have the same page stride and lie apart within a page.)
  * Rows from the plan's last token on are not touched.  Sequences as the plan
  * says, their last new_lens[s] keys being the new ones (a plan that is not
  * causal too).  Alignment as paged_attention.
