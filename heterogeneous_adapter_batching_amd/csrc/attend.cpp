@@ -496,6 +496,16 @@ lora::CacheArgs cache_args(const Batch &p, const lora_kv_cache &c) {
     return a;
 }
 
+// What the debug build checks a call's table entries against.
+hipError_t bounds_of(const Batch &p, int32_t pages_per_seq, lora::AttnBounds *b) {
+    b->tokens = int32_t(p.tokens.size());
+    b->seqs = int32_t(p.new_lens.size());
+    b->kv_heads = p.d.kv_heads;
+    b->group = p.group;
+    b->keys = int64_t(pages_per_seq) * p.d.page_size;
+    return lora::debug_word(&b->word);
+}
+
 // A C entry ends with a status whatever happens below it.
 template <typename Fn> lora_status guarded(Fn fn) {
     try {
@@ -649,7 +659,7 @@ lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
     a.causal = p->d.causal;
     a.window = p->d.window;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e = hipSuccess;
+    hipError_t e = bounds_of(*p, pages_per_seq, &a.dbg);
     for (const Side *side : {&p->rows, &p->prompt}) {
         const bool prompt = side == &p->prompt;
         a.units = reinterpret_cast<const AttnUnit *>(ws + side->off_units);
@@ -658,6 +668,7 @@ lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
         a.lse = reinterpret_cast<float *>(ws + side->off_lse);
         a.num_units = int32_t(side->cap_units);
         a.num_joins = int32_t(side->cap_joins);
+        a.dbg.slots = side->cap_slots;
         a.scale2 = scale2;
         if (prompt) {
             a.negate = scale2 < 0;
@@ -776,7 +787,8 @@ lora_status rotary_append(const attn_plan *p, const lora_rotary_desc *r, const v
     a.rotary_dim = freqs ? r->rotary_dim : 0;
     a.layout = r->layout;
     a.magnitude = r->magnitude;
-    const hipError_t e = lora::launch_rotary(p->d.dtype, a, static_cast<hipStream_t>(stream));
+    hipError_t e = bounds_of(*p, pages_per_seq, &a.dbg);
+    if (e == hipSuccess) e = lora::launch_rotary(p->d.dtype, a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return set_errorf(LORA_EHIP, "rotary launch: %s", hipGetErrorString(e));
     return LORA_OK;
 }

@@ -49,7 +49,7 @@ __global__ __launch_bounds__(NW * kWaveSize, sizeof(T) == 2 && DP <= 128 ? 2 : 1
     __shared__ float sm[NW][16], sl[NW][16];
 
     const AttnUnit u = load_invariant(a.units + blockIdx.x);
-    if (u.seq < 0) return;
+    if (!held(a.dbg, u) || u.seq < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
     const int n = lane & 15, g = lane >> 4;
     const int D = a.head_dim;
@@ -334,7 +334,7 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a, int tile_
     constexpr int OW = DP / 16, ROWS = 16 / WAYS;
     __shared__ float tops[16], totals[WAYS > 1 ? 16 : 1], sums[WAYS > 1 ? 16 : 1][DP + 4];
     const AttnJoin j = load_invariant(a.joins + blockIdx.x);
-    if (j.slots <= 0 || j.row0 + int(blockIdx.y) * ROWS >= j.rows) return;
+    if (!held(a.dbg, j) || j.slots <= 0 || j.row0 + int(blockIdx.y) * ROWS >= j.rows) return;
     const int group = threadIdx.x >> 4, way = group % WAYS, col = (threadIdx.x & 15) * OW;
     const int row = int(blockIdx.y) * ROWS + group / WAYS, rr = j.row0 + row;
     const bool ok = row < tile_rows && rr < j.rows;

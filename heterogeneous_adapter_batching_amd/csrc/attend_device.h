@@ -11,6 +11,22 @@ namespace {
 
 constexpr float kNone = -__builtin_inff();   // the score of a key that a row does not see
 
+// Whether a table entry may be followed (debug build; one that may not is noted).
+#ifdef LORA_SGMV_DEBUG
+constexpr bool kDebug = true;
+#else
+constexpr bool kDebug = false;
+#endif
+template <typename Entry>
+__device__ __forceinline__ bool held([[maybe_unused]] const AttnBounds &b, [[maybe_unused]] const Entry &e) {
+    if constexpr (kDebug) {
+        const uint32_t bits = wrong(b, e);
+        if (bits) atomicOr(b.word, bits);
+        return bits == 0;
+    }
+    return true;
+}
+
 // fn over both halves of the wave's rows of 16 lanes: lanes l, l ^ 16, l ^ 32
 // and l ^ 48 end with the same value.
 template <typename Fn> __device__ __forceinline__ float over_groups(float v, Fn fn) {

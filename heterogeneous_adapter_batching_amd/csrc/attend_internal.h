@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include "lora_sgmv.h"
+#include "sgmv_internal.h"
 
 namespace lora {
 
@@ -38,6 +39,41 @@ struct AttnToken {
 constexpr int kAttnPage = 16;    // pages hold a multiple of this many tokens
 constexpr int kAttnBlock = 64;   // unit boundaries are multiples of this many keys
 
+// What the debug build checks every table entry against before it is followed
+// (LORA_SGMV_DEBUG): the batch, a sequence's row of the page table, the partial
+// sums.  The word notes what failed (debug_word).
+struct AttnBounds {
+    int32_t tokens, seqs, kv_heads, group;
+    int64_t keys;                // that pages_per_seq pages hold
+    int64_t slots;
+    uint32_t *word;
+};
+// The bits of what does not hold, 0 if all does (no sum can overflow, whatever
+// the plan's memory has).
+constexpr uint32_t wrong_tile(const AttnBounds &b, int32_t tok0, int32_t kv_head, int32_t row0,
+                              int32_t rows) {
+    return kv_head >= 0 && kv_head < b.kv_heads && tok0 >= 0 && row0 >= 0 && row0 <= rows &&
+                   tok0 + (int64_t(rows) + b.group - 1) / b.group <= b.tokens
+               ? 0u
+               : kDbgToken;
+}
+constexpr uint32_t wrong(const AttnBounds &b, const AttnUnit &u) {
+    if (u.seq == -1) return 0u;
+    return wrong_tile(b, u.tok0, u.kv_head, u.row0, u.rows) |
+           (u.seq >= 0 && u.seq < b.seqs && u.key0 >= 0 && u.key0 % kAttnBlock == 0 &&
+                    u.key1 <= b.keys && (u.slot == -1 || (u.slot >= 0 && u.slot < b.slots))
+                ? 0u
+                : kDbgRow);
+}
+constexpr uint32_t wrong(const AttnBounds &b, const AttnJoin &j) {
+    if (j.slots == 0) return 0u;
+    return wrong_tile(b, j.tok0, j.kv_head, j.row0, j.rows) |
+           (j.slots > 0 && j.slot0 >= 0 && int64_t(j.slot0) + j.slots <= b.slots ? 0u : kDbgRow);
+}
+constexpr uint32_t wrong(const AttnBounds &b, const AttnToken &t) {
+    return t.seq >= 0 && t.seq < b.seqs && t.pos < b.keys ? 0u : kDbgRow;
+}
+
 // One head's rows of the cache, in elements.
 struct CacheArgs {
     uint8_t *k, *v;
@@ -64,6 +100,7 @@ struct AttnArgs {
     // of -q, so that scale2 is positive; and of zeros for every finite element of
     // q where scale2 is zero (1 is passed)
     bool negate, zero;
+    AttnBounds dbg;
 };
 
 // What a head is padded to, and the most rows of a tile of the kernel for few
@@ -96,6 +133,7 @@ struct RotaryArgs {
     int32_t T, heads, kv_heads, head_dim, rotary_dim;
     int32_t layout;              // lora_rotary_layout
     float magnitude;
+    AttnBounds dbg;
 };
 hipError_t launch_rotary(int dtype, const RotaryArgs &a, hipStream_t s);
 

@@ -100,7 +100,7 @@ k_attend_prompt(const AttnArgs a) {
     __shared__ __align__(1024) uint8_t lds[4 * STAGE];   // two of K, two of V
 
     const AttnUnit u = load_invariant(a.units + blockIdx.x);
-    if (u.seq < 0) return;
+    if (!held(a.dbg, u) || u.seq < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
     const int n = lane & 31, h = lane >> 5;
     const int D = a.head_dim;

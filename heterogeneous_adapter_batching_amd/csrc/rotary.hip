@@ -14,8 +14,7 @@
 // TB/s; a copy of 1 GiB 5.16).
 #include <hip/hip_runtime.h>
 
-#include "attend_internal.h"
-#include "device_ops.h"
+#include "attend_device.h"
 
 namespace lora {
 namespace {
@@ -83,7 +82,7 @@ __global__ __launch_bounds__(kThreads) void k_rotary(const RotaryArgs a) {
     // the place of the token's key and value; none in a page that is none, or
     // where a replayed graph's sequence has fewer keys than new tokens now
     T *kc = nullptr, *vc = nullptr;
-    if (a.cache.k && tok.pos >= 0) {
+    if (a.cache.k && held(a.dbg, tok) && tok.pos >= 0) {
         const int p = tok.pos / a.cache.page_size, slot = tok.pos % a.cache.page_size;
         const int page = load_invariant(a.pages + int64_t(tok.seq) * a.ld_pages + p);
         if (page >= 0 && page < a.cache.num_pages) {

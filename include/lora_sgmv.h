@@ -837,7 +837,10 @@ lora_status rotary_append(const attn_plan *p, const lora_rotary_desc *r, const v
  * each plan position it indexes a per-row table with, and each adapter group
  * that the product with adapters goes through, lies inside the plan
  * (LORA_DEBUG_ROW; a group's padded rank that is none counts as a block
- * outside the slab).  A failed check sets its bit in a device-wide error word
+ * outside the slab).  Attention and rotary positions check the rows of the batch
+ * (LORA_DEBUG_TOKEN), and the sequence, keys and partial sums (LORA_DEBUG_ROW), of
+ * each part, join and token that they read from their plan; one that is outside is
+ * left out.  A failed check sets its bit in a device-wide error word
  * and switches that access off (the block reads as zeros, the row is taken
  * as absent), so the launch ends normally with a wrong result instead of
  * reading outside the slab or the caller's tensors.  The release build
