@@ -45,6 +45,7 @@ constexpr int kCus = 256, kShortKeys = 1024;
 // One kernel's share of a plan: its tiles of rows, and their keys in parts.
 struct Side {
     int32_t tile_rows = 0, waves = 4;      // rows of a tile; waves of a workgroup (few rows)
+    bool once = true;                      // no sequence has more than one tile (few rows)
     int64_t tiles = 0;                     // tiles of rows, over all key heads
     std::vector<AttnUnit> units;
     std::vector<AttnJoin> joins;
@@ -251,6 +252,7 @@ Batch plan_batch(const lora_attn_desc &d, const int32_t *new_lens, const int32_t
         return n * p->d.kv_heads;
     };
     while (p->rows.tile_rows > 16 && tiles(p->rows.tile_rows) < kCus) p->rows.tile_rows /= 2;
+    p->rows.once = few <= p->rows.tile_rows;
     // A few tiles over short contexts: 8 waves a workgroup and all of a tile's
     // keys, without a launch to join parts (8 key heads, us: one token over 701
     // keys 12.3 against 14.1, 4 over 700 15.2 and 14.2, 16 17.0 and 17.5, 32 over
@@ -677,7 +679,7 @@ lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
         }
         if (e == hipSuccess)
             e = prompt ? lora::launch_attn_prompt(a, s)
-                       : lora::launch_attn_rows(p->d.dtype, side->tile_rows, side->waves, a, s);
+                       : lora::launch_attn_rows(p->d.dtype, side->tile_rows, side->waves, side->once, a, s);
         if (e == hipSuccess) e = lora::launch_attn_join(p->d.dtype, side->tile_rows, a, s);
     }
     if (e != hipSuccess)

@@ -27,10 +27,13 @@
 namespace lora {
 namespace {
 
-template <typename T> constexpr int dtype_of = sizeof(T) == 2 ? LORA_BF16 : LORA_F32;
-
-// NQ tiles of 16 rows, NW waves that take the unit's keys in turn.
-template <typename T, int DP, int NQ, int NW>
+// NQ tiles of 16 rows, NW waves that take the unit's keys in turn.  ONCE: every
+// tile has all of its sequence's rows, so that its keys are read once, past the
+// L2 (128 sequences of 19 to 7824 keys, 730 MB: 123 us against 139; four of 68157
+// to 127138, 1.7 GB: 260 against 298, 6.6 TB/s).  Float32 sequences of several
+// tiles keep them there (300 tokens behind 8000 keys 672 against 706; 64 tokens
+// of 32 heads over one key head, 4000 keys, 92 against 106).
+template <typename T, int DP, int NQ, int NW, bool ONCE>
 __global__ __launch_bounds__(NW * kWaveSize, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void k_attend_rows(const AttnArgs a) {
     static_assert(NW == 4 || NQ == 1, "the join of 16 rows takes 256 threads");
     constexpr int E = Elem<T>::E;                     // elements of 16 bytes
@@ -41,10 +44,7 @@ __global__ __launch_bounds__(NW * kWaveSize, sizeof(T) == 2 && DP <= 128 ? 2 : 1
     constexpr int VC = DP / (16 * VW);                // and its vectors of a key
     constexpr int VD = VW * int(sizeof(T)) / 4;       // words of such a vector
     constexpr int LD = DP + 4;
-    // Tiles that hold all of a sequence's rows read its keys once: past the L2.
-    // (128 sequences of 19 to 7824 keys, 730 MB: 123 us against 139; four of
-    // 68157 to 127138, 1.7 GB: 260 against 298, 6.6 TB/s.)
-    constexpr int POLICY = NQ * 16 < attn_rows_most(dtype_of<T>, DP) || NQ == 1 ? kNT : 0;
+    constexpr int POLICY = ONCE ? kNT : 0;
     __shared__ float so[NW][16][LD];
     __shared__ float sm[NW][16], sl[NW][16];
 
@@ -401,28 +401,36 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a, int tile_
 }
 
 template <typename T, int DP, int NQ, int NW = 4>
-hipError_t rows_launch(const AttnArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((k_attend_rows<T, DP, NQ, NW>), dim3(a.num_units), dim3(NW * kWaveSize), 0, s, a);
+hipError_t rows_launch(bool once, const AttnArgs &a, hipStream_t s) {
+    const dim3 grid(a.num_units), block(NW * kWaveSize);
+    if (once)
+        hipLaunchKernelGGL((k_attend_rows<T, DP, NQ, NW, true>), grid, block, 0, s, a);
+    else if constexpr (sizeof(T) == 4)
+        hipLaunchKernelGGL((k_attend_rows<T, DP, NQ, NW, false>), grid, block, 0, s, a);
+    else
+        return hipErrorInvalidValue;       // (a tile has all of the 16 rows there can be)
     return hipGetLastError();
 }
-template <typename T, int DP> hipError_t rows_dim(int tile_rows, int waves, const AttnArgs &a, hipStream_t s) {
+template <typename T, int DP>
+hipError_t rows_dim(int tile_rows, int waves, bool once, const AttnArgs &a, hipStream_t s) {
     if constexpr (DP <= 128) {
-        if (tile_rows == 16 && waves == kManyWaves) return rows_launch<T, DP, 1, kManyWaves>(a, s);
+        if (tile_rows == 16 && waves == kManyWaves) return rows_launch<T, DP, 1, kManyWaves>(once, a, s);
     }
-    if (tile_rows == 16) return rows_launch<T, DP, 1>(a, s);
+    if (tile_rows == 16) return rows_launch<T, DP, 1>(once, a, s);
     if constexpr (sizeof(T) == 4) {
-        if (tile_rows == 32) return rows_launch<T, DP, 2>(a, s);
+        if (tile_rows == 32) return rows_launch<T, DP, 2>(once, a, s);
     }
     if constexpr (sizeof(T) == 4 && DP <= 128) {
-        if (tile_rows == 64) return rows_launch<T, DP, 4>(a, s);
+        if (tile_rows == 64) return rows_launch<T, DP, 4>(once, a, s);
     }
     return hipErrorInvalidValue;
 }
-template <typename T> hipError_t rows_types(int tile_rows, int waves, const AttnArgs &a, hipStream_t s) {
+template <typename T>
+hipError_t rows_types(int tile_rows, int waves, bool once, const AttnArgs &a, hipStream_t s) {
     switch (attn_dim(a.head_dim)) {
-        case 64: return rows_dim<T, 64>(tile_rows, waves, a, s);
-        case 128: return rows_dim<T, 128>(tile_rows, waves, a, s);
-        default: return rows_dim<T, 256>(tile_rows, waves, a, s);
+        case 64: return rows_dim<T, 64>(tile_rows, waves, once, a, s);
+        case 128: return rows_dim<T, 128>(tile_rows, waves, once, a, s);
+        default: return rows_dim<T, 256>(tile_rows, waves, once, a, s);
     }
 }
 template <typename T, int DP> hipError_t join_launch(int tile_rows, const AttnArgs &a, hipStream_t s) {
@@ -445,10 +453,11 @@ template <typename T> hipError_t join_types(int tile_rows, const AttnArgs &a, hi
 
 }  // namespace
 
-hipError_t launch_attn_rows(int dtype, int tile_rows, int waves, const AttnArgs &a, hipStream_t s) {
+hipError_t launch_attn_rows(int dtype, int tile_rows, int waves, bool once, const AttnArgs &a,
+                            hipStream_t s) {
     if (a.num_units <= 0) return hipSuccess;
-    return dtype == LORA_F32 ? rows_types<float>(tile_rows, waves, a, s)
-                             : rows_types<uint16_t>(tile_rows, waves, a, s);
+    return dtype == LORA_F32 ? rows_types<float>(tile_rows, waves, once, a, s)
+                             : rows_types<uint16_t>(tile_rows, waves, once, a, s);
 }
 
 hipError_t launch_attn_join(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s) {

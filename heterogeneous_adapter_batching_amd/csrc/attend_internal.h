@@ -115,7 +115,9 @@ constexpr int attn_rows_most(int dtype, int head_dim) {
 }
 // Waves of a workgroup of tiles of 16 rows: 4, or (heads of up to 128) 8.
 constexpr int kManyWaves = 8;
-hipError_t launch_attn_rows(int dtype, int tile_rows, int waves, const AttnArgs &a, hipStream_t s);
+// once: no sequence has more than one tile of rows
+hipError_t launch_attn_rows(int dtype, int tile_rows, int waves, bool once, const AttnArgs &a,
+                            hipStream_t s);
 constexpr int kPromptRows = 128; // of a tile of prompts
 hipError_t launch_attn_prompt(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_join(int dtype, int tile_rows, const AttnArgs &a, hipStream_t s);

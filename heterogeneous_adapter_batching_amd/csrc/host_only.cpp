@@ -34,7 +34,7 @@ hipError_t launch_operand(int, const OperandArgs &, hipStream_t) { return hipErr
 hipError_t launch_linear(int, const LinearPlan &, bool, LinearArgs, hipStream_t) {
     return hipErrorInvalidValue;
 }
-hipError_t launch_attn_rows(int, int, int, const AttnArgs &, hipStream_t) {
+hipError_t launch_attn_rows(int, int, int, bool, const AttnArgs &, hipStream_t) {
     return hipErrorInvalidValue;
 }
 hipError_t launch_attn_prompt(const AttnArgs &, hipStream_t) { return hipErrorInvalidValue; }
