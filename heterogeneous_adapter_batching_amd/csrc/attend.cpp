@@ -34,10 +34,11 @@ constexpr int32_t kMostTokens = 1 << 23, kMostKeys = 1 << 30;
 constexpr int64_t kMostStride = int64_t(1) << 36, kMostCache = int64_t(1) << 40;
 
 // Units a launch aims for when it cuts the tiles' keys into parts, and the
-// fewest keys of a part.  The kernel for few rows has two workgroups a CU, the
-// prompts' too: a round, or two of them (four sequences behind 68157 to 127138
-// keys, us: 512 parts 383, 768 324, 1024 299, 1536 324, 2048 302; 128 sequences
-// of 19 to 7824 keys 144, 137, 141, 140, 141).
+// fewest keys of a part.  With heads of 128 the kernel for few rows has two
+// workgroups a CU, the prompts' too: a round, or two of them (four sequences
+// behind 68157 to 127138 keys, us: 512 parts 383, 768 324, 1024 299, 1536 324,
+// 2048 302; 128 sequences of 19 to 7824 keys 144, 137, 141, 140, 141).  Heads of
+// 64 and 256, four workgroups and one a CU, take the same numbers.
 constexpr int kRowsUnits = 1024, kRowsKeys = 256;
 constexpr int kPromptUnits = 512, kPromptKeys = 512;
 constexpr int kCus = 256, kShortKeys = 1024;
@@ -254,9 +255,17 @@ Batch plan_batch(const lora_attn_desc &d, const int32_t *new_lens, const int32_t
     while (p->rows.tile_rows > 16 && tiles(p->rows.tile_rows) < kCus) p->rows.tile_rows /= 2;
     p->rows.once = few <= p->rows.tile_rows;
     // A few tiles over short contexts: 8 waves a workgroup and all of a tile's
-    // keys, without a launch to join parts (8 key heads, us: one token over 701
-    // keys 12.3 against 14.1, 4 over 700 15.2 and 14.2, 16 17.0 and 17.5, 32 over
-    // 950 24.5 and 29.5).
+    // keys, without a launch to join parts.  8 waves against 4, replayed, heads of
+    // 128, us:
+    //   tiles   320 keys     512          701          1000
+    //       8   7.8  10.1    10.0 10.6    12.4 10.8    16.3 11.0
+    //     128  10.3  12.3    13.9 13.7    17.5 17.0    22.3 18.4
+    //     160  10.9  12.8    14.2 16.6    18.4 17.6    22.8 22.6
+    //     192  10.9  13.7    14.3 17.2    17.8 21.7    22.4 25.1
+    //     256  11.3  15.5    15.2 19.4    19.2 23.5    24.6 30.4
+    // So up to 512 keys, or 1024 where 4 waves' parts would be more than a round
+    // of workgroups; 1 and 2 key heads balance alike, heads of 64 a little later
+    // and float32 a little earlier (at most 9% from the better of the two).
     int64_t longest = p->d.max_kv;
     if (!longest)
         each_seq(*p, false, [&](int32_t s, int32_t, int64_t rows) {
@@ -264,8 +273,9 @@ Batch plan_batch(const lora_attn_desc &d, const int32_t *new_lens, const int32_t
             tile_keys(*p, s, 0, rows, &lo, &hi);
             longest = std::max<int64_t>(longest, hi - lo);
         });
+    const int64_t few_tiles = tiles(16);
     p->rows.waves = p->rows.tile_rows == 16 && lora::attn_dim(p->d.head_dim) <= 128 &&
-                            tiles(16) <= kCus && longest <= kShortKeys
+                            few_tiles <= kCus && longest <= (few_tiles > 160 ? kShortKeys : kShortKeys / 2)
                         ? lora::kManyWaves
                         : 4;
     cut(*p, &p->rows, false, kRowsUnits, p->rows.waves == 4 ? kRowsKeys : kShortKeys);
@@ -303,7 +313,7 @@ struct Rows {
     int64_t ld, width;
 };
 // A matrix of whole 16-byte vectors.
-lora_status check_rows(const Rows &r, int32_t es) {
+lora_status check_rows(const Rows &r) {
     if (!r.ptr || !aligned(r.ptr, 16))
         return set_errorf(LORA_EINVAL, "%s must be non-null and 16-byte aligned", r.name);
     if (r.ld < r.width || r.ld % 8 || r.ld > kMostStride)
@@ -641,7 +651,7 @@ lora_status paged_attention(const attn_plan *p, const void *q, int64_t ldq,
     const int32_t es = esize(p->d.dtype);
     const Rows rq{"q", q, ldq, width}, ro{"o", o, ldo, width};
     for (const Rows *r : {&rq, &ro})
-        if ((st = check_rows(*r, es)) != LORA_OK) return st;
+        if ((st = check_rows(*r)) != LORA_OK) return st;
     if (overlap(rq, ro, T, es)) return set_errorf(LORA_EINVAL, "o overlaps q");
     if ((st = check_cache(*p, cache, pages, ld_pages, pages_per_seq, false, {ro})) != LORA_OK)
         return st;
@@ -745,7 +755,7 @@ lora_status rotary_append(const attn_plan *p, const lora_rotary_desc *r, const v
         rv{"v", v, ldv, wk};
     if (q) {
         for (const Rows *x : {&rq, &ro})
-            if ((st = check_rows(*x, es)) != LORA_OK) return st;
+            if ((st = check_rows(*x)) != LORA_OK) return st;
         if (overlap(rq, ro, T, es) && !(q == q_out && (ldq == ldqo || T == 1)))
             return set_errorf(LORA_EINVAL, "q_out overlaps q without being it");
     } else if (q_out) {
@@ -753,7 +763,7 @@ lora_status rotary_append(const attn_plan *p, const lora_rotary_desc *r, const v
     }
     if (cache) {
         for (const Rows *x : {&rk, &rv}) {
-            if ((st = check_rows(*x, es)) != LORA_OK) return st;
+            if ((st = check_rows(*x)) != LORA_OK) return st;
             if (q && overlap(ro, *x, T, es)) return set_errorf(LORA_EINVAL, "q_out overlaps %s", x->name);
         }
         if ((st = check_cache(*p, cache, pages, ld_pages, pages_per_seq, true, {rq, ro, rk, rv})) !=

@@ -15,7 +15,7 @@
 // the lane's own.  V^T takes a lane's 8 keys of one element: it loads 8
 // elements of each and exchanges halves of words among its own registers.
 // bfloat16 weights enter as two values, the rounded one and the remainder
-// (2^-17 of the weight is lost), which costs nothing here.  128 sequences of 19
+// (at most 2^-16 of the weight is lost), which costs nothing here.  128 sequences of 19
 // to 7824 keys, one token each, 32 heads over 8 of 128: 730 MB in 119 to 122 us
 // with the join (6.0 TB/s); four of 68157 to 127138 1.7 GB in 260 (6.5); 64 over
 // 1500 states of an encoder, 16 heads of 64, 393 MB in 65 (6.0; a copy of 1 GiB
