@@ -24,6 +24,6 @@ def test_parts_of_short_contexts(tokens, kv_heads, whole, parts, dim, dtype):
 
 def test_other_plans():
     # more tiles than workgroups of 8 waves; heads of 256; room for longer contexts
-    assert stats(33, 300)["joins"] == 0 and stats(33, 1024)["joins"] == 264
+    assert stats(33, 256)["joins"] == 0 and stats(33, 300)["joins"] == 264
     assert stats(1, 500, dim=256)["joins"] == 8
     assert stats(1, 400, max_kv=512)["joins"] == 0 and stats(1, 400, max_kv=8192)["joins"] == 8
