@@ -152,6 +152,14 @@ def _device(plan, t):
     return t.device
 
 
+def _call(fn, plan, args, device, stream):
+    """A call on `stream` keeps the plan's workspace until it is done (what the
+    caller holds, and the current stream's order, the caller sees to)."""
+    _enqueue(fn, (plan.handle, *args), device, stream)
+    if stream is not None and plan.ws is not None:
+        plan.ws.record_stream(stream)
+
+
 def _heads(t, name, plan, width, device):
     """A matrix of the plan's tokens (and rows past them): pointer, stride."""
     if not isinstance(t, _Tensor) or t.get_device() != device.index or t.dtype != plan.dtype:
@@ -251,9 +259,8 @@ def paged_attention(plan, q, k_cache, v_cache, pages, *, scale=None, o=None, str
     if o is None:
         o = _padded(q, plan, device, stream)
     op, ldo = _heads(o, "o", plan, plan.q_width, device)
-    _enqueue(plan.lib.paged_attention,
-             (plan.handle, qp, ldq, *_cache(plan, k_cache, v_cache, pages, device), scale, op, ldo),
-             device, stream)
+    _call(plan.lib.paged_attention, plan,
+          (qp, ldq, *_cache(plan, k_cache, v_cache, pages, device), scale, op, ldo), device, stream)
     return o
 
 
@@ -298,6 +305,6 @@ def rotary_append(plan, q, k, v, k_cache, v_cache, pages, freqs, *, layout="half
     if freqs is not None:
         fp, n = _vector(freqs, "freqs", torch.float64, 1, device)
     desc = _rotary_desc(2 * n, layout, float(magnitude))
-    _enqueue(plan.lib.rotary_append,
-             (plan.handle, desc, qp, ldq, op, ldo, kp, ldk, vp, ldv, *cache, pp, fp), device, stream)
+    _call(plan.lib.rotary_append, plan, (desc, qp, ldq, op, ldo, kp, ldk, vp, ldv, *cache, pp, fp),
+          device, stream)
     return q_out

@@ -1,0 +1,42 @@
+"""A plan's workspace and staging outlive the work that reads them."""
+import pytest
+import torch
+
+import heterogeneous_adapter_batching_amd as hab
+from attention_reference import Batch
+from test_gpu_attention import plan_of, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("call", ["attention", "rotary"])
+def test_a_workspace_replaced_behind_a_call_on_another_stream(call):
+    """Its memory is not given out while the call is queued.  (A plan that is
+    destroyed waits.)"""
+    b = Batch([1] * 4, [300, 20, 4000, 9], seed=1, page=64)
+    want = run(b)
+    side = torch.cuda.Stream()
+    plan = plan_of(b).upload().upload()          # (both staging buffers are there)
+    at, size = plan.ws.data_ptr(), plan.ws.nbytes
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(int(4e8))              # (a fifth of a second)
+    if call == "attention":
+        o = hab.paged_attention(plan, b.q, b.k, b.v, b.pages, stream=side)
+    else:
+        f = hab.rotary_frequencies(64, device="cuda")
+        o = hab.rotary_append(plan, b.q, None, None, None, None, None, f, stream=side)
+    plan.upload()
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert not side.query(), "the queue ran empty before the memory was asked for"
+    # (only asked for, never written: where it is the plan's, the call has lost it)
+    assert all(t.data_ptr() + size <= at or at + size <= t.data_ptr() for t in others)
+    torch.cuda.synchronize()
+    if call == "attention":
+        assert torch.equal(o, want)
+
+
+def test_nothing_to_keep():
+    """A plan of no tokens, never uploaded, on a stream."""
+    b = Batch([0, 0], [5, 0])
+    assert hab.paged_attention(plan_of(b), b.q, b.k, b.v, b.pages, stream=torch.cuda.Stream()).shape == (0, 512)
