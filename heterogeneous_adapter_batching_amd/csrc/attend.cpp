@@ -594,9 +594,14 @@ lora_status attn_plan_upload(attn_plan *p, void *ws, uint64_t ws_bytes, void *st
         return set_errorf(LORA_ESTATE, "workspace of %llu bytes < %llu needed",
                           (unsigned long long)ws_bytes,
                           (unsigned long long)attn_plan_workspace_bytes(p));
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    hipError_t e = hipStreamIsCapturing(static_cast<hipStream_t>(stream), &capture);
+    if (e != hipSuccess) return set_errorf(LORA_EHIP, "plan upload: %s", hipGetErrorString(e));
+    if (capture != hipStreamCaptureStatusNone)
+        return set_errorf(LORA_ESTATE, "an upload cannot be captured: later ones write its staging again");
     return guarded([&] {
         const int32_t k = p->next_staging;
-        hipError_t e = p->staged[k] ? hipEventSynchronize(p->staged[k])
+        e = p->staged[k] ? hipEventSynchronize(p->staged[k])
                                     : hipEventCreateWithFlags(&p->staged[k], hipEventDisableTiming);
         if (e != hipSuccess)
             return set_errorf(LORA_EHIP, "plan staging event: %s", hipGetErrorString(e));

@@ -725,9 +725,10 @@ typedef struct {
  * attn_plan_rebuild re-plans in place (an error leaves the plan as it was);
  * attn_plan_upload copies the tables into `ws` (256-byte aligned,
  * attn_plan_workspace_bytes) on `stream`, from one of two pinned buffers in
- * turn.  A call with a plan that was rebuilt since, or that another plan, of
- * either kind, has been uploaded over in part or whole, is refused
- * (LORA_ESTATE); so is one whose tensors reach into the workspace (LORA_EINVAL).
+ * turn, and not into a captured graph (LORA_ESTATE).  A call with a plan that was
+ * rebuilt since, or that another plan, of either kind, has been uploaded over in
+ * part or whole, is refused (LORA_ESTATE); so is one whose tensors reach into the
+ * workspace (LORA_EINVAL).
  * A captured graph keeps the launches it was captured with.  With max_kv they
  * depend on new_lens (and max_kv) alone: such a graph may be replayed after a
  * rebuild with the same new_lens and an upload into the same workspace.

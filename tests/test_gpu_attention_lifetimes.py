@@ -40,3 +40,25 @@ def test_nothing_to_keep():
     """A plan of no tokens, never uploaded, on a stream."""
     b = Batch([0, 0], [5, 0])
     assert hab.paged_attention(plan_of(b), b.q, b.k, b.v, b.pages, stream=torch.cuda.Stream()).shape == (0, 512)
+
+
+def test_an_upload_is_not_captured():
+    """A graph would copy out of staging that later uploads have written again:
+    refused, with the capture and the plan as they were."""
+    b = Batch([1, 40], [300, 90], seed=2)
+    want = run(b)
+    plan = plan_of(b).upload().upload()
+    o = torch.empty_like(b.q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(hab.LoraError, match="captured"):
+            plan.upload(ws=plan.ws)
+        hab.paged_attention(plan, b.q, b.k, b.v, b.pages, o=o)
+    for _ in range(3):
+        o.zero_()
+        plan.rebuild(b.new, b.kv).upload(ws=plan.ws)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+        assert torch.equal(hab.paged_attention(plan, b.q, b.k, b.v, b.pages), want)
