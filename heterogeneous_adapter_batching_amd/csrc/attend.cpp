@@ -52,6 +52,15 @@ struct Side {
     std::vector<AttnJoin> joins;
     int64_t cap_units = 0, cap_joins = 0, cap_slots = 0;   // places in the workspace
     uint64_t off_units = 0, off_joins = 0, off_partial = 0, off_lse = 0;
+
+    void clear() {
+        Side empty;
+        empty.units.swap(units);
+        empty.joins.swap(joins);
+        empty.units.clear();
+        empty.joins.clear();
+        *this = std::move(empty);
+    }
 };
 
 // What a plan holds of its batch: built as a whole, so that a rebuild that fails
@@ -69,6 +78,7 @@ struct Batch {
 }  // namespace
 
 struct attn_plan : Batch {
+    Batch spare;                           // where a rebuild builds; the two change places
     void *ws = nullptr;
     // pinned staging, two buffers in turn: an upload waits only for the copy
     // before last
@@ -167,9 +177,6 @@ template <typename Fn> void each_seq(const Batch &p, bool prompt, Fn fn) {
 // units, none shorter than `least` keys, and lays them out one after another.
 // The cut is even: no more parts than tiles + target in all.
 void cut(const Batch &p, Side *side, bool prompt, int64_t target, int64_t least) {
-    side->units.clear();
-    side->joins.clear();
-    side->tiles = 0;
     int64_t total = 0, longest = 0;
     each_seq(p, prompt, [&](int32_t s, int32_t, int64_t rows) {
         for (int64_t r = 0; r < rows; r += side->tile_rows) {
@@ -231,10 +238,15 @@ void cut(const Batch &p, Side *side, bool prompt, int64_t target, int64_t least)
     }
 }
 
-Batch plan_batch(const lora_attn_desc &d, const int32_t *new_lens, const int32_t *kv_lens, int32_t S) {
-    Batch batch, *const p = &batch;
+// (in the memory that `p` has, whatever it held)
+void plan_batch(Batch *p, const lora_attn_desc &d, const int32_t *new_lens, const int32_t *kv_lens,
+                int32_t S) {
     p->d = d;
     p->group = d.heads / d.kv_heads;
+    p->tokens.clear();
+    p->most_kv = 0;
+    p->rows.clear();
+    p->prompt.clear();
     p->new_lens.assign(new_lens, new_lens + S);
     p->kv_lens.assign(kv_lens, kv_lens + S);
     for (int32_t s = 0; s < S; ++s) {
@@ -300,7 +312,6 @@ Batch plan_batch(const lora_attn_desc &d, const int32_t *new_lens, const int32_t
         side->off_lse = place(rows * 4);
     }
     p->ws_bytes = at;
-    return batch;
 }
 
 bool aligned(const void *ptr, int64_t bytes) {
@@ -539,7 +550,7 @@ lora_status attn_plan_create(attn_plan **out, const lora_attn_desc *d, const int
     if ((st = check_lens(*d, new_lens, kv_lens, num_seqs)) != LORA_OK) return st;
     return guarded([&] {
         std::unique_ptr<attn_plan> p(new attn_plan());
-        static_cast<Batch &>(*p) = plan_batch(*d, new_lens, kv_lens, num_seqs);
+        plan_batch(p.get(), *d, new_lens, kv_lens, num_seqs);
         *out = p.release();
         return LORA_OK;
     });
@@ -551,7 +562,8 @@ lora_status attn_plan_rebuild(attn_plan *p, const int32_t *new_lens, const int32
     const lora_status st = check_lens(p->d, new_lens, kv_lens, num_seqs);
     if (st != LORA_OK) return st;
     return guarded([&] {
-        static_cast<Batch &>(*p) = plan_batch(p->d, new_lens, kv_lens, num_seqs);
+        plan_batch(&p->spare, p->d, new_lens, kv_lens, num_seqs);
+        std::swap(static_cast<Batch &>(*p), p->spare);
         p->ws = nullptr;                   // its tables are the last batch's
         return LORA_OK;
     });
