@@ -41,7 +41,9 @@ class AttentionPlan:
     encoder's states; new_lens and kv_lens are then independent).  max_kv: the
     most keys of any later rebuild, so that a captured graph may be replayed
     after rebuild(the same new_lens, other kv_lens).upload(the same ws); the
-    page table then has room for max_kv keys."""
+    page table then has room for max_kv keys.  A rebuild that fails leaves the
+    plan as it was.  A workspace that any other plan, an adapter plan too, has
+    been uploaded over is refused until this one is uploaded again."""
 
     def __init__(self, heads, kv_heads, head_dim, page_size, new_lens, kv_lens, *, dtype="bf16",
                  causal=True, window=0, max_kv=0):
@@ -98,7 +100,8 @@ class AttentionPlan:
 
     def upload(self, ws=None, stream=None, device="cuda"):
         """Copy the plan into a device workspace (made on `device` unless
-        given, from the memory of the stream that the copy is queued on)."""
+        given, from the memory of the stream that the copy is queued on).  Not
+        while the stream is being captured."""
         if ws is None:
             device = torch.device(device) if stream is None else stream.device
             if device.index is None:
@@ -244,7 +247,7 @@ def paged_attention(plan, q, k_cache, v_cache, pages, *, scale=None, o=None, str
         o = softmax(scale q . k) v
 
     for every query head, over the keys that the plan lets the token see; zeros
-    where there are none.  q and o are [tokens][heads * head_dim] (q may be a
+    where there are none, NaN where all of them score -inf.  q and o are [tokens][heads * head_dim] (q may be a
     slice of the q/k/v product; rows past the plan's tokens are not looked at
     and stay as they are, or are zeros in a new o), k_cache and v_cache
     [pages][kv_heads][page_size][head_dim] with contiguous elements and any
@@ -278,7 +281,8 @@ def rotary_append(plan, q, k, v, k_cache, v_cache, pages, freqs, *, layout="half
     in the cache.  freqs: float64 on the device (rotary_frequencies), or None
     to append alone.  positions: int32 [tokens], or None for the tokens' places
     among their keys.  q may be None (an encoder's keys and values), or k, v,
-    both caches and pages together (queries alone).  Other arguments as
+    both caches and pages together (queries alone).  A cache in which two
+    places have elements in common is refused.  Other arguments as
     paged_attention."""
     if q is None and k is None:
         raise ValueError("neither q nor k")

@@ -22,7 +22,7 @@
 //
 // What bounds it: the matrix cores, busy half of the cycles at the 1.85 GHz that
 // the chip's power leaves them.  Four prompts of 4096 tokens, 32 heads over 8
-// of 128: 548 to 570 us (965 to 1003 TFLOP/s of what is seen; 16384 tokens 1130;
+// of 128: 546 to 568 us (968 to 1006 TFLOP/s of what is seen; 16384 tokens 1130;
 // the large product of linear.hip 1320 to 1350).  An eighth of it is the copies
 // (the same without them: 486 us), a tenth the weights; LDS has no conflicts.
 // Tried and left: two tiles of 32 rows a wave, which halve the reads of LDS, at
