@@ -174,8 +174,9 @@ template <typename Fn> void each_seq(const Batch &p, bool prompt, Fn fn) {
 }
 
 // Cuts every tile's keys into parts, so that the launch has about `target`
-// units, none shorter than `least` keys, and lays them out one after another.
-// The cut is even: no more parts than tiles + target in all.
+// units, and lays them out one after another.  A tile of up to `least` keys is
+// not cut; the cut is even, so that its parts may be half as long, and there are
+// no more of them than tiles + target in all.
 void cut(const Batch &p, Side *side, bool prompt, int64_t target, int64_t least) {
     int64_t total = 0, longest = 0;
     each_seq(p, prompt, [&](int32_t s, int32_t, int64_t rows) {
